@@ -72,7 +72,17 @@ typedef enum {
  *                 the fp16 whose high byte is the stored byte and whose low byte is zero,
  *                 no scale (ElasticKV Sec. 3.2 and App. B.3: "shift-and-bitcast"). The low
  *                 bytes, kept by the caller, restore TARGET exactly (ekv_promote_pages). */
-typedef enum { EKV_MODE_TARGET_FP16 = 0, EKV_MODE_COMPACT_E4M3 = 1, EKV_MODE_BASE = 2 } ekv_page_mode;
+typedef enum { EKV_MODE_TARGET_FP16 = 0, EKV_MODE_COMPACT_E4M3 = 1, EKV_MODE_BASE = 2,
+/*  MICRO_FP4:     microscaled FP4: the page's first 17*H_kv*D/2 bytes hold, KV head after KV
+ *                 head, the head's 16 rows of E2M1 codes ([16][D/2] bytes, element 2i in the low
+ *                 and 2i+1 in the high half of byte i), then its 16 rows of scale bytes
+ *                 ([16][D/32], E8M0: scale = 2^(byte - 127)); value = E2M1(code) * scale, one scale per
+ *                 32 values of a token's head row. Scale bytes run from 103 to 140 (2^-24 .. 2^13),
+ *                 so that every value is an fp16 value; any other byte is a data error
+ *                 (EKV_DETAIL_SCALE) and its 32 values read as zero. Pages of this form are written by
+ *                 ekv_demote_pages_micro and ekv_append_kv_rope, read by ekv_extend_attention and
+ *                 ekv_expand_pages_micro; every other call reports EKV_DETAIL_PAGE_MODE for them. */
+               EKV_MODE_MICRO_FP4 = 3 } ekv_page_mode;
 
 /* Granularity of the compact-page value scales (fp32, device memory).
  * PER_TENSOR: v_scales[0] applies to every compact page (a per-layer scale is one
@@ -87,7 +97,7 @@ typedef enum {
   EKV_DETAIL_SEQ_LEN = 3,        /* seq_lens[b] < 0 or > block_table_stride * 16 */
   EKV_DETAIL_NONFINITE_PAGE = 4, /* a page given to demotion holds NaN or inf */
   EKV_DETAIL_TIMEOUT = 5,        /* a bounded pipeline wait gave up */
-  EKV_DETAIL_PAGE_MODE = 6       /* a page_mode byte is not TARGET, COMPACT or BASE */
+  EKV_DETAIL_PAGE_MODE = 6       /* a page_mode byte is not one of the modes the call reads */
 } ekv_detail;
 
 typedef struct ekv_ctx ekv_ctx;
@@ -316,6 +326,92 @@ ekv_status ekv_append_kv(ekv_ctx* ctx, const void* k_new, const void* v_new, voi
                          const float* v_scales, int scale_mode, const uint8_t* page_mode,
                          int uniform_mode, const int32_t* block_table, int block_table_stride,
                          const int32_t* positions, int batch, void* stream);
+
+/* Rotary cache writer for ragged batches: the new tokens of every sequence, one (a decode
+ * step) or many (a prompt chunk), with the position rotation applied on the way. Sequence b
+ * has n_b = cu_q[b+1] - cu_q[b] new tokens, the last of its seq_lens[b] tokens; its r-th is
+ * row i = cu_q[b] + r of q, k_new and v_new and stands at position t = seq_lens[b] - n_b + r:
+ *   q_out[i] = R(t) q[i];  K row t % 16 of page p = block_table[b][t / 16] = R(t) k_new[i];
+ *   V row: v_new[i] in the page's form, as ekv_append_kv stores it; a MICRO_FP4 page's row gets
+ *   scales of its own, per 32 values 2^k with the least k in [-24, 13] for which 6 * 2^k
+ *   reaches the largest magnitude, and E2M1 codes rounded to nearest-even, saturating (NaN
+ *   has no code: it is stored as +6 times the scale).
+ * R(t) turns the pairs (x_i, x_j) of a head's first rope_dim values by the angle whose cosine and
+ * sine the table holds: (x_i c - x_j s, x_j c + x_i s) in fp32, rounded once to fp16; the rest
+ * of the head is copied.
+ *  q, k_new, v_new  fp16 rows of [H_q][D], [H_kv][D], [H_kv][D]; q_stride, k_stride, v_stride:
+ *                   values between the rows of consecutive tokens (a multiple of 8, at least the
+ *                   row), so that all three may be slices of one projection's output. q may be NULL
+ *                   (then q_out is not written). 16-byte aligned.
+ *  rope_table       fp32 [rope_len][rope_dim]: cosines of the rope_dim / 2 angles of a position, then
+ *                   their sines; 16-byte aligned. A position >= rope_len is reported
+ *                   (EKV_DETAIL_SEQ_LEN) and its token not written. NULL only if rope_dim == 0.
+ *  rope_dim         0 (no rotation) .. D, a multiple of 16.
+ *  rope_style       0: pairs (i, i + rope_dim / 2); 1: pairs (2i, 2i + 1).
+ *  q_out            fp16 [total_q][H_q][D], contiguous; may be q itself when q is contiguous.
+ *  seq_lens         int32 [batch]: tokens of each sequence with the new ones; cu_q int32 [batch + 1],
+ *                   nondecreasing from 0; total_q: rows of q (host). Rows >= cu_q[batch] are neither
+ *                   read nor written.
+ * Device checks (reported; nothing is written): n_b < 0 or > seq_lens[b], seq_lens[b] >
+ * block_table_stride * 16 (EKV_DETAIL_SEQ_LEN, the whole sequence); a page id outside the
+ * pool, a mode byte > 3 (the token's K and V rows); a scale that is not positive finite
+ * (that head's V row keeps its old bytes). No two tokens of a call may share a row of a
+ * page. Other arguments as for ekv_paged_decode; batch is not bound by max_batch. */
+ekv_status ekv_append_kv_rope(ekv_ctx* ctx, const void* q, const void* k_new, const void* v_new,
+                              long long q_stride, long long k_stride, long long v_stride,
+                              const float* rope_table, int rope_len, int rope_dim, int rope_style,
+                              void* q_out, void* k_pages, void* v_pages,
+                              long long v_page_stride_bytes, int num_pages, const float* v_scales,
+                              int scale_mode, const uint8_t* page_mode, int uniform_mode,
+                              const int32_t* block_table, int block_table_stride,
+                              const int32_t* seq_lens, const int32_t* cu_q, int batch, int total_q,
+                              void* stream);
+
+/* Attention of new tokens over the paged cache: for a decode step, for the verification of
+ * draft tokens, for a prompt chunk behind a cached prefix, and for ragged mixes of them. With b, r, i
+ * and t as for ekv_append_kv_rope (which writes the new tokens' rows beforehand), query head h_q
+ * of KV head h = h_q / G:
+ *   out[i][h_q] = sum_k softmax_k(sm_scale * q[i][h_q] . K_k) V_k,
+ *   lse[i][h_q] = log sum_k exp(sm_scale * q[i][h_q] . K_k)
+ * over the keys max(0, t - window + 1) <= k <= t of sequence b (window 0: all k <= t). Pages
+ * may hold values in any of the four forms. Keys outside that range are not used, whatever
+ * their rows hold (NaN included).
+ *  q, out       fp16 [total_q][H_q][D], contiguous, 16-byte aligned; must not overlap.
+ *  seq_lens, cu_q, total_q  as for ekv_append_kv_rope; rows >= cu_q[batch] are left as they are.
+ *  max_q        host int, at least every n_b: chooses the kernel. A longer sequence is
+ *               reported (EKV_DETAIL_SEQ_LEN), as is one that the writer would report: its out
+ *               is zeroed and its lse -inf.
+ *  window       keys a query sees, its own among them; 0: no window.
+ *  lse          fp32 [total_q][H_q], natural logarithm, or NULL.
+ * A page that fails its check (id, mode byte > 3, scale) zeroes out and sets lse = -inf for the
+ * queries that see one of its keys (of one KV head for a bad per-(page, head) scale). Returns
+ * EKV_ERR_CAPACITY when batch > cfg.max_batch. Other arguments as for ekv_paged_decode; sums are
+ * fp32, the weights enter the product with V rounded to fp16. */
+ekv_status ekv_extend_attention(ekv_ctx* ctx, const void* q, const void* k_pages, const void* v_pages,
+                                long long v_page_stride_bytes, int num_pages, const float* v_scales,
+                                int scale_mode, const uint8_t* page_mode, int uniform_mode,
+                                const int32_t* block_table, int block_table_stride,
+                                const int32_t* seq_lens, const int32_t* cu_q, int batch, int total_q,
+                                int max_q, int window, float sm_scale, void* out, float* lse,
+                                void* stream);
+
+/* TARGET -> MICRO_FP4 demotion, in place: for each page p = page_ids[i] whose page_mode[p] is
+ * TARGET, every 32 values of a token's head row get the scale 2^k with the least k in [-24, 13]
+ * for which 6 * 2^k >= their largest magnitude, and E2M1 codes of value / 2^k, rounded to
+ * nearest-even and saturating at 6; they fill the first 17*H_kv*D/2 bytes of the page's slot,
+ * then page_mode[p] = MICRO_FP4. Pages that are not TARGET are skipped; a page holding NaN or
+ * inf is left TARGET and reported (EKV_DETAIL_NONFINITE_PAGE). Arguments as for ekv_demote_pages. */
+ekv_status ekv_demote_pages_micro(ekv_ctx* ctx, void* v_pages, long long v_page_stride_bytes,
+                                  int num_pages, const int32_t* page_ids, int n,
+                                  uint8_t* page_mode, void* stream);
+
+/* MICRO_FP4 -> TARGET, in place: the values that the codes of page p = page_ids[i] stand for, as fp16
+ * (exact), then page_mode[p] = TARGET: hands a page to the calls that do not read MICRO_FP4. Pages
+ * that are not MICRO_FP4 are skipped. Demoting the page again gives the same values. Arguments
+ * as for ekv_demote_pages_micro. */
+ekv_status ekv_expand_pages_micro(ekv_ctx* ctx, void* v_pages, long long v_page_stride_bytes,
+                                  int num_pages, const int32_t* page_ids, int n,
+                                  uint8_t* page_mode, void* stream);
 
 /* Paged decode that allocates nothing, for callers that must not call cudaMalloc on
  * this path (a runtime whose pool owns all device memory, an enqueue hook of a host

@@ -10,7 +10,9 @@
 #include <vector>
 
 #include "decode.cuh"
+#include "extend.cuh"
 #include "gather_demote.cuh"
+#include "micro.cuh"
 #include "pool_maps.h"
 #include "prefill.cuh"
 
@@ -439,7 +441,7 @@ ekv_status transition(ekv_ctx* c, int op, void* v_pages, long long v_page_stride
   if (n == 0) return EKV_OK;
   const int Hkv = c->cfg.num_kv_heads, D = c->cfg.head_dim;
   if (!v_pages || !page_ids || !page_mode || num_pages < 1 || num_slots < 1) return EKV_ERR_INVALID_ARG;
-  if (op < kToE4M3 || op > kPromote) return EKV_ERR_INVALID_ARG;
+  if (op < kToE4M3 || op > kFromMicro) return EKV_ERR_INVALID_ARG;
   if (op == kToE4M3 && !scale_out) return EKV_ERR_INVALID_ARG;
   if (op == kPromote && !low) return EKV_ERR_INVALID_ARG;
   if (low && !aligned16(low)) return EKV_ERR_INVALID_ARG;
@@ -491,10 +493,23 @@ ekv_status ekv_promote_pages(ekv_ctx* c, void* v_pages, long long v_page_stride_
                     n, page_mode, nullptr, static_cast<uint8_t*>(const_cast<void*>(low_in)), stream);
 }
 
+ekv_status ekv_demote_pages_micro(ekv_ctx* c, void* v_pages, long long v_page_stride_bytes, int num_pages,
+                                  const int32_t* page_ids, int n, uint8_t* page_mode, void* stream) {
+  return transition(c, kToMicro, v_pages, v_page_stride_bytes, num_pages, num_pages, page_ids, nullptr, nullptr,
+                    n, page_mode, nullptr, nullptr, stream);
+}
+
+ekv_status ekv_expand_pages_micro(ekv_ctx* c, void* v_pages, long long v_page_stride_bytes, int num_pages,
+                                  const int32_t* page_ids, int n, uint8_t* page_mode, void* stream) {
+  return transition(c, kFromMicro, v_pages, v_page_stride_bytes, num_pages, num_pages, page_ids, nullptr, nullptr,
+                    n, page_mode, nullptr, nullptr, stream);
+}
+
 ekv_status ekv_transition_pages(ekv_ctx* c, int op, void* v_pages, long long v_page_stride_bytes, int num_slots,
                                 int num_pages, const int32_t* page_ids, const int32_t* src_loc,
                                 const int32_t* dst_loc, int n, uint8_t* page_mode, float* scale_out, void* low,
                                 void* stream) {
+  if (op > kPromote) op = -1;                       // the microscaled forms have no half-slot locations
   return transition(c, op, v_pages, v_page_stride_bytes, num_pages, num_slots, page_ids, src_loc, dst_loc, n,
                     page_mode, scale_out, static_cast<uint8_t*>(low), stream);
 }
@@ -539,6 +554,125 @@ ekv_status ekv_append_kv(ekv_ctx* c, const void* k_new, const void* v_new, void*
   p.err = c->err;
   if (launch_append(p, batch, st) != cudaSuccess) return EKV_ERR_CUDA;
   note_launch(st, kAfterAppend);
+  return EKV_OK;
+}
+
+namespace {
+
+// Checks and view of the cache for the calls that take new tokens.
+ekv_status cache_view(ekv_ctx* c, CacheView* v, const void* k_pages, const void* v_pages,
+                      long long v_page_stride_bytes, int num_pages, const float* v_scales, int scale_mode,
+                      const uint8_t* page_mode, int uniform_mode, const int32_t* block_table,
+                      int block_table_stride, const int32_t* seq_lens, const int32_t* cu_q, int batch,
+                      int total_q) {
+  const int Hkv = c->cfg.num_kv_heads, D = c->cfg.head_dim;
+  if (!k_pages || !v_pages || !block_table || !seq_lens || !cu_q) return EKV_ERR_INVALID_ARG;
+  if (num_pages < 1 || block_table_stride < 1) return EKV_ERR_INVALID_ARG;
+  if (scale_mode != EKV_SCALE_PER_TENSOR && scale_mode != EKV_SCALE_PER_PAGE_HEAD) return EKV_ERR_INVALID_ARG;
+  if (uniform_mode < EKV_MODE_TARGET_FP16 || uniform_mode > EKV_MODE_MICRO_FP4) return EKV_ERR_INVALID_ARG;
+  // a uniform E4M3 or microscaled pool may have small slots; any other holds FP16-sized ones
+  const long long n_elem = (long long)kPage * Hkv * D;
+  const long long need = page_mode || uniform_mode == EKV_MODE_TARGET_FP16 || uniform_mode == EKV_MODE_BASE ? 2 * n_elem
+                         : uniform_mode == EKV_MODE_COMPACT_E4M3 ? n_elem
+                                                                 : (long long)Hkv * micro_head_bytes(D);
+  if (v_page_stride_bytes < need || (v_page_stride_bytes & 15)) return EKV_ERR_INVALID_ARG;
+  if (!page_mode && uniform_mode == EKV_MODE_COMPACT_E4M3 && !v_scales) return EKV_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return EKV_ERR_INVALID_ARG;
+  v->k_pages = static_cast<const __half*>(k_pages);
+  v->v_pages = static_cast<const uint8_t*>(v_pages);
+  v->v_page_stride = v_page_stride_bytes;
+  v->num_pages = num_pages;
+  v->v_scales = v_scales;
+  v->scale_mode = scale_mode;
+  v->page_mode = page_mode;
+  v->uniform_mode = uniform_mode;
+  v->block_table = block_table;
+  v->bt_stride = block_table_stride;
+  v->seq_lens = seq_lens;
+  v->cu_q = cu_q;
+  v->batch = batch;
+  v->total_q = total_q;
+  v->Hq = c->cfg.num_q_heads;
+  v->Hkv = Hkv;
+  v->D = D;
+  v->err = c->err;
+  return EKV_OK;
+}
+
+}  // namespace
+
+ekv_status ekv_append_kv_rope(ekv_ctx* c, const void* q, const void* k_new, const void* v_new, long long q_stride,
+                              long long k_stride, long long v_stride, const float* rope_table, int rope_len,
+                              int rope_dim, int rope_style, void* q_out, void* k_pages, void* v_pages,
+                              long long v_page_stride_bytes, int num_pages, const float* v_scales, int scale_mode,
+                              const uint8_t* page_mode, int uniform_mode, const int32_t* block_table,
+                              int block_table_stride, const int32_t* seq_lens, const int32_t* cu_q, int batch,
+                              int total_q, void* stream) {
+  if (!c || batch < 0 || total_q < 0) return EKV_ERR_INVALID_ARG;
+  if (batch == 0 || total_q == 0) return EKV_OK;
+  const int Hq = c->cfg.num_q_heads, Hkv = c->cfg.num_kv_heads, D = c->cfg.head_dim;
+  if (!k_new || !v_new || (q && !q_out)) return EKV_ERR_INVALID_ARG;
+  if (rope_dim < 0 || rope_dim > D || rope_dim % 16 != 0 || (rope_style != 0 && rope_style != 1)) return EKV_ERR_INVALID_ARG;
+  if (rope_dim > 0 && (!rope_table || rope_len < 1 || !aligned16(rope_table))) return EKV_ERR_INVALID_ARG;
+  if ((q && (q_stride < (long long)Hq * D || (q_stride & 7))) || k_stride < (long long)Hkv * D || (k_stride & 7) ||
+      v_stride < (long long)Hkv * D || (v_stride & 7))
+    return EKV_ERR_INVALID_ARG;
+  if (q && (!aligned16(q) || !aligned16(q_out))) return EKV_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new)) return EKV_ERR_INVALID_ARG;
+  RopeAppendParams p;
+  const ekv_status s = cache_view(c, &p.c, k_pages, v_pages, v_page_stride_bytes, num_pages, v_scales, scale_mode,
+                                  page_mode, uniform_mode, block_table, block_table_stride, seq_lens, cu_q, batch,
+                                  total_q);
+  if (s != EKV_OK) return s;
+  p.q = static_cast<const __half*>(q);
+  p.k_new = static_cast<const __half*>(k_new);
+  p.v_new = static_cast<const __half*>(v_new);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.rope = rope_table;
+  p.rope_len = rope_len;
+  p.rope_dim = rope_dim;
+  p.rope_style = rope_style;
+  p.q_out = static_cast<__half*>(q_out);
+  DeviceGuard g(c->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  c->last_stream = st;
+  if (launch_rope_append(p, c->num_sms, st) != cudaSuccess) return EKV_ERR_CUDA;
+  note_launch(st, kAfterTransition);               // may write any page of a sequence, not its last alone
+  return EKV_OK;
+}
+
+ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, const void* v_pages,
+                                long long v_page_stride_bytes, int num_pages, const float* v_scales,
+                                int scale_mode, const uint8_t* page_mode, int uniform_mode,
+                                const int32_t* block_table, int block_table_stride, const int32_t* seq_lens,
+                                const int32_t* cu_q, int batch, int total_q, int max_q, int window, float sm_scale,
+                                void* out, float* lse, void* stream) {
+  if (!c || batch < 0 || total_q < 0 || max_q < 0 || window < 0) return EKV_ERR_INVALID_ARG;
+  if (batch > c->cfg.max_batch) return EKV_ERR_CAPACITY;
+  if (batch == 0 || total_q == 0) return EKV_OK;
+  const int Hq = c->cfg.num_q_heads, Hkv = c->cfg.num_kv_heads, D = c->cfg.head_dim;
+  if (!q || !out || !aligned16(q) || !aligned16(out)) return EKV_ERR_INVALID_ARG;
+  if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return EKV_ERR_INVALID_ARG;
+  ExtendParams p;
+  const ekv_status s = cache_view(c, &p.c, k_pages, v_pages, v_page_stride_bytes, num_pages, v_scales, scale_mode,
+                                  page_mode, uniform_mode, block_table, block_table_stride, seq_lens, cu_q, batch,
+                                  total_q);
+  if (s != EKV_OK) return s;
+  if (!(sm_scale > 0.f) || !isfinite(sm_scale)) sm_scale = 1.0f / sqrtf((float)D);
+  p.q = static_cast<const __half*>(q);
+  p.out = static_cast<__half*>(out);
+  p.lse = lse;
+  p.G = Hq / Hkv;
+  p.max_q = max_q;
+  p.window = window > 0 ? window : 0x7fffffff;
+  p.qscale = sm_scale * 1.4426950408889634f;
+  DeviceGuard g(c->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  c->last_stream = st;
+  if (launch_extend(p, c->num_sms, st) != cudaSuccess) return EKV_ERR_CUDA;
+  note_launch(st, kAfterReader);
   return EKV_OK;
 }
 

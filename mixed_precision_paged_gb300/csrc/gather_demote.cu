@@ -5,6 +5,7 @@
 // four persistent CTAs per SM, each with a ring of whole pages in shared memory.
 #include "common.cuh"
 #include "gather_demote.cuh"
+#include "micro.cuh"
 
 namespace ekv {
 
@@ -165,6 +166,9 @@ gather_kernel(const GatherParams p, const GatherRanges r) {
 //    to the page's first half, the low bytes to the caller's backing row (if any).
 //  kPromote (BASE -> TARGET, App. B.2): the fp16 words are rebuilt from the page's high
 //    bytes and the backing's low bytes.
+//  kToMicro (TARGET -> microscaled FP4): a thread's vector of 8 values and those of the 3
+//    lanes beside it are one block of 32; its largest magnitude is two shuffles away.
+//  kFromMicro (microscaled FP4 -> TARGET): every code times its scale, an fp16 value.
 // Demotions skip (and report) a page holding NaN/inf and leave it TARGET.
 //
 // Streaming form: 4 CTAs per SM, each takes items blockIdx.x, blockIdx.x + grid, ...
@@ -201,14 +205,14 @@ transition_kernel(const DemoteParams p, int n, int S) {
   const int grid = (int)gridDim.x;
   const int m = (n - (int)blockIdx.x + grid - 1) / grid;   // items of this CTA
   const int half_bytes = kPage * p.Hkv * p.D;     // one byte per value
-  const int page_bytes = 2 * half_bytes;          // stage size
-  const int nvec = page_bytes / 16;               // fp16 vectors of a page
+  const int page_bytes = OP == kFromMicro ? p.Hkv * micro_head_bytes(p.D) : 2 * half_bytes;   // stage size
+  const int nvec = 2 * half_bytes / 16;           // fp16 vectors of a page
   const int lanes_per_row = p.D / 8;              // 8 or 16: a row of one head
   // Vector v holds elements 8v .. 8v+7 of the page [16][H_kv][D], in KV head
   // (8v / D) mod H_kv. A thread's vectors are tid + 256u, 2048u elements apart, a
   // multiple of H_kv * D (<= 1024): they all lie in the same head.
   const int head = ((tid * 8) / p.D) % p.Hkv;
-  const int want = OP == kPromote ? EKV_MODE_BASE : EKV_MODE_TARGET_FP16;
+  const int want = OP == kPromote ? EKV_MODE_BASE : OP == kFromMicro ? EKV_MODE_MICRO_FP4 : EKV_MODE_TARGET_FP16;
 
   // items k0 .. k0 + kChunk - 1 of this CTA: page id if valid and in the source mode,
   // with its source and destination value locations (half-slot indices)
@@ -289,6 +293,24 @@ transition_kernel(const DemoteParams p, int n, int S) {
                                 __byte_perm(lb.y, hb.y, 0x5140), __byte_perm(lb.y, hb.y, 0x7362));
           }
         }
+      } else if (OP == kFromMicro) {
+        // vector v: 8 values of token row 8v / (H_kv D), from 4 code bytes and their scale
+        const uint8_t* st = ring + sl * page_bytes + head * micro_head_bytes(p.D);
+        const int col = (tid * 8) % p.D;
+        bool bad = false;
+#pragma unroll
+        for (int u = 0; u < kMaxVec; ++u) {
+          const int v = tid + u * kDemoteThreads;
+          if (v < nvec) {
+            const int row = (v * 8) / (p.Hkv * p.D);
+            const uint32_t codes = *reinterpret_cast<const uint32_t*>(st + (row * p.D + col) / 2);
+            const uint32_t sb = st[micro_scale_off(p.D) + (row * p.D + col) / kMicroBlock];
+            const bool good = micro_scale_ok(sb);
+            bad |= !good;
+            buf[u] = good ? micro_decode8(codes, micro_scale_h2(sb)) : make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        if (bad) report_error(p.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SCALE, page);
       } else {
         const uint4* src = reinterpret_cast<const uint4*>(ring + sl * page_bytes);
         // every vector of this thread lies in KV head `head`: reduce locally first,
@@ -329,7 +351,7 @@ transition_kernel(const DemoteParams p, int n, int S) {
     if (page < 0) continue;                        // block-uniform
     // a demotion writes the half at dst_loc; a promotion the slot of dst_loc (even)
     uint8_t* base = p.v_pages + (size_t)(dst_loc >> 1) * p.v_page_stride + (dst_loc & 1) * half_bytes;
-    if (OP == kPromote) {
+    if (OP == kPromote || OP == kFromMicro) {
       uint4* dst = reinterpret_cast<uint4*>(base);
 #pragma unroll
       for (int u = 0; u < kMaxVec; ++u) {
@@ -388,10 +410,28 @@ transition_kernel(const DemoteParams p, int n, int S) {
               make_uint2(__byte_perm(w.x, w.y, 0x6420), __byte_perm(w.z, w.w, 0x6420));
       }
     }
+    if (!skip && OP == kToMicro) {
+      uint8_t* slice = base + head * micro_head_bytes(p.D);
+      const int col = (tid * 8) % p.D;
+#pragma unroll
+      for (int u = 0; u < kMaxVec; ++u) {
+        const int v = tid + u * kDemoteThreads;
+        // nvec is a multiple of 128: whole warps leave here, so the shuffles see full warps
+        if (v >= nvec) break;
+        const int row = (v * 8) / (p.Hkv * p.D);
+        uint32_t mx2 = __vmaxu2(__vmaxu2(buf[u].x & 0x7fff7fffu, buf[u].y & 0x7fff7fffu),
+                                __vmaxu2(buf[u].z & 0x7fff7fffu, buf[u].w & 0x7fff7fffu));
+        mx2 = __vmaxu2(mx2, __shfl_xor_sync(0xffffffffu, mx2, 1));
+        mx2 = __vmaxu2(mx2, __shfl_xor_sync(0xffffffffu, mx2, 2));
+        const int e = micro_exponent(max(mx2 & 0xffffu, mx2 >> 16));
+        *reinterpret_cast<uint32_t*>(slice + (row * p.D + col) / 2) = micro_encode8(buf[u], e);
+        if (col % kMicroBlock == 0) slice[micro_scale_off(p.D) + (row * p.D + col) / kMicroBlock] = (uint8_t)(127 + e);
+      }
+    }
     __syncthreads();                               // s_nonfinite and the scales are read
     if (tid == 0) {
       if (skip) report_error(p.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_NONFINITE_PAGE, page);
-      else p.page_mode[page] = OP == kToBase ? EKV_MODE_BASE : EKV_MODE_COMPACT_E4M3;
+      else p.page_mode[page] = OP == kToBase ? EKV_MODE_BASE : OP == kToMicro ? EKV_MODE_MICRO_FP4 : EKV_MODE_COMPACT_E4M3;
       s_nonfinite = 0;
     }
   }
@@ -401,7 +441,7 @@ cudaError_t set_smem_attr(const void* kern, int bytes);
 
 template <int OP>
 static cudaError_t launch_op(const DemoteParams& p, int n, int num_sms, cudaStream_t st) {
-  const int page_bytes = kPage * p.Hkv * p.D * 2;
+  const int page_bytes = OP == kFromMicro ? p.Hkv * micro_head_bytes(p.D) : kPage * p.Hkv * p.D * 2;
   int S = kDemoteRingBytes / page_bytes;
   S = S > kDemoteMaxStages ? kDemoteMaxStages : S;
   const int grid = n < 4 * num_sms ? n : 4 * num_sms;
@@ -416,6 +456,8 @@ cudaError_t launch_transition(const DemoteParams& p, int op, int n, int num_sms,
   if (n <= 0) return cudaSuccess;
   if (op == kToBase) return launch_op<kToBase>(p, n, num_sms, st);
   if (op == kPromote) return launch_op<kPromote>(p, n, num_sms, st);
+  if (op == kToMicro) return launch_op<kToMicro>(p, n, num_sms, st);
+  if (op == kFromMicro) return launch_op<kFromMicro>(p, n, num_sms, st);
   return launch_op<kToE4M3>(p, n, num_sms, st);
 }
 

@@ -45,7 +45,7 @@ struct GatherParams {
 };
 
 // Page-mode transitions run by the same streaming kernel.
-enum TransitionOp { kToE4M3 = 0, kToBase = 1, kPromote = 2 };
+enum TransitionOp { kToE4M3 = 0, kToBase = 1, kPromote = 2, kToMicro = 3, kFromMicro = 4 };
 
 struct DemoteParams {
   uint8_t* v_pages;

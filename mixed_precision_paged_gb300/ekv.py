@@ -32,6 +32,7 @@ EKV_ERR_DEVICE_CHECK = 5
 EKV_MODE_TARGET_FP16 = 0
 EKV_MODE_COMPACT_E4M3 = 1
 EKV_MODE_BASE = 2
+EKV_MODE_MICRO_FP4 = 3
 EKV_SCALE_PER_TENSOR = 0
 EKV_SCALE_PER_PAGE_HEAD = 1
 
@@ -48,6 +49,7 @@ EXPORTED = ["ekv_create", "ekv_destroy", "ekv_paged_decode", "ekv_gather_prefill
             "ekv_set_decode_variant", "ekv_query", "ekv_paged_decode_noalloc",
             "ekv_demote_pages_base", "ekv_promote_pages", "ekv_append_kv", "ekv_paged_decode_elastic",
             "ekv_transition_pages", "ekv_prefill_attention", "ekv_gather_prefill_elastic",
+            "ekv_append_kv_rope", "ekv_extend_attention", "ekv_demote_pages_micro", "ekv_expand_pages_micro",
             "ekv_set_pdl", "ekv_profile_launch_floor", "ekv_status_string"]
 
 
@@ -76,6 +78,12 @@ _lib.ekv_paged_decode_elastic.argtypes = [_vp, _vp, _vp, _vp, _ll, _i, _i, _vp, 
 _lib.ekv_transition_pages.argtypes = [_vp, _i, _vp, _ll, _i, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp]
 _lib.ekv_prefill_attention.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, ctypes.c_float, _vp, _vp, _vp]
 _lib.ekv_append_kv.argtypes = [_vp, _vp, _vp, _vp, _vp, _ll, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp]
+_lib.ekv_append_kv_rope.argtypes = [_vp, _vp, _vp, _vp, _ll, _ll, _ll, _vp, _i, _i, _i, _vp, _vp, _vp, _ll, _i, _vp, _i,
+                                    _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp]
+_lib.ekv_extend_attention.argtypes = [_vp, _vp, _vp, _vp, _ll, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i,
+                                      ctypes.c_float, _vp, _vp, _vp]
+_lib.ekv_demote_pages_micro.argtypes = [_vp, _vp, _ll, _i, _vp, _i, _vp, _vp]
+_lib.ekv_expand_pages_micro.argtypes = [_vp, _vp, _ll, _i, _vp, _i, _vp, _vp]
 _lib.ekv_paged_decode_noalloc.argtypes = [_i, _i, _i, _vp, _vp, _vp, _ll, _i, _vp, _i, _vp, _i, _vp, _i,
                                           _vp, _i, ctypes.c_float, _vp, _vp, _vp, _vp]
 _lib.ekv_get_error.argtypes = [_vp, ctypes.POINTER(_i), ctypes.POINTER(_i)]
@@ -248,6 +256,39 @@ def ekv_append_kv(ctx, k_new, v_new, k_pages, v_pages, v_page_stride_bytes, num_
                               v_page_stride_bytes, num_pages, _ptr(v_scales), scale_mode, _ptr(page_mode),
                               uniform_mode, _ptr(block_table), block_table_stride, _ptr(positions), batch,
                               _stream(stream)), "ekv_append_kv")
+
+
+def ekv_append_kv_rope(ctx, q, k_new, v_new, q_stride, k_stride, v_stride, rope_table, rope_len, rope_dim, rope_style,
+                       q_out, k_pages, v_pages, v_page_stride_bytes, num_pages, v_scales, scale_mode, page_mode,
+                       uniform_mode, block_table, block_table_stride, seq_lens, cu_q, batch, total_q, stream=None):
+    """Rotate the new tokens' queries and keys by their positions and write keys and values into the paged cache."""
+    _check(_lib.ekv_append_kv_rope(ctx, _ptr(q), _ptr(k_new), _ptr(v_new), q_stride, k_stride, v_stride,
+                                   _ptr(rope_table), rope_len, rope_dim, rope_style, _ptr(q_out), _ptr(k_pages),
+                                   _ptr(v_pages), v_page_stride_bytes, num_pages, _ptr(v_scales), scale_mode,
+                                   _ptr(page_mode), uniform_mode, _ptr(block_table), block_table_stride,
+                                   _ptr(seq_lens), _ptr(cu_q), batch, total_q, _stream(stream)), "ekv_append_kv_rope")
+
+
+def ekv_extend_attention(ctx, q, k_pages, v_pages, v_page_stride_bytes, num_pages, v_scales, scale_mode, page_mode,
+                         uniform_mode, block_table, block_table_stride, seq_lens, cu_q, batch, total_q, max_q, window,
+                         sm_scale, out, lse=None, stream=None):
+    """Attention of every sequence's new tokens (one or many) over the paged cache, causal, with an optional window."""
+    _check(_lib.ekv_extend_attention(ctx, _ptr(q), _ptr(k_pages), _ptr(v_pages), v_page_stride_bytes, num_pages,
+                                     _ptr(v_scales), scale_mode, _ptr(page_mode), uniform_mode, _ptr(block_table),
+                                     block_table_stride, _ptr(seq_lens), _ptr(cu_q), batch, total_q, max_q, window,
+                                     float(sm_scale), _ptr(out), _ptr(lse), _stream(stream)), "ekv_extend_attention")
+
+
+def ekv_demote_pages_micro(ctx, v_pages, v_page_stride_bytes, num_pages, page_ids, n, page_mode, stream=None):
+    """TARGET -> microscaled FP4, in place."""
+    _check(_lib.ekv_demote_pages_micro(ctx, _ptr(v_pages), v_page_stride_bytes, num_pages, _ptr(page_ids), n,
+                                       _ptr(page_mode), _stream(stream)), "ekv_demote_pages_micro")
+
+
+def ekv_expand_pages_micro(ctx, v_pages, v_page_stride_bytes, num_pages, page_ids, n, page_mode, stream=None):
+    """Microscaled FP4 -> TARGET, in place: the values that the codes stand for."""
+    _check(_lib.ekv_expand_pages_micro(ctx, _ptr(v_pages), v_page_stride_bytes, num_pages, _ptr(page_ids), n,
+                                       _ptr(page_mode), _stream(stream)), "ekv_expand_pages_micro")
 
 
 def ekv_get_error(ctx):

@@ -26,6 +26,9 @@ It is written from the pages' statement of the problem, plainly and slowly:
                  (knlp.io "What changes in vLLM's prefill routing?": native FP16 prefill).
 * ``writer`` -- the K16/V8 cache writer: one new token per sequence into its page row
                 (knlp.io implementation checks: "K bit-exact, V within FP8 noise").
+* ``micro``  -- microscaled FP4 value pages (E2M1 codes, a power-of-two scale per 32 values).
+* ``extend`` -- new tokens of a ragged batch: the rotary cache writer and their causal
+                attention, optionally windowed, over the paged cache.
 * ``demote`` -- TARGET -> compact requantisation of FP16 value pages with absmax
                 scales (ElasticKV Sec. 3.4 "Transition protocols", with the compact
                 format of the knlp.io page).
@@ -35,7 +38,7 @@ no code with the CUDA path. Pins that tie each function to something other than
 itself live in ``tests/test_oracle_*.py``.
 """
 
-from . import base, e4m3, decode, gather, demote, writer, elastic, prefill  # noqa: F401
+from . import base, e4m3, decode, gather, demote, writer, elastic, prefill, micro, extend  # noqa: F401
 
 PAGE_SIZE = 16
 MODE_TARGET_FP16 = 0
