@@ -10,7 +10,7 @@
 #include <vector>
 
 #include "decode.cuh"
-#include "extend.cuh"
+#include "extend_split.cuh"
 #include "gather_demote.cuh"
 #include "micro.cuh"
 #include "pool_maps.h"
@@ -21,6 +21,9 @@ cudaError_t launch_split_simt(const CUtensorMap& tk, const CUtensorMap& t8, cons
                               const DecodeParams& p, int D, int vmode, int grid, size_t smem, cudaStream_t st);
 cudaError_t launch_split_mma(const CUtensorMap& tk, const CUtensorMap& t8, const CUtensorMap& t16,
                              const DecodeParams& p, int D, int vmode, int grid, size_t smem, cudaStream_t st);
+
+cudaError_t launch_extend_split_64(const CUtensorMap (&tm)[3], const ExtSplitParams& p, int vm, int grid, cudaStream_t st);
+cudaError_t launch_extend_split_128(const CUtensorMap (&tm)[3], const ExtSplitParams& p, int vm, int grid, cudaStream_t st);
 
 // ------------------------------------------------------------- launch floor
 // An empty kernel with the split kernel's block, shared memory and parameter list: what
@@ -64,6 +67,10 @@ struct ekv_ctx {
   float* part_acc = nullptr;
   float2* part_ml = nullptr;
   int* plan = nullptr;
+  // attention of new tokens: partial rows (two segments per range or CTA) and group tickets
+  float* ext_acc = nullptr;
+  float2* ext_ml = nullptr;
+  int* ext_ticket = nullptr;
   int* err = nullptr;
   cudaStream_t last_stream = nullptr;
   bool profiling = false;
@@ -117,6 +124,11 @@ int last_kernel(cudaStream_t st) {
 int g_inject_timeout_calls = 0;
 #endif
 
+// Rows of the partial results of ekv_extend_attention: two segments of kXRows rows per page range
+// and KV head (8 / H_kv ranges per CTA), and its group tickets.
+size_t ext_rows(const ekv_ctx* c) { return (size_t)c->split_ctas * 2 * kXWarps * kXRows; }
+size_t ext_tickets(const ekv_ctx* c) { return (size_t)c->split_ctas * 2 * kXWarps; }
+
 bool supported_shape(int Hq, int Hkv, int D) {
   if (D != 64 && D != 128) return false;
   if (Hkv != 1 && Hkv != 2 && Hkv != 4 && Hkv != 8) return false;
@@ -164,6 +176,10 @@ ekv_status ekv_create(ekv_ctx** out, const ekv_config* cfg) {
   bool ok = cudaMalloc(&c->part_acc, records * hq * cfg->head_dim * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&c->part_ml, records * hq * sizeof(float2)) == cudaSuccess &&
             cudaMalloc(&c->plan, kPlanInts * sizeof(int)) == cudaSuccess &&
+            cudaMalloc(&c->ext_acc, ext_rows(c) * cfg->head_dim * sizeof(float)) == cudaSuccess &&
+            cudaMalloc(&c->ext_ml, ext_rows(c) * sizeof(float2)) == cudaSuccess &&
+            cudaMalloc(&c->ext_ticket, ext_tickets(c) * sizeof(int)) == cudaSuccess &&
+            cudaMemset(c->ext_ticket, 0, ext_tickets(c) * sizeof(int)) == cudaSuccess &&
             cudaMalloc(&c->err, 4 * sizeof(int)) == cudaSuccess &&
             cudaMemset(c->plan, 0, kPlanInts * sizeof(int)) == cudaSuccess &&
             cudaMemset(c->err, 0, 4 * sizeof(int)) == cudaSuccess &&
@@ -184,6 +200,9 @@ ekv_status ekv_destroy(ekv_ctx* c) {
   cudaFree(c->part_acc);
   cudaFree(c->part_ml);
   cudaFree(c->plan);
+  cudaFree(c->ext_acc);
+  cudaFree(c->ext_ml);
+  cudaFree(c->ext_ticket);
   cudaFree(c->err);
   delete c;
   return EKV_OK;
@@ -671,7 +690,32 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
   DeviceGuard g(c->device);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   c->last_stream = st;
-  if (launch_extend(p, c->num_sms, st) != cudaSuccess) return EKV_ERR_CUDA;
+  cudaError_t e;
+  if ((long long)p.G * max_q <= kXRows) {
+    const int vm = page_mode || uniform_mode == EKV_MODE_BASE ? kXMixed
+                   : uniform_mode == EKV_MODE_TARGET_FP16     ? kXFP16
+                   : uniform_mode == EKV_MODE_COMPACT_E4M3    ? kXE4M3
+                                                              : kXMicro;
+    const int map_mode = vm == kXMixed ? kVMixed : vm == kXE4M3 ? kVE4M3 : kVFP16;
+    CUtensorMap tm[3];
+    // (a microscaled pool has small slots: no map over its values)
+    if (!decode_pool_maps(&tm[0], &tm[1], &tm[2], k_pages, v_pages, D, Hkv, num_pages,
+                          vm == kXMicro ? 2ll * kPage * Hkv * D : v_page_stride_bytes, map_mode))
+      return EKV_ERR_INVALID_ARG;
+    ExtSplitParams x;
+    memset(&x, 0, sizeof(x));
+    x.e = p;
+    x.part_acc = c->ext_acc;
+    x.part_ml = c->ext_ml;
+    x.ticket = c->plan + kPlanTicket;
+    x.group_ticket = c->ext_ticket;
+    x.NG = c->NG;
+    e = D == 128 ? launch_extend_split_128(tm, x, vm, c->split_ctas, st)
+                 : launch_extend_split_64(tm, x, vm, c->split_ctas, st);
+  } else {
+    e = launch_extend(p, c->num_sms, st);
+  }
+  if (e != cudaSuccess) return EKV_ERR_CUDA;
   note_launch(st, kAfterReader);
   return EKV_OK;
 }
@@ -725,6 +769,7 @@ ekv_status ekv_get_error(ekv_ctx* c, int* code, int* detail) {
   // a clean plan buffer: no stale tickets. Only the context's stream is synchronised.
   if (cudaStreamSynchronize(st) != cudaSuccess) return EKV_ERR_CUDA;
   if (h[0] != 0 && (cudaMemsetAsync(c->plan, 0, kPlanInts * sizeof(int), st) != cudaSuccess ||
+                    cudaMemsetAsync(c->ext_ticket, 0, ext_tickets(c) * sizeof(int), st) != cudaSuccess ||
                     cudaStreamSynchronize(st) != cudaSuccess))
     return EKV_ERR_CUDA;
   if (code) *code = h[0];
