@@ -385,8 +385,8 @@ ekv_status ekv_append_kv_rope(ekv_ctx* ctx, const void* q, const void* k_new, co
  *  lse          fp32 [total_q][H_q], natural logarithm, or NULL.
  * A page that fails its check (id, mode byte > 3, scale) zeroes out and sets lse = -inf for the
  * queries that see one of its keys (of one KV head for a bad per-(page, head) scale). Returns
- * EKV_ERR_CAPACITY when batch > cfg.max_batch. Other arguments as for ekv_paged_decode; sums are
- * fp32, the weights enter the product with V rounded to fp16. */
+ * EKV_ERR_CAPACITY when batch > cfg.max_batch, EKV_ERR_UNSUPPORTED when block_table_stride > 131072
+ * or a pool has 2^31 or more head rows. Other arguments as for ekv_paged_decode; sums are fp32, the weights enter the product with V rounded to fp16. */
 ekv_status ekv_extend_attention(ekv_ctx* ctx, const void* q, const void* k_pages, const void* v_pages,
                                 long long v_page_stride_bytes, int num_pages, const float* v_scales,
                                 int scale_mode, const uint8_t* page_mode, int uniform_mode,

@@ -10,7 +10,7 @@
 #include <vector>
 
 #include "decode.cuh"
-#include "extend_split.cuh"
+#include "extend_tc05.cuh"
 #include "gather_demote.cuh"
 #include "micro.cuh"
 #include "pool_maps.h"
@@ -24,6 +24,9 @@ cudaError_t launch_split_mma(const CUtensorMap& tk, const CUtensorMap& t8, const
 
 cudaError_t launch_extend_split_64(const CUtensorMap (&tm)[3], const ExtSplitParams& p, int vm, int grid, cudaStream_t st);
 cudaError_t launch_extend_split_128(const CUtensorMap (&tm)[3], const ExtSplitParams& p, int vm, int grid, cudaStream_t st);
+
+cudaError_t launch_extend_tc05_64(const ExtTcMaps& m, const ExtTcParams& p, int vm, int grid, cudaStream_t st);
+cudaError_t launch_extend_tc05_128(const ExtTcMaps& m, const ExtTcParams& p, int vm, int grid, cudaStream_t st);
 
 // ------------------------------------------------------------- launch floor
 // An empty kernel with the split kernel's block, shared memory and parameter list: what
@@ -71,6 +74,7 @@ struct ekv_ctx {
   float* ext_acc = nullptr;
   float2* ext_ml = nullptr;
   int* ext_ticket = nullptr;
+  ExtTcSplit* ext_split = nullptr;
   int* err = nullptr;
   cudaStream_t last_stream = nullptr;
   bool profiling = false;
@@ -179,6 +183,7 @@ ekv_status ekv_create(ekv_ctx** out, const ekv_config* cfg) {
             cudaMalloc(&c->ext_acc, ext_rows(c) * cfg->head_dim * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&c->ext_ml, ext_rows(c) * sizeof(float2)) == cudaSuccess &&
             cudaMalloc(&c->ext_ticket, ext_tickets(c) * sizeof(int)) == cudaSuccess &&
+            cudaMalloc(&c->ext_split, c->split_ctas * sizeof(ExtTcSplit)) == cudaSuccess &&
             cudaMemset(c->ext_ticket, 0, ext_tickets(c) * sizeof(int)) == cudaSuccess &&
             cudaMalloc(&c->err, 4 * sizeof(int)) == cudaSuccess &&
             cudaMemset(c->plan, 0, kPlanInts * sizeof(int)) == cudaSuccess &&
@@ -203,6 +208,7 @@ ekv_status ekv_destroy(ekv_ctx* c) {
   cudaFree(c->ext_acc);
   cudaFree(c->ext_ml);
   cudaFree(c->ext_ticket);
+  cudaFree(c->ext_split);
   cudaFree(c->err);
   delete c;
   return EKV_OK;
@@ -673,6 +679,7 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
   if (batch == 0 || total_q == 0) return EKV_OK;
   const int Hq = c->cfg.num_q_heads, Hkv = c->cfg.num_kv_heads, D = c->cfg.head_dim;
   if (!q || !out || !aligned16(q) || !aligned16(out)) return EKV_ERR_INVALID_ARG;
+  if (block_table_stride > kMaxExtendPages) return EKV_ERR_UNSUPPORTED;
   if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return EKV_ERR_INVALID_ARG;
   ExtendParams p;
   const ekv_status s = cache_view(c, &p.c, k_pages, v_pages, v_page_stride_bytes, num_pages, v_scales, scale_mode,
@@ -690,12 +697,12 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
   DeviceGuard g(c->device);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   c->last_stream = st;
+  const int vm = page_mode || uniform_mode == EKV_MODE_BASE ? kXMixed
+                 : uniform_mode == EKV_MODE_TARGET_FP16     ? kXFP16
+                 : uniform_mode == EKV_MODE_COMPACT_E4M3    ? kXE4M3
+                                                            : kXMicro;
   cudaError_t e;
-  if ((long long)p.G * max_q <= kXRows) {
-    const int vm = page_mode || uniform_mode == EKV_MODE_BASE ? kXMixed
-                   : uniform_mode == EKV_MODE_TARGET_FP16     ? kXFP16
-                   : uniform_mode == EKV_MODE_COMPACT_E4M3    ? kXE4M3
-                                                              : kXMicro;
+  if ((long long)p.G * max_q <= kXRows) {          // few query rows: the stream over the cache
     const int map_mode = vm == kXMixed ? kVMixed : vm == kXE4M3 ? kVE4M3 : kVFP16;
     CUtensorMap tm[3];
     // (a microscaled pool has small slots: no map over its values)
@@ -713,7 +720,29 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
     e = D == 128 ? launch_extend_split_128(tm, x, vm, c->split_ctas, st)
                  : launch_extend_split_64(tm, x, vm, c->split_ctas, st);
   } else {
-    e = launch_extend(p, c->num_sms, st);
+    ExtTcMaps m;
+    memset(&m, 0, sizeof(m));
+    ExtTcParams x;
+    memset(&x, 0, sizeof(x));
+    x.e = p;
+    x.part_acc = c->ext_acc;
+    x.part_ml = c->ext_ml;
+    x.split = c->ext_split;
+    if (vm == kXE4M3 && scale_mode == EKV_SCALE_PER_TENSOR) x.scale_ptr = v_scales;
+    // one coordinate for (page, head): in units that divide both the page stride and a head's row
+    int unit = 2 * D;
+    while (v_page_stride_bytes % unit) unit /= 2;
+    const long long places = (long long)num_pages * (v_page_stride_bytes / unit);
+    if ((long long)num_pages * kPage * Hkv > 0x7fffffffLL || places > 0x7fffffffLL) return EKV_ERR_UNSUPPORTED;
+    x.v16_mul = (int)(v_page_stride_bytes / unit);
+    x.v16_head = 2 * D / unit;
+    if (!encode_query_map(&m.q, q, D, Hkv, p.G, total_q) ||
+        !encode_group_map(&m.k, k_pages, D, Hkv, (unsigned long long)num_pages * kPage * Hkv, 2 * D))
+      return EKV_ERR_INVALID_ARG;
+    if ((vm == kXFP16 || vm == kXMixed) && !encode_group_map(&m.v16, v_pages, D, Hkv, places, unit)) return EKV_ERR_INVALID_ARG;
+    if ((vm == kXE4M3 || vm == kXMixed) && !encode_e4m3_slice_map(&m.v8, v_pages, D, Hkv, num_pages, v_page_stride_bytes))
+      return EKV_ERR_INVALID_ARG;
+    e = D == 128 ? launch_extend_tc05_128(m, x, vm, c->split_ctas, st) : launch_extend_tc05_64(m, x, vm, c->split_ctas, st);
   }
   if (e != cudaSuccess) return EKV_ERR_CUDA;
   note_launch(st, kAfterReader);

@@ -37,6 +37,9 @@ struct RopeAppendParams {
   __half* q_out;
 };
 
+// Pages of a sequence at most (2^21 tokens): keeps the block counts of the plan in 32 bits.
+constexpr int kMaxExtendPages = 1 << 17;
+
 struct ExtendParams {
   CacheView c;
   const __half* q;
@@ -66,6 +69,5 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t* cu, int batch, 
 }
 
 cudaError_t launch_rope_append(const RopeAppendParams& p, int num_sms, cudaStream_t st);
-cudaError_t launch_extend(const ExtendParams& p, int num_sms, cudaStream_t st);
 
 }  // namespace ekv

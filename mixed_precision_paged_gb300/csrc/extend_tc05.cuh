@@ -1,0 +1,1051 @@
+// extend_tc05.cuh -- attention of many new tokens per sequence over the paged cache (prompt
+// chunks behind a cached prefix) on the fifth-generation tensor cores.
+//
+// For a block of 128 keys and a tile of 128 query rows the work is two products,
+//   S = Q K^T,  O += P V,  P = 2^(S sm_scale log2 e - m),
+// 4 * 128 * 128 * D operations against 128 * D * (2 + 1) bytes of a K16/V8 block: with 256 rows the tensor
+// pipe bounds it, and the softmax (128 exponentials a row and block) comes next. So:
+//   * rows: a tile packs the G query heads of a KV head, row = token * G + g, 128 / G tokens each,
+//     and a work item is a pair of tiles that share every block: one read of K and V serves 256
+//     rows, and one tile's softmax runs while the other's products do.
+//   * blocks: 8 pages by one TMA box each, 8-token groups of [D / 64][8 rows][128 B] (128B swizzle),
+//     which serve as K-major B of S and, for V, as N-major B of the second product.
+//   * values: FP16 pages land in a V stage directly. E4M3, BASE and microscaled pages land raw in a
+//     ring of their own and two warps expand them into the V stage, exactly; E4M3 scales join the
+//     exponent as in the split kernel (extend_split.cuh), or the output when one scale serves all.
+//   * split: the blocks of all items form one stream, cut into equal ranges, one persistent CTA
+//     each; an item that crosses a border leaves partial rows (m, l, O) in at most two slots a CTA, and
+//     a second kernel joins them. Long causal chunks so balance to a block, and one short chunk
+//     behind a long prefix still uses every SM.
+// Roles: warp 0 loads Q, K and raw values and checks the pages; warp 1 issues the MMAs; warps 2 and 3
+// make the V stages (warp 2 owns tensor memory); warps 4-7 and 8-11 are the softmax of tile 0 and
+// 1, a thread per row. Tensor memory of tile t: S and P at 256 t, O at 256 t + 128. The order of
+// the MMAs and the lazily moved maximum are those of the prefill (prefill_tc05.cu). Every wait is
+// bounded; a timeout is reported and every role winds down.
+#pragma once
+
+#include "extend_split.cuh"
+#include "pool_maps.h"
+#include "tc05.cuh"
+
+namespace ekv {
+
+constexpr int kTRows = 128;                 // rows of a query tile (MMA M)
+constexpr int kTKeys = 128;                 // keys of a block (N of S)
+constexpr int kTPages = kTKeys / kPage;
+constexpr int kT5Threads = 384;
+constexpr int kItemCost = 1;                // an item's start (query load, epilogue) in blocks
+
+struct ExtTcSplit {                         // an item that crosses CTAs, for the joining kernel
+  int n;                                    // CTAs it spans; 0: none
+  int first;                                // its first slot; the others are 2 * (cta + 1), ...
+  int b, h, i;
+};
+
+struct ExtTcParams {
+  ExtendParams e;
+  float* part_acc;                          // [2 * grid][256][D]
+  float2* part_ml;                          // [2 * grid][256]
+  ExtTcSplit* split;                        // [grid]
+  const float* scale_ptr;                   // one E4M3 scale for every code (it scales the output), or null
+  int v16_mul, v16_head;                    // FP16 value map: index = page * v16_mul + head * v16_head
+};
+
+template <int D, int VM>
+struct XT {
+  static constexpr int NB = D / 64;                    // 64-value slabs of a row
+  static constexpr int GB = NB * 1024;                 // bytes of an 8-token group
+  static constexpr int QB = kTRows * D * 2;            // a query tile
+  static constexpr int IB = kTKeys * D * 2;            // a K or V block
+  static constexpr int RB = VM == kXFP16 ? 0 : kTKeys * D;   // a raw block: a page at every 16 * D bytes
+  static constexpr int NK = VM == kXFP16 ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 4);
+  static constexpr int NV = D == 128 ? 2 : 4;
+  static constexpr int NR = D == 128 ? 2 : 4;
+  static constexpr int NM = 8;                         // block descriptions; at least NK + 1
+};
+
+struct BlockMeta {
+  int page[kTPages];
+  int flags[kTPages];                       // xs::kSkip: not loaded
+  float lsc[kTPages];                       // log2 of the scale
+  float ivs[kTPages];                       // and its reciprocal
+  int bad;                                  // bit per page that failed its checks
+};
+
+template <int D, int VM>
+struct XTBars {
+  using C = XT<D, VM>;
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[C::NK], k_empty[C::NK];
+  uint64_t raw_full[C::NR], raw_empty[C::NR];
+  uint64_t v_full[C::NV], v_empty[C::NV];
+  uint64_t v_dir[C::NV];                    // FP16 pages of a stage whose edge rows are zeroed after they land
+  uint64_t meta_full[C::NM];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t mma_final;
+  BlockMeta meta[C::NM];
+  long long red[kT5Threads / 32];
+  int st_b, st_h, st_i, st_j;               // where this CTA's range begins
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D, int VM>
+constexpr int xt_smem_bytes() {
+  using C = XT<D, VM>;
+  return 1024 + 2 * C::QB + C::NK * C::IB + C::NV * C::IB + C::NR * C::RB + (int)sizeof(XTBars<D, VM>);
+}
+
+namespace xt {
+
+using xs::Seq;
+using xs::load_seq;
+using xs::seq_ok;
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > kWaitTimeoutNs)) return false;
+  }
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
+}
+__device__ __forceinline__ void give_up(int* err, volatile int* abort) {
+  if (!*abort) report_error(err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_TIMEOUT, -1);
+  *abort = 1;
+}
+// A bounded wait that ignores an abort: for copies in flight at the end.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+  }
+}
+__device__ __forceinline__ void expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// (d0, d1) = (a0, a1) * b + c, and (a0, a1) += (b0, b1): packed FP32 instructions
+__device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b, float c) {
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void fadd2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb;\n\t"
+      "mov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %3};\n\t"
+      "add.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ void tst16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// ------------------------------------------------------------------------ plan
+// sum over i < n of floor((a i + b) / m), n, a, b >= 0 (the Euclid-like reduction of the lattice
+// point count under a line; Graham, Knuth, Patashnik, Concrete Mathematics, Sec. 3.5).
+__device__ __forceinline__ int floor_sum(int n, int m, int a, int b) {
+  uint32_t s = 0, un = n, um = m, ua = a, ub = b;      // n <= 2^16, the sum < 2^31 (see the entry point's limit)
+  while (un > 0) {
+    s += un * (un - 1) / 2 * (ua / um) + un * (ub / um);
+    ua %= um;
+    ub %= um;
+    const uint32_t y = ua * un + ub;
+    if (y < um) break;
+    un = y / um;
+    ub = y % um;
+    const uint32_t t = um;
+    um = ua;
+    ua = t;
+  }
+  return (int)s;
+}
+
+// The items of one sequence and KV head: pairs of tiles, `step` tokens each.
+struct Items {
+  int L, n, t0, step, np, window;
+  // keys of item i: [lo, hi)
+  __device__ __forceinline__ int lo(int i) const {
+    const int first = t0 + i * step;
+    return first < window ? 0 : first - window + 1;
+  }
+  __device__ __forceinline__ int hi(int i) const { return t0 + min((i + 1) * step, n); }
+  __device__ __forceinline__ int jlo(int i) const { return lo(i) / kTKeys; }
+  __device__ __forceinline__ int jhi(int i) const { return (hi(i) + kTKeys - 1) / kTKeys; }
+  // blocks, and kItemCost each, of the items before i
+  __device__ __forceinline__ int before(int i) const {
+    if (i <= 0) return 0;
+    const int full = i == np ? np - 1 : i;            // the last item may be short
+    int s = kItemCost * i + floor_sum(full, kTKeys, step, t0 + step + kTKeys - 1);
+    if (i == np) s += jhi(np - 1);
+    const int i0 = t0 >= window - 1 ? 0 : min(i, (window - 2 - t0) / step + 1);   // items whose window starts at key 0
+    if (i > i0) s -= floor_sum(i - i0, kTKeys, step, t0 + i0 * step - window + 1);
+    return s;
+  }
+};
+__device__ __forceinline__ Items items_of(const ExtendParams& e, const Seq& s) {
+  Items it;
+  it.L = s.L;
+  it.n = s.n;
+  it.t0 = s.L - s.n;
+  it.step = 2 * (kTRows / e.G);
+  it.np = (s.n + it.step - 1) / it.step;
+  it.window = e.window;
+  return it;
+}
+
+// A walk over this CTA's segments; every role makes the same one.
+struct Walk {
+  int b, h, i, j;           // next: sequence, KV head, item, block (j may lie kItemCost before the item's first)
+  int budget;               // blocks left in the CTA's range
+  int index;                // segments so far
+  Seq sq;
+  Items it;
+};
+struct Segment {
+  int ja, jb;               // blocks
+  int jlo, jhi;             // of the whole item
+  int h, i, slot;
+  int nt[2];                // blocks that each tile takes part in, from ja on
+  bool whole;
+};
+
+__device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segment& sg) {
+  while (w.budget > 0 && w.b < e.c.batch) {
+    sg.jlo = w.it.jlo(w.i);
+    sg.jhi = w.it.jhi(w.i);
+    sg.h = w.h;
+    sg.i = w.i;
+    const int ja = w.j, jb = min(sg.jhi, w.j + w.budget);
+    w.budget -= jb - ja;
+    w.j = jb;
+    sg.ja = max(ja, sg.jlo);
+    sg.jb = jb;
+    sg.whole = sg.ja == sg.jlo && jb == sg.jhi;
+    // tile 0 ends with its own last token's block
+    const int half = w.it.step / 2;
+    const int e0 = (w.it.t0 + min(w.i * w.it.step + half, w.it.n) + kTKeys - 1) / kTKeys;
+    sg.nt[0] = max(0, min(jb, e0) - sg.ja);
+    sg.nt[1] = w.i * w.it.step + half < w.it.n ? max(0, jb - sg.ja) : 0;
+    if (jb == sg.jhi) {                              // on to the next item
+      if (++w.i == w.it.np) {
+        w.i = 0;
+        if (++w.h == e.c.Hkv) {
+          w.h = 0;
+          do {
+            ++w.b;
+          } while (w.b < e.c.batch && (!load_seq(e, w.b, w.sq) || !seq_ok(e, w.sq)));
+          if (w.b < e.c.batch) w.it = items_of(e, w.sq);
+        }
+      }
+      if (w.b < e.c.batch) w.j = w.it.jlo(w.i) - kItemCost;
+    }
+    if (sg.ja < sg.jb) {
+      sg.slot = 2 * (int)blockIdx.x + (w.index == 0 ? 0 : 1);
+      ++w.index;
+      return true;
+    }
+  }
+  return false;
+}
+
+}  // namespace xt
+
+// -------------------------------------------------------------------- the kernel
+// PS: E4M3 scales differ by page (and head), or pages differ in form.
+template <int D, int VM, bool PS>
+__global__ void __launch_bounds__(kT5Threads, 1)
+extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv16, const __grid_constant__ CUtensorMap tv8,
+                   const ExtTcParams p) {
+  using namespace xt;
+  using C = XT<D, VM>;
+  using Bars = XTBars<D, VM>;
+  constexpr int NK = C::NK, NV = C::NV, NR = C::NR, NM = C::NM, NB = C::NB;
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* base = aligned_smem(sm_raw);
+  uint8_t* sQ = base;                                  // [2][NB][128 rows][128 B]
+  uint8_t* sK = sQ + 2 * C::QB;                        // [NK][16 groups][NB][8 rows][128 B]
+  uint8_t* sV = sK + NK * C::IB;
+  uint8_t* sR = sV + NV * C::IB;                       // [NR][8 pages][16 * D B]
+  Bars* bars = reinterpret_cast<Bars*>(sR + NR * C::RB);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const ExtendParams& e = p.e;
+  const CacheView& c = e.c;
+  griddep_launch_dependents();
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->q_full[t], 1);
+      mbar_init(&bars->q_empty[t], 1);
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t], kTRows / 32);
+      mbar_init(&bars->pv_done[t], 1);
+      mbar_init(&bars->o_free[t], kTRows / 32);
+    }
+    for (int s = 0; s < NK; ++s) mbar_init(&bars->k_full[s], 1), mbar_init(&bars->k_empty[s], 1);
+    for (int s = 0; s < NR; ++s) mbar_init(&bars->raw_full[s], 1), mbar_init(&bars->raw_empty[s], 2);
+    for (int s = 0; s < NV; ++s) mbar_init(&bars->v_full[s], 2), mbar_init(&bars->v_empty[s], 1), mbar_init(&bars->v_dir[s], 1);
+    for (int s = 0; s < NM; ++s) mbar_init(&bars->meta_full[s], 1);
+    mbar_init(&bars->mma_final, 1);
+    bars->abort = 0;
+    bars->st_b = -1;
+    fence_barrier_init();
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    if (VM == kXFP16 || VM == kXMixed) tma_prefetch_desc(&tv16);
+    if (VM == kXE4M3 || VM == kXMixed) tma_prefetch_desc(&tv8);
+  }
+  if (warp == 2) tc05::tmem_alloc(&bars->tmem_base, 512);
+
+  // ---- plan: the blocks of all items, in equal ranges (see the top)
+  auto cost = [&](int b) -> long long {
+    Seq s;
+    if (b >= c.batch || !load_seq(e, b, s) || !seq_ok(e, s)) return 0;
+    const Items it = items_of(e, s);
+    return (long long)it.before(it.np) * c.Hkv;
+  };
+  const int tid = threadIdx.x;
+  long long total = 0;
+  bool fails = false;
+  for (int b = tid; b < c.batch; b += kT5Threads) {
+    total += cost(b);
+    Seq s;
+    if (load_seq(e, b, s) && !seq_ok(e, s)) {
+      fails = true;
+      if (blockIdx.x == 0) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SEQ_LEN, b);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) bars->red[warp] = total;
+  tc05::fence_before_sync();
+  const int any_fails = __syncthreads_or(fails);
+  tc05::fence_after_sync();
+  total = 0;
+  for (int w = 0; w < kT5Threads / 32; ++w) total += bars->red[w];
+  if (any_fails && blockIdx.x == 0) {
+    for (int b = 0; b < c.batch; ++b) {
+      Seq s;
+      if (load_seq(e, b, s) && !seq_ok(e, s)) xs::zero_rows(e, s);
+    }
+  }
+  long long per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < 2) per = 2;
+  const long long start = per * blockIdx.x;
+  const int budget0 = (int)max(0ll, min(per, total - start));
+  // the sequence, head, item and block of position `start`
+  long long carry = 0;
+  for (int b0 = 0; b0 < c.batch && budget0 > 0 && carry <= start; b0 += kT5Threads) {
+    const long long mine = cost(b0 + tid);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();                                   // the last use of red is behind
+    if (lane == 31) bars->red[warp] = incl;
+    __syncthreads();
+    long long before = carry, chunk = 0;
+    for (int w = 0; w < kT5Threads / 32; ++w) {
+      const long long v = bars->red[w];
+      if (w < warp) before += v;
+      chunk += v;
+    }
+    const long long at = start - (before + incl - mine);
+    if (mine > 0 && at >= 0 && at < mine) {
+      Seq s;
+      load_seq(e, b0 + tid, s);
+      const Items it = items_of(e, s);
+      const int each = it.before(it.np);
+      const int h = (int)(at / each), off = (int)(at % each);
+      int lo = 0, hi = it.np - 1;                      // the last item that begins at or before `off`
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (it.before(mid) <= off) lo = mid;
+        else hi = mid - 1;
+      }
+      bars->st_b = b0 + tid;
+      bars->st_h = h;
+      bars->st_i = lo;
+      bars->st_j = it.jlo(lo) - kItemCost + off - it.before(lo);
+    }
+    carry += chunk;
+  }
+  __syncthreads();
+  Walk w;
+  w.b = bars->st_b;
+  w.h = bars->st_h;
+  w.i = bars->st_i;
+  w.j = bars->st_j;
+  w.budget = w.b < 0 ? 0 : budget0;
+  w.index = 0;
+  if (w.budget > 0) {
+    load_seq(e, w.b, w.sq);
+    w.it = items_of(e, w.sq);
+  }
+  const uint32_t tbase = bars->tmem_base;
+  const int TT = kTRows / e.G;                         // tokens of a tile
+  const int h_rows = TT * e.G;
+
+  if (warp == 0) {
+    // -------------------------------------------- producer: Q, page checks, K, raw values
+    int ks = 0, rs = 0, u = 0;
+    uint32_t kph = 0, rph = 0, ql[2] = {0u, 0u};
+    ExtTcSplit split;
+    split.n = 0;
+    bool ok = true;
+    Segment sg;
+    int b = w.b;
+    Seq sq = w.sq;
+    Items it = w.it;
+    while (ok && walk_next(e, w, sg)) {
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (sg.nt[t] == 0) continue;
+        if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(h_rows * D * 2));
+          for (int s = 0; s < NB; ++s)
+            tma_load_5d(sQ + t * C::QB + s * (kTRows * 128), &tq, 0, 0, s, sg.h, sq.q0 + (2 * sg.i + t) * TT, &bars->q_full[t]);
+        }
+        ++ql[t];
+      }
+      if (!ok) break;
+      const int klo = it.lo(sg.i), khi = it.hi(sg.i);
+      const int plo = klo / kPage, phi = (khi + kPage - 1) / kPage;
+      // the ids of a block's pages are fetched a block ahead (their modes and scales depend on them)
+      int id = 0;
+      auto fetch = [&](int j) {
+        const int lp = j * kTPages + lane;
+        id = lane < kTPages && lp >= plo && lp < phi ? __ldg(c.block_table + (size_t)b * c.bt_stride + lp) : 0;
+      };
+      fetch(sg.ja);
+      for (int j = sg.ja; j < sg.jb && ok; ++j, ++u) {
+        const int lp = j * kTPages + lane;
+        const int page = id;
+        const bool in = lane < kTPages && lp >= plo && lp < phi;
+        int flags = xs::kSkip, detail = EKV_DETAIL_NONE;
+        float vs = 1.f;
+        if (in) {
+          flags = VM == kXE4M3 ? xs::kE4 : VM == kXMicro ? xs::kMx : 0;
+          if (page < 0 || page >= c.num_pages) detail = EKV_DETAIL_PAGE_ID;
+          if (!detail && VM == kXMixed) {
+            const int mode = c.page_mode ? (int)__ldg(c.page_mode + page) : c.uniform_mode;
+            flags = mode == EKV_MODE_COMPACT_E4M3 ? xs::kE4 : mode == EKV_MODE_BASE ? xs::kBs : mode == EKV_MODE_MICRO_FP4 ? xs::kMx : 0;
+            if (mode > EKV_MODE_MICRO_FP4) detail = EKV_DETAIL_PAGE_MODE;
+          }
+          if (!detail && (VM == kXE4M3 || VM == kXMixed) && (flags & xs::kE4)) {
+            vs = !c.v_scales ? 0.f : __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)page * c.Hkv + sg.h));
+            if (!scale_ok(vs)) detail = EKV_DETAIL_SCALE;
+          }
+          if (detail) {
+            report_error(c.err, EKV_ERR_DEVICE_CHECK, detail, b);
+            flags = xs::kSkip;
+            vs = 1.f;
+          }
+        }
+        if (j + 1 < sg.jb) fetch(j + 1);
+        const uint32_t bad = __ballot_sync(0xffffffffu, detail != EKV_DETAIL_NONE);
+        const uint32_t loads = __ballot_sync(0xffffffffu, !(flags & xs::kSkip));
+        BlockMeta& mt = bars->meta[u % NM];
+        // K stage first: its wait bounds how far this warp runs ahead, so the description
+        // that block u - NM left is no longer read
+        if (u >= NK) ok = wait_warp(&bars->k_empty[ks], kph ^ 1u, abort);
+        if (!ok) break;
+        if (lane < kTPages) {
+          mt.page[lane] = page;
+          mt.flags[lane] = flags;
+          mt.lsc[lane] = log2f(vs);
+          mt.ivs[lane] = 1.f / vs;
+          if (lane == 0) mt.bad = (int)bad;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->meta_full[u % NM]);
+          mbar_arrive_expect_tx(&bars->k_full[ks], (uint32_t)__popc(loads) * (kPage * D * 2));
+        }
+        __syncwarp();
+        if (!(flags & xs::kSkip))
+          tma_load_5d(sK + ks * C::IB + lane * (2 * C::GB), &tk, 0, 0, 0, 0, page * kPage * c.Hkv + sg.h, &bars->k_full[ks]);
+        if (++ks == NK) {
+          ks = 0;
+          kph ^= 1u;
+        }
+        if (VM != kXFP16) {
+          if (u >= NR) ok = wait_warp(&bars->raw_empty[rs], rph ^ 1u, abort);
+          if (!ok) break;
+          const bool mx = flags & xs::kMx, by = flags & (xs::kE4 | xs::kBs);
+          uint32_t bytes = mx ? micro_head_bytes(D) : by ? kPage * D : 0;
+          uint32_t sum = bytes;
+#pragma unroll
+          for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[rs], sum);
+          __syncwarp();
+          uint8_t* dst = sR + rs * C::RB + lane * (kPage * D);
+          if (mx) bulk_load(dst, c.v_pages + (size_t)page * c.v_page_stride + sg.h * micro_head_bytes(D), bytes, &bars->raw_full[rs]);
+          else if (by) tma_load_4d(dst, &tv8, 0, sg.h, 0, page, &bars->raw_full[rs]);
+          if (++rs == NR) {
+            rs = 0;
+            rph ^= 1u;
+          }
+        }
+      }
+      if (sg.ja == sg.jlo && sg.jb < sg.jhi) {         // the item goes on in later CTAs
+        split.n = 1 + (int)((sg.jhi - sg.jb + per - 1) / per);
+        split.first = sg.slot;
+        split.b = b;
+        split.h = sg.h;
+        split.i = sg.i;
+      }
+      b = w.b;
+      sq = w.sq;
+      it = w.it;
+    }
+    if (!ok && lane == 0) give_up(c.err, abort);
+    if (lane == 0) p.split[blockIdx.x] = split;
+    // the copies still in flight land before the CTA can exit
+    for (int v = max(0, u - NK); v < u; ++v) drain(&bars->k_full[v % NK], (v / NK) & 1);
+    if (VM != kXFP16)
+      for (int v = max(0, u - NR); v < u; ++v) drain(&bars->raw_full[v % NR], (v / NR) & 1);
+    for (int t = 0; t < 2; ++t)
+      if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idS = tc05::idesc_f16_f32(kTRows, kTKeys, false);
+    constexpr uint32_t idO = tc05::idesc_f16_f32(kTRows, D, true);
+    constexpr uint32_t HIQ = tc05::sdesc_hi(1024), HIB = tc05::sdesc_hi(C::GB);
+    const uint32_t q_lo = tc05::sdesc_lo(smem_u32(sQ), 16);
+    const uint32_t k_lo = tc05::sdesc_lo(smem_u32(sK), 16);
+    const uint32_t v_lo = tc05::sdesc_lo(smem_u32(sV), 1024);     // the next 64 columns lie 1024 B on
+    int ks = 0, vst = 0;
+    uint32_t kph = 0, vph = 0;
+    uint32_t qc[2] = {0u, 0u}, pc[2] = {0u, 0u}, oc[2] = {0u, 0u};
+    auto issue_s = [&](int t) {                        // S_t = Q_t K^T from stage ks
+      const uint32_t qa = q_lo + t * (C::QB >> 4), ka = k_lo + ks * (C::IB >> 4);
+      const uint32_t d = tbase + t * 256;
+      if (tc05::elect_one()) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc05::mma_ss(d, tc05::sdesc_join(qa + (((k >> 2) * (kTRows * 128) + (k & 3) * 32) >> 4), HIQ),
+                       tc05::sdesc_join(ka + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), HIB), idS, k > 0);
+        tc05::commit(&bars->s_full[t]);
+      }
+      __syncwarp();
+    };
+    auto commit_one = [&](uint64_t* bar) {
+      if (tc05::elect_one()) tc05::commit(bar);
+      __syncwarp();
+    };
+    bool ok = true;
+    Segment sg;
+    while (ok && walk_next(e, w, sg)) {
+      const int n = sg.jb - sg.ja;
+      ok = wait_warp(&bars->k_full[ks], kph, abort);
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (sg.nt[t] == 0) continue;
+        ok = wait_warp(&bars->q_full[t], qc[t] & 1u, abort);
+        ++qc[t];
+        if (!ok) break;
+        tc05::fence_after_sync();
+        issue_s(t);
+        if (sg.nt[t] == 1) commit_one(&bars->q_empty[t]);
+      }
+      if (!ok) break;
+      commit_one(&bars->k_empty[ks]);
+      if (++ks == NK) ks = 0, kph ^= 1u;
+      for (int j = 0; ok && j < n; ++j) {
+        ok = wait_warp(&bars->v_full[vst], vph, abort);
+        if (!ok) break;
+        tc05::fence_after_sync();
+        const uint32_t va = v_lo + vst * (C::IB >> 4);
+        bool k_ready = false;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (j >= sg.nt[t]) continue;
+          ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
+          ++pc[t];
+          if (ok && j == 0 && oc[t] > 0) ok = wait_warp(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
+          if (!ok) break;
+          tc05::fence_after_sync();
+          const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
+          if (tc05::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kTKeys / 16; ++k)
+              tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2 * C::GB >> 4), HIB), idO, j > 0 || k > 0);
+            if (j + 1 == sg.nt[t]) tc05::commit(&bars->pv_done[t]);
+          }
+          __syncwarp();
+          if (j + 1 < sg.nt[t]) {                      // the next S overwrites P, behind its product
+            ok = k_ready || wait_warp(&bars->k_full[ks], kph, abort);
+            if (!ok) break;
+            k_ready = true;
+            tc05::fence_after_sync();
+            issue_s(t);
+            if (j + 2 == sg.nt[t]) commit_one(&bars->q_empty[t]);
+          }
+        }
+        if (!ok) break;
+        commit_one(&bars->v_empty[vst]);
+        if (++vst == NV) vst = 0, vph ^= 1u;
+        if (j + 1 < n) {
+          commit_one(&bars->k_empty[ks]);
+          if (++ks == NK) ks = 0, kph ^= 1u;
+        }
+      }
+      for (int t = 0; t < 2; ++t)
+        if (sg.nt[t] > 0) ++oc[t];
+    }
+    if (!ok && lane == 0) give_up(c.err, abort);
+    commit_one(&bars->mma_final);
+    if (lane == 0) drain(&bars->mma_final, 0);
+  } else if (warp < 4) {
+    // ----------------------------------------------------------- the V stages
+    int u = 0;
+    uint32_t dir_ph = 0;                               // bit s: parity of v_dir[s]'s next phase
+    const int half = warp - 2;                         // this warp's pages: those of its parity
+    bool ok = true;
+    Segment sg;
+    Items it = w.it;
+    Seq sq = w.sq;
+    int b = w.b;
+    while (ok && walk_next(e, w, sg)) {
+      const int klo = it.lo(sg.i), khi = it.hi(sg.i);
+      for (int j = sg.ja; j < sg.jb && ok; ++j, ++u) {
+        const int vs = u % NV, rs = u % NR;
+        ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
+        if (ok && VM != kXFP16) ok = wait_warp(&bars->raw_full[rs], (uint32_t)(u / NR) & 1u, abort);
+        if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
+        if (!ok) break;
+        const BlockMeta& mt = bars->meta[u % NM];
+        uint8_t* dv = sV + vs * C::IB;
+        const int flags = lane < kTPages ? mt.flags[lane] : xs::kSkip;
+        const int page = lane < kTPages ? mt.page[lane] : 0;
+        const bool dir = VM == kXFP16 ? flags == 0 : VM == kXMixed && flags == 0;
+        const uint32_t dmask = __ballot_sync(0xffffffffu, dir);
+        // keys of the block that no row of the item sees: zero rows, whatever the pages hold
+        const int z0 = max(0, klo - j * kTKeys), z1 = min(kTKeys, khi - j * kTKeys);   // seen: [z0, z1)
+        const bool edge = z0 > 0 || z1 < kTKeys;
+        if (VM == kXFP16 || VM == kXMixed) {
+          if (dmask && half == 0) {
+            uint64_t* bar = edge ? &bars->v_dir[vs] : &bars->v_full[vs];
+            if (lane == 0) {
+              if (edge) mbar_arrive_expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
+              else expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
+            }
+            __syncwarp();
+            if (dir) tma_load_5d(dv + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + sg.h * p.v16_head, bar);
+          }
+        }
+        if (VM != kXFP16) {
+          // 16 codes of one token become two 16-byte chunks; the lanes of the second slab write
+          // theirs in the other order, so that eight lanes never meet in a bank
+          for (int pg = half; pg < kTPages; pg += 2) {
+            const int fl = __shfl_sync(0xffffffffu, flags, pg);
+            if (fl == 0 || (fl & xs::kSkip)) continue;
+            const uint8_t* src = sR + rs * C::RB + pg * (kPage * D);
+#pragma unroll 4
+            for (int x = lane; x < kPage * D / 16; x += 32) {
+              const int t = x / (D / 16), ch = x % (D / 16);
+              uint4 lo, hi;
+              if (fl & xs::kMx) {
+                const uint2 codes = *reinterpret_cast<const uint2*>(src + t * (D / 2) + ch * 8);
+                uint32_t sb = src[micro_scale_off(D) + t * (D / kMicroBlock) + ch / 2];
+                if (!micro_scale_ok(sb)) {
+                  const int key = j * kTKeys + pg * kPage + t;
+                  if (key >= klo && key < khi) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SCALE, b);
+                  sb = 0;
+                }
+                const __half2 s2 = micro_scale_h2(sb);
+                lo = micro_decode8(codes.x, s2);
+                hi = micro_decode8(codes.y, s2);
+              } else {
+                const uint32_t off = D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16);
+                const uint4 q = *reinterpret_cast<const uint4*>(src + off);
+                if (fl & xs::kBs) {
+                  lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
+                                  __byte_perm(q.y, 0u, 0x3424));
+                  hi = make_uint4(__byte_perm(q.z, 0u, 0x1404), __byte_perm(q.z, 0u, 0x3424), __byte_perm(q.w, 0u, 0x1404),
+                                  __byte_perm(q.w, 0u, 0x3424));
+                } else {
+                  lo = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.x)), xs::bits(e4m3x2_to_half2((uint16_t)(q.x >> 16))),
+                                  xs::bits(e4m3x2_to_half2((uint16_t)q.y)), xs::bits(e4m3x2_to_half2((uint16_t)(q.y >> 16))));
+                  hi = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.z)), xs::bits(e4m3x2_to_half2((uint16_t)(q.z >> 16))),
+                                  xs::bits(e4m3x2_to_half2((uint16_t)q.w)), xs::bits(e4m3x2_to_half2((uint16_t)(q.w >> 16))));
+                }
+              }
+              const int c0 = 2 * (ch & 3), slab = ch >> 2, r = t & 7;
+              uint8_t* row = dv + (pg * 2 + (t >> 3)) * C::GB + slab * 1024 + r * 128;
+              const bool swap = slab & 1;
+              *reinterpret_cast<uint4*>(row + ((c0 + (swap ? 1 : 0)) ^ r) * 16) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(row + ((c0 + (swap ? 0 : 1)) ^ r) * 16) = swap ? lo : hi;
+            }
+          }
+          __syncwarp();
+        }
+        if ((VM == kXFP16 || VM == kXMixed) && dmask && edge) {
+          ok = wait_warp(&bars->v_dir[vs], (dir_ph >> vs) & 1u, abort);
+          dir_ph ^= 1u << vs;
+          if (!ok) break;
+        }
+        const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (flags & xs::kSkip));
+        if (edge || smask) {
+          for (int x = lane; x < kTKeys / 2 * (D / 8); x += 32) {
+            const int pg = half + 2 * (x / (kPage * (D / 8))), t = x / (D / 8) % kPage, ch = x % (D / 8);
+            const int key = pg * kPage + t;
+            if (key < z0 || key >= z1 || ((smask >> pg) & 1u))
+              *reinterpret_cast<uint4*>(dv + (key >> 3) * C::GB + (ch >> 3) * 1024 + (key & 7) * 128 + (ch & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        fence_async();                                 // written for the MMAs; the raw bytes read for their refill
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->v_full[vs]);
+          if (VM != kXFP16) mbar_arrive(&bars->raw_empty[rs]);
+        }
+      }
+      it = w.it;
+      sq = w.sq;
+      b = w.b;
+    }
+    if (!ok && lane == 0) give_up(c.err, abort);
+    // direct copies in flight (a V stage whose product never came is drained here)
+    if (VM == kXFP16 || VM == kXMixed)
+      for (int v = max(0, u - NV); v < u; ++v) drain(&bars->v_full[v % NV], (uint32_t)(v / NV) & 1u);
+  } else {
+    // ------------------------------------------------------- softmax, tile t
+    const int t = (warp - 4) >> 2, r = threadIdx.x - 128 - t * kTRows;
+    const uint32_t lanebase = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float qs = e.qscale;
+    const float osc = p.scale_ptr ? __ldg(p.scale_ptr) : 1.f;   // one E4M3 scale for every code
+    const uint32_t t_s = tbase + t * 256 + lanebase, t_o = tbase + t * 256 + 128 + lanebase;
+    uint32_t sc = 0, pvc = 0;
+    int u = 0;
+    bool ok = true;
+    Segment sg;
+    Items it = w.it;
+    Seq sq = w.sq;
+    const int tok_t = r / e.G, g = r % e.G;            // this thread's token within the tile, and head
+    while (ok && walk_next(e, w, sg)) {
+      const int nmine = sg.nt[t], u0 = u;
+      u += sg.jb - sg.ja;
+      const int first = (2 * sg.i + t) * TT;           // the tile's first token
+      const int tok = first + tok_t;
+      const bool valid = tok_t < TT && tok < it.n;
+      const int pos = it.t0 + tok, lo = max(pos - e.window, -1);   // keys lo + 1 .. pos
+      // keys that every valid row sees: from the last row's window start to the first row's own
+      const int all_lo = it.t0 + min(first + TT, it.n) - 1 - e.window, all_hi = it.t0 + first;
+      float m_ref = -INFINITY, l = 0.f;
+      bool bad = false;
+      for (int jj = 0; jj < nmine; ++jj) {
+        ok = wait_warp(&bars->s_full[t], sc & 1u, abort);
+        ++sc;
+        if (ok) ok = wait_warp(&bars->meta_full[(u0 + jj) % NM], (uint32_t)((u0 + jj) / NM) & 1u, abort);
+        if (!ok) break;
+        tc05::fence_after_sync();
+        const BlockMeta& mt = bars->meta[(u0 + jj) % NM];
+        const int k0 = (sg.ja + jj) * kTKeys;
+        const int badp = mt.bad;
+        uint32_t a[4][32];
+        tc05::ld32(t_s, a[0]);
+        tc05::ld32(t_s + 32, a[1]);
+        tc05::ld32(t_s + 64, a[2]);
+        tc05::ld32(t_s + 96, a[3]);
+        tc05::wait_ld();
+        if (k0 + kTKeys - 1 > all_hi || k0 <= all_lo || badp) {
+          const int hi_c = pos - k0, lo_c = lo - k0;
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4)
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (32 * c4 + x > hi_c || 32 * c4 + x <= lo_c) a[c4][x] = __float_as_uint(-INFINITY);
+          if (badp) {
+            for (int pg = 0; pg < kTPages; ++pg)
+              if (((badp >> pg) & 1) && pg * kPage <= hi_c && pg * kPage + kPage - 1 > lo_c) bad = true;
+          }
+        }
+        // the row's maximum, in log2 units
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {
+          float m8[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* y = a[c4] + 8 * q;
+            m8[q] = fmaxf(max3(max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2])),
+                               __uint_as_float(y[3]), __uint_as_float(y[4])),
+                          max3(__uint_as_float(y[5]), __uint_as_float(y[6]), __uint_as_float(y[7])));
+          }
+          if (PS) {
+            mx = max3(mx, fmaf(fmaxf(m8[0], m8[1]), qs, mt.lsc[2 * c4]), fmaf(fmaxf(m8[2], m8[3]), qs, mt.lsc[2 * c4 + 1]));
+          } else {
+            mx = max3(mx, max3(m8[0], m8[1], m8[2]), m8[3]);
+          }
+        }
+        if (!PS) mx *= qs;
+        const float m_new = fmaxf(m_ref, mx);
+        const bool need = m_new > m_ref + 8.f;
+        if (__any_sync(0xffffffffu, need)) {
+          const float alpha = need ? xs::ex2(m_ref - m_new) : 1.f;
+          if (jj > 0) {
+#pragma unroll 1
+            for (int x = 0; x < D / 16; ++x) {
+              uint32_t o[16];
+              tld16(t_o + 16 * x, o);
+              tc05::wait_ld();
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
+              tst16(t_o + 16 * x, o);
+            }
+          }
+          l *= alpha;
+          if (need) m_ref = m_new;
+        }
+        // a row that has seen no key yet keeps m = -inf: its weights are 2^-inf = 0
+        const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+#pragma unroll
+        for (int c4 = 0; c4 < 4; ++c4) {
+#pragma unroll
+          for (int pg = 0; pg < 2; ++pg) {
+            const float add = PS ? nm + mt.lsc[2 * c4 + pg] : nm;
+            float la[2] = {0.f, 0.f}, lb[2] = {0.f, 0.f};
+#pragma unroll
+            for (int x = 8 * pg; x < 8 * pg + 8; ++x) {
+              float a0, a1;
+              ffma2(a0, a1, __uint_as_float(a[c4][2 * x]), __uint_as_float(a[c4][2 * x + 1]), qs, add);
+              const float p0 = xs::ex2(a0), p1 = xs::ex2(a1);
+              fadd2(la[x & 1], lb[x & 1], p0, p1);
+              a[c4][x] = pack2(p0, p1);
+            }
+            fadd2(la[0], lb[0], la[1], lb[1]);
+            l = PS ? fmaf(la[0] + lb[0], mt.ivs[2 * c4 + pg], l) : l + (la[0] + lb[0]);
+          }
+          tst16(t_s + 16 * c4, &a[c4][0]);
+        }
+        tc05::wait_st();
+        tc05::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[t]);
+      }
+      if (!ok) break;
+      const size_t prow = (size_t)sg.slot * (2 * kTRows) + t * kTRows + r;
+      if (nmine == 0) {
+        if (!sg.whole && valid) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
+        it = w.it;
+        sq = w.sq;
+        continue;
+      }
+      ok = wait_warp(&bars->pv_done[t], pvc & 1u, abort);
+      ++pvc;
+      if (!ok) break;
+      tc05::fence_after_sync();
+      const bool none = bad || !(l > 0.f);
+      const float inv = none ? 0.f : osc / l;
+      const size_t orow = (size_t)(sq.q0 + tok) * c.Hq + sg.h * e.G + g;
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t o[32];
+        tc05::ld32(t_o + 32 * x, o);
+        tc05::wait_ld();
+        if (x == D / 32 - 1) {                         // O is read out: the next item may overwrite it
+          tc05::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->o_free[t]);
+        }
+        if (valid && sg.whole) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            uint4 q;
+            q.x = pack2(__uint_as_float(o[8 * y + 0]) * inv, __uint_as_float(o[8 * y + 1]) * inv);
+            q.y = pack2(__uint_as_float(o[8 * y + 2]) * inv, __uint_as_float(o[8 * y + 3]) * inv);
+            q.z = pack2(__uint_as_float(o[8 * y + 4]) * inv, __uint_as_float(o[8 * y + 5]) * inv);
+            q.w = pack2(__uint_as_float(o[8 * y + 6]) * inv, __uint_as_float(o[8 * y + 7]) * inv);
+            if (none) q = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(e.out + orow * D + 32 * x + 8 * y) = q;
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            *reinterpret_cast<uint4*>(p.part_acc + prow * D + 32 * x + 4 * y) =
+                make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        }
+      }
+      if (valid) {
+        if (!sg.whole) p.part_ml[prow] = make_float2(m_ref, bad ? kBadRecord : l);
+        else if (e.lse) e.lse[orow] = none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+      }
+      it = w.it;
+      sq = w.sq;
+    }
+    if (!ok && lane == 0) give_up(c.err, abort);
+  }
+  tc05::fence_before_sync();
+  __syncthreads();
+  if (warp == 2) {
+    tc05::fence_after_sync();
+    tc05::tmem_free(tbase, 512);
+  }
+}
+
+// Joins the items that crossed CTAs: block (x, y) takes rows 32 y .. 32 y + 31 of the item that
+// begins in CTA x and ends in a later one, a warp per row.
+template <int D>
+__global__ void __launch_bounds__(256)
+extend_join_kernel(const ExtTcParams p) {
+  griddep_wait();
+  const ExtTcSplit s = p.split[blockIdx.x];
+  if (s.n == 0) return;
+  const ExtendParams& e = p.e;
+  const int lane = threadIdx.x & 31;
+  xs::Seq sq;
+  xs::load_seq(e, s.b, sq);
+  const int TT = kTRows / e.G;
+  const float osc = p.scale_ptr ? __ldg(p.scale_ptr) : 1.f;
+  constexpr int C = D / 32;
+  for (int x = threadIdx.x >> 5; x < 32; x += 8) {
+    const int row = blockIdx.y * 32 + x, t = row / kTRows, r = row % kTRows;
+    const int tok = (2 * s.i + t) * TT + r / e.G;
+    if (r >= TT * e.G || tok >= sq.n) continue;
+    auto at = [&](int i) { return (size_t)(i == 0 ? s.first : 2 * ((int)blockIdx.x + i)) * (2 * kTRows) + row; };
+    // weights, 32 records at a time with a running maximum (the sums as everywhere)
+    float M = -INFINITY, L = 0.f, acc[C];
+    bool bad = false;
+#pragma unroll
+    for (int y = 0; y < C; ++y) acc[y] = 0.f;
+    for (int i0 = 0; i0 < s.n; i0 += 32) {
+      const float2 ml = i0 + lane < s.n ? p.part_ml[at(i0 + lane)] : make_float2(-INFINITY, 0.f);
+      bad |= ml.y < 0.f;
+      float mx = ml.y > 0.f ? ml.x : -INFINITY;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(M, mx);
+      const float a = mn == -INFINITY ? 1.f : exp2f(M - mn);
+      const float w = ml.y > 0.f ? exp2f(ml.x - mn) : 0.f;
+      float li = w * fmaxf(ml.y, 0.f);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) li += __shfl_xor_sync(0xffffffffu, li, o);
+      L = fmaf(L, a, li);
+      M = mn;
+#pragma unroll
+      for (int y = 0; y < C; ++y) acc[y] *= a;
+      const int n = min(32, s.n - i0);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        if (wi > 0.f) {
+          const float* src = p.part_acc + at(i0 + i) * D + lane * C;
+#pragma unroll
+          for (int y = 0; y < C; ++y) acc[y] = fmaf(wi, src[y], acc[y]);
+        }
+      }
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    const size_t o = (size_t)(sq.q0 + tok) * e.c.Hq + s.h * e.G + r % e.G;
+    const bool none = bad || !(L > 0.f);
+    const float inv = none ? 0.f : osc / L;
+#pragma unroll
+    for (int y = 0; y < C; y += 2)
+      *reinterpret_cast<__half2*>(e.out + o * D + lane * C + y) =
+          none ? __floats2half2_rn(0.f, 0.f) : __floats2half2_rn(acc[y] * inv, acc[y + 1] * inv);
+    if (lane == 0 && e.lse) e.lse[o] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+  }
+}
+
+// ------------------------------------------------------------------------- host
+// FP16 page slices of one KV head as 8-token groups: 5-D view (d mod 64, t mod 8, d / 64, t / 8, place) of
+// an fp16 pool, `place` counting `unit` bytes, so that one coordinate names page and head; the
+// box {64, 8, D / 64, 2, 1} lands as [2][D / 64][8][128 B].
+inline bool encode_group_map(CUtensorMap* tm, const void* base, int D, int Hkv, unsigned long long places, int unit) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t row = (cuuint64_t)Hkv * D * 2;
+  cuuint64_t dims[5] = {64, 8, (cuuint64_t)(D / 64), 2, (cuuint64_t)places};
+  cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)unit};
+  cuuint32_t box[5] = {64, 8, (cuuint32_t)(D / 64), 2, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query rows: 5-D view (d mod 64, g, d / 64, KV head, token) of q [T][Hq][D]; the box {64, G, 1, 1, TT}
+// lands TT * G rows of 128 B, row = token * G + g. Tokens past T read as zeros.
+inline bool encode_query_map(CUtensorMap* tm, const void* q, int D, int Hkv, int G, int T) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[5] = {64, (cuuint64_t)G, (cuuint64_t)(D / 64), (cuuint64_t)Hkv, (cuuint64_t)T};
+  cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)G * D * 2, (cuuint64_t)Hkv * G * D * 2};
+  cuuint32_t box[5] = {64, (cuuint32_t)G, 1, 1, (cuuint32_t)(kTRows / G)};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct ExtTcMaps {
+  CUtensorMap q, k, v16, v8;
+};
+
+template <int D, int VM, bool PS>
+cudaError_t launch_ext_tc(const ExtTcMaps& m, const ExtTcParams& p, int grid, cudaStream_t st) {
+  auto kern = extend_tc05_kernel<D, VM, PS>;
+  constexpr int smem = xt_smem_bytes<D, VM>();
+  static_assert(smem <= 232448, "shared memory of one CTA");
+  cudaError_t err = set_smem_attr(reinterpret_cast<const void*>(kern), smem);
+  if (err != cudaSuccess) return err;
+  kern<<<grid, kT5Threads, smem, st>>>(m.q, m.k, m.v16, m.v8, p);
+  if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 2 * kTRows / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, extend_join_kernel<D>, p);
+}
+
+template <int D>
+cudaError_t launch_ext_tc_d(const ExtTcMaps& m, const ExtTcParams& p, int vm, int grid, cudaStream_t st) {
+  switch (vm) {
+    case kXFP16: return launch_ext_tc<D, kXFP16, false>(m, p, grid, st);
+    case kXE4M3:
+      return p.scale_ptr ? launch_ext_tc<D, kXE4M3, false>(m, p, grid, st) : launch_ext_tc<D, kXE4M3, true>(m, p, grid, st);
+    case kXMicro: return launch_ext_tc<D, kXMicro, false>(m, p, grid, st);
+    default: return launch_ext_tc<D, kXMixed, true>(m, p, grid, st);
+  }
+}
+
+}  // namespace ekv
