@@ -702,7 +702,7 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
                  : uniform_mode == EKV_MODE_COMPACT_E4M3    ? kXE4M3
                                                             : kXMicro;
   cudaError_t e;
-  if ((long long)p.G * max_q <= kXRows) {          // few query rows: the stream over the cache
+  if ((long long)p.G * max_q <= (getenv("EKV_SPLIT") ? kXRows : 0)) {          // few query rows: the stream over the cache
     const int map_mode = vm == kXMixed ? kVMixed : vm == kXE4M3 ? kVE4M3 : kVFP16;
     CUtensorMap tm[3];
     // (a microscaled pool has small slots: no map over its values)
@@ -728,6 +728,8 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
     x.part_acc = c->ext_acc;
     x.part_ml = c->ext_ml;
     x.split = c->ext_split;
+    const long long rows = (long long)p.G * max_q;
+    x.nw = max_q <= kTRows / p.G ? (int)((rows + 31) / 32) : 0;
     if (vm == kXE4M3 && scale_mode == EKV_SCALE_PER_TENSOR) x.scale_ptr = v_scales;
     // one coordinate for (page, head): in units that divide both the page stride and a head's row
     int unit = 2 * D;

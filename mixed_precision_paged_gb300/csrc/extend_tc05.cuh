@@ -38,7 +38,7 @@ constexpr int kItemCost = 1;                // an item's start (query load, epil
 
 struct ExtTcSplit {                         // an item that crosses CTAs, for the joining kernel
   int n;                                    // CTAs it spans; 0: none
-  int first;                                // its first slot; the others are 2 * (cta + 1), ...
+  int first;                                // its first slot; the others are 2 * (cta + H_kv), ...
   int b, h, i;
 };
 
@@ -48,33 +48,38 @@ struct ExtTcParams {
   float2* part_ml;                          // [2 * grid][256]
   ExtTcSplit* split;                        // [grid]
   const float* scale_ptr;                   // one E4M3 scale for every code (it scales the output), or null
+  int nw;                                   // ALT: softmax warps of a stream, for rows below 32 * nw
   int v16_mul, v16_head;                    // FP16 value map: index = page * v16_mul + head * v16_head
 };
 
-template <int D, int VM>
+template <int D, int VM, bool ALT>
 struct XT {
   static constexpr int NB = D / 64;                    // 64-value slabs of a row
   static constexpr int GB = NB * 1024;                 // bytes of an 8-token group
   static constexpr int QB = kTRows * D * 2;            // a query tile
   static constexpr int IB = kTKeys * D * 2;            // a K or V block
   static constexpr int RB = VM == kXFP16 ? 0 : kTKeys * D;   // a raw block: a page at every 16 * D bytes
-  static constexpr int NK = VM == kXFP16 ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 4);
-  static constexpr int NV = D == 128 ? 2 : 4;
+  static constexpr int NQ = ALT ? 1 : 2;               // query tiles
+  static constexpr int NK = (VM == kXFP16 || ALT ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 4)) + (ALT && D == 64 ? 1 : 0);
+  static constexpr int NV = (D == 128 ? 2 : 4) + (ALT && VM == kXFP16 ? 1 : 0);
   static constexpr int NR = D == 128 ? 2 : 4;
-  static constexpr int NM = 8;                         // block descriptions; at least NK + 1
+  // block descriptions. The producer writes one once the K stage NK blocks back is free, so once
+  // that block's S is issued, which is behind the product of the block before (ALT: two before)
+  static constexpr int NM = D == 128 ? (ALT ? 5 : 4) : 8;
+  static_assert(NM >= NK + (ALT ? 2 : 1), "a description is read until its block's weights are handed over");
 };
 
 struct BlockMeta {
   int page[kTPages];
-  int flags[kTPages];                       // xs::kSkip: not loaded
   float lsc[kTPages];                       // log2 of the scale
   float ivs[kTPages];                       // and its reciprocal
   int bad;                                  // bit per page that failed its checks
+  uint8_t flags[kTPages];                   // xs::kSkip: not loaded
 };
 
-template <int D, int VM>
+template <int D, int VM, bool ALT>
 struct XTBars {
-  using C = XT<D, VM>;
+  using C = XT<D, VM, ALT>;
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[C::NK], k_empty[C::NK];
   uint64_t raw_full[C::NR], raw_empty[C::NR];
@@ -83,17 +88,19 @@ struct XTBars {
   uint64_t meta_full[C::NM];
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t mma_final;
+  uint64_t x_full[2];                       // ALT: a stream's (m, l) of the segment posted
+  float2 xch[2][ALT ? kTRows : 1];
   BlockMeta meta[C::NM];
   long long red[kT5Threads / 32];
-  int st_b, st_h, st_i, st_j;               // where this CTA's range begins
+  int st_b, st_i, st_j;               // where this CTA's range begins
   uint32_t tmem_base;
   int abort;
 };
 
-template <int D, int VM>
+template <int D, int VM, bool ALT>
 constexpr int xt_smem_bytes() {
-  using C = XT<D, VM>;
-  return 1024 + 2 * C::QB + C::NK * C::IB + C::NV * C::IB + C::NR * C::RB + (int)sizeof(XTBars<D, VM>);
+  using C = XT<D, VM, ALT>;
+  return C::NQ * C::QB + C::NK * C::IB + C::NV * C::IB + C::NR * C::RB + (int)sizeof(XTBars<D, VM, ALT>);
 }
 
 namespace xt {
@@ -211,12 +218,13 @@ struct Items {
     return s;
   }
 };
+template <bool ALT>
 __device__ __forceinline__ Items items_of(const ExtendParams& e, const Seq& s) {
   Items it;
   it.L = s.L;
   it.n = s.n;
   it.t0 = s.L - s.n;
-  it.step = 2 * (kTRows / e.G);
+  it.step = (ALT ? 1 : 2) * (kTRows / e.G);
   it.np = (s.n + it.step - 1) / it.step;
   it.window = e.window;
   return it;
@@ -224,7 +232,7 @@ __device__ __forceinline__ Items items_of(const ExtendParams& e, const Seq& s) {
 
 // A walk over this CTA's segments; every role makes the same one.
 struct Walk {
-  int b, h, i, j;           // next: sequence, KV head, item, block (j may lie kItemCost before the item's first)
+  int b, i, j;              // next: sequence, item, block (j may lie kItemCost before the item's first)
   int budget;               // blocks left in the CTA's range
   int index;                // segments so far
   Seq sq;
@@ -233,16 +241,16 @@ struct Walk {
 struct Segment {
   int ja, jb;               // blocks
   int jlo, jhi;             // of the whole item
-  int h, i, slot;
+  int i, slot;
   int nt[2];                // blocks that each tile takes part in, from ja on
   bool whole;
 };
 
+template <bool ALT>
 __device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segment& sg) {
   while (w.budget > 0 && w.b < e.c.batch) {
     sg.jlo = w.it.jlo(w.i);
     sg.jhi = w.it.jhi(w.i);
-    sg.h = w.h;
     sg.i = w.i;
     const int ja = w.j, jb = min(sg.jhi, w.j + w.budget);
     w.budget -= jb - ja;
@@ -250,21 +258,22 @@ __device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segmen
     sg.ja = max(ja, sg.jlo);
     sg.jb = jb;
     sg.whole = sg.ja == sg.jlo && jb == sg.jhi;
-    // tile 0 ends with its own last token's block
-    const int half = w.it.step / 2;
-    const int e0 = (w.it.t0 + min(w.i * w.it.step + half, w.it.n) + kTKeys - 1) / kTKeys;
-    sg.nt[0] = max(0, min(jb, e0) - sg.ja);
-    sg.nt[1] = w.i * w.it.step + half < w.it.n ? max(0, jb - sg.ja) : 0;
+    if (ALT) {                                       // one tile, its blocks in turn
+      sg.nt[0] = (jb - sg.ja + 1) / 2;
+      sg.nt[1] = (jb - sg.ja) / 2;
+    } else {                                         // tile 0 ends with its own last token's block
+      const int half = w.it.step / 2;
+      const int e0 = (w.it.t0 + min(w.i * w.it.step + half, w.it.n) + kTKeys - 1) / kTKeys;
+      sg.nt[0] = max(0, min(jb, e0) - sg.ja);
+      sg.nt[1] = w.i * w.it.step + half < w.it.n ? max(0, jb - sg.ja) : 0;
+    }
     if (jb == sg.jhi) {                              // on to the next item
       if (++w.i == w.it.np) {
         w.i = 0;
-        if (++w.h == e.c.Hkv) {
-          w.h = 0;
-          do {
-            ++w.b;
-          } while (w.b < e.c.batch && (!load_seq(e, w.b, w.sq) || !seq_ok(e, w.sq)));
-          if (w.b < e.c.batch) w.it = items_of(e, w.sq);
-        }
+        do {
+          ++w.b;
+        } while (w.b < e.c.batch && (!load_seq(e, w.b, w.sq) || !seq_ok(e, w.sq)));
+        if (w.b < e.c.batch) w.it = items_of<ALT>(e, w.sq);
       }
       if (w.b < e.c.batch) w.j = w.it.jlo(w.i) - kItemCost;
     }
@@ -280,20 +289,20 @@ __device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segmen
 }  // namespace xt
 
 // -------------------------------------------------------------------- the kernel
-// PS: E4M3 scales differ by page (and head), or pages differ in form.
-template <int D, int VM, bool PS>
+// PS: E4M3 scales differ by page (and head), or pages differ in form. ALT: every sequence's rows fit
+// one tile; its key blocks alternate between the two softmax groups ("streams").
+template <int D, int VM, bool PS, bool ALT>
 __global__ void __launch_bounds__(kT5Threads, 1)
 extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv16, const __grid_constant__ CUtensorMap tv8,
                    const ExtTcParams p) {
   using namespace xt;
-  using C = XT<D, VM>;
-  using Bars = XTBars<D, VM>;
+  using C = XT<D, VM, ALT>;
+  using Bars = XTBars<D, VM, ALT>;
   constexpr int NK = C::NK, NV = C::NV, NR = C::NR, NM = C::NM, NB = C::NB;
-  extern __shared__ uint8_t sm_raw[];
-  uint8_t* base = aligned_smem(sm_raw);
-  uint8_t* sQ = base;                                  // [2][NB][128 rows][128 B]
-  uint8_t* sK = sQ + 2 * C::QB;                        // [NK][16 groups][NB][8 rows][128 B]
+  extern __shared__ __align__(1024) uint8_t sm_1k[];   // (no room to align by hand)
+  uint8_t* sQ = sm_1k;                                  // [2][NB][128 rows][128 B]
+  uint8_t* sK = sQ + C::NQ * C::QB;                        // [NK][16 groups][NB][8 rows][128 B]
   uint8_t* sV = sK + NK * C::IB;
   uint8_t* sR = sV + NV * C::IB;                       // [NR][8 pages][16 * D B]
   Bars* bars = reinterpret_cast<Bars*>(sR + NR * C::RB);
@@ -302,19 +311,32 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   const ExtendParams& e = p.e;
   const CacheView& c = e.c;
   griddep_launch_dependents();
+  if (smem_u32(sm_1k) & 1023u) {                       // the swizzled layouts would not hold
+    if (threadIdx.x == 0) {
+      report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_TIMEOUT, -2);
+      p.split[blockIdx.x].n = 0;
+    }
+    return;
+  }
+  // softmax warps per tile (ALT: those with rows), and the warps that make the V stages
+  const int nw = ALT ? p.nw : kTRows / 32;
+  const int nvw = 2 + 2 * (4 - nw);
+  const bool idle = ALT && warp >= 4 && (warp & 3) >= nw;
+  const int vi = warp < 4 ? warp - 2 : 2 + (warp >> 2 == 1 ? 0 : 4 - nw) + (warp & 3) - nw;   // index among the latter
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->q_full[t], 1);
       mbar_init(&bars->q_empty[t], 1);
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_full[t], kTRows / 32);
+      mbar_init(&bars->p_full[t], nw);
       mbar_init(&bars->pv_done[t], 1);
-      mbar_init(&bars->o_free[t], kTRows / 32);
+      mbar_init(&bars->o_free[t], ALT ? 2 * nw : nw);
+      mbar_init(&bars->x_full[t], nw);
     }
     for (int s = 0; s < NK; ++s) mbar_init(&bars->k_full[s], 1), mbar_init(&bars->k_empty[s], 1);
-    for (int s = 0; s < NR; ++s) mbar_init(&bars->raw_full[s], 1), mbar_init(&bars->raw_empty[s], 2);
-    for (int s = 0; s < NV; ++s) mbar_init(&bars->v_full[s], 2), mbar_init(&bars->v_empty[s], 1), mbar_init(&bars->v_dir[s], 1);
+    for (int s = 0; s < NR; ++s) mbar_init(&bars->raw_full[s], 1), mbar_init(&bars->raw_empty[s], nvw);
+    for (int s = 0; s < NV; ++s) mbar_init(&bars->v_full[s], nvw), mbar_init(&bars->v_empty[s], 1), mbar_init(&bars->v_dir[s], 1);
     for (int s = 0; s < NM; ++s) mbar_init(&bars->meta_full[s], 1);
     mbar_init(&bars->mma_final, 1);
     bars->abort = 0;
@@ -331,8 +353,8 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   auto cost = [&](int b) -> long long {
     Seq s;
     if (b >= c.batch || !load_seq(e, b, s) || !seq_ok(e, s)) return 0;
-    const Items it = items_of(e, s);
-    return (long long)it.before(it.np) * c.Hkv;
+    const Items it = items_of<ALT>(e, s);
+    return it.before(it.np);
   };
   const int tid = threadIdx.x;
   long long total = 0;
@@ -359,9 +381,12 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       if (load_seq(e, b, s) && !seq_ok(e, s)) xs::zero_rows(e, s);
     }
   }
-  long long per = (total + gridDim.x - 1) / gridDim.x;
+  // CTA x works on KV head x mod H_kv and range x / H_kv: the heads of a page are read at about the
+  // same time
+  const int ranges = (int)gridDim.x / c.Hkv, h = (int)blockIdx.x % c.Hkv;
+  long long per = (total + ranges - 1) / ranges;
   if (per < 2) per = 2;
-  const long long start = per * blockIdx.x;
+  const long long start = (int)blockIdx.x / c.Hkv < ranges ? per * ((int)blockIdx.x / c.Hkv) : total;
   const int budget0 = (int)max(0ll, min(per, total - start));
   // the sequence, head, item and block of position `start`
   long long carry = 0;
@@ -386,9 +411,8 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     if (mine > 0 && at >= 0 && at < mine) {
       Seq s;
       load_seq(e, b0 + tid, s);
-      const Items it = items_of(e, s);
-      const int each = it.before(it.np);
-      const int h = (int)(at / each), off = (int)(at % each);
+      const Items it = items_of<ALT>(e, s);
+      const int off = (int)at;
       int lo = 0, hi = it.np - 1;                      // the last item that begins at or before `off`
       while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -396,7 +420,6 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         else hi = mid - 1;
       }
       bars->st_b = b0 + tid;
-      bars->st_h = h;
       bars->st_i = lo;
       bars->st_j = it.jlo(lo) - kItemCost + off - it.before(lo);
     }
@@ -405,14 +428,13 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   __syncthreads();
   Walk w;
   w.b = bars->st_b;
-  w.h = bars->st_h;
   w.i = bars->st_i;
   w.j = bars->st_j;
   w.budget = w.b < 0 ? 0 : budget0;
   w.index = 0;
   if (w.budget > 0) {
     load_seq(e, w.b, w.sq);
-    w.it = items_of(e, w.sq);
+    w.it = items_of<ALT>(e, w.sq);
   }
   const uint32_t tbase = bars->tmem_base;
   const int TT = kTRows / e.G;                         // tokens of a tile
@@ -429,15 +451,15 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     int b = w.b;
     Seq sq = w.sq;
     Items it = w.it;
-    while (ok && walk_next(e, w, sg)) {
-      for (int t = 0; t < 2 && ok; ++t) {
+    while (ok && walk_next<ALT>(e, w, sg)) {
+      for (int t = 0; t < C::NQ && ok; ++t) {
         if (sg.nt[t] == 0) continue;
         if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(h_rows * D * 2));
           for (int s = 0; s < NB; ++s)
-            tma_load_5d(sQ + t * C::QB + s * (kTRows * 128), &tq, 0, 0, s, sg.h, sq.q0 + (2 * sg.i + t) * TT, &bars->q_full[t]);
+            tma_load_5d(sQ + t * C::QB + s * (kTRows * 128), &tq, 0, 0, s, h, sq.q0 + (C::NQ * sg.i + t) * TT, &bars->q_full[t]);
         }
         ++ql[t];
       }
@@ -466,7 +488,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (mode > EKV_MODE_MICRO_FP4) detail = EKV_DETAIL_PAGE_MODE;
           }
           if (!detail && (VM == kXE4M3 || VM == kXMixed) && (flags & xs::kE4)) {
-            vs = !c.v_scales ? 0.f : __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)page * c.Hkv + sg.h));
+            vs = !c.v_scales ? 0.f : __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)page * c.Hkv + h));
             if (!scale_ok(vs)) detail = EKV_DETAIL_SCALE;
           }
           if (detail) {
@@ -485,7 +507,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (!ok) break;
         if (lane < kTPages) {
           mt.page[lane] = page;
-          mt.flags[lane] = flags;
+          mt.flags[lane] = (uint8_t)flags;
           mt.lsc[lane] = log2f(vs);
           mt.ivs[lane] = 1.f / vs;
           if (lane == 0) mt.bad = (int)bad;
@@ -497,7 +519,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         __syncwarp();
         if (!(flags & xs::kSkip))
-          tma_load_5d(sK + ks * C::IB + lane * (2 * C::GB), &tk, 0, 0, 0, 0, page * kPage * c.Hkv + sg.h, &bars->k_full[ks]);
+          tma_load_5d(sK + ks * C::IB + lane * (2 * C::GB), &tk, 0, 0, 0, 0, page * kPage * c.Hkv + h, &bars->k_full[ks]);
         if (++ks == NK) {
           ks = 0;
           kph ^= 1u;
@@ -513,8 +535,8 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[rs], sum);
           __syncwarp();
           uint8_t* dst = sR + rs * C::RB + lane * (kPage * D);
-          if (mx) bulk_load(dst, c.v_pages + (size_t)page * c.v_page_stride + sg.h * micro_head_bytes(D), bytes, &bars->raw_full[rs]);
-          else if (by) tma_load_4d(dst, &tv8, 0, sg.h, 0, page, &bars->raw_full[rs]);
+          if (mx) bulk_load(dst, c.v_pages + (size_t)page * c.v_page_stride + h * micro_head_bytes(D), bytes, &bars->raw_full[rs]);
+          else if (by) tma_load_4d(dst, &tv8, 0, h, 0, page, &bars->raw_full[rs]);
           if (++rs == NR) {
             rs = 0;
             rph ^= 1u;
@@ -525,7 +547,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         split.n = 1 + (int)((sg.jhi - sg.jb + per - 1) / per);
         split.first = sg.slot;
         split.b = b;
-        split.h = sg.h;
+        split.h = h;
         split.i = sg.i;
       }
       b = w.b;
@@ -552,7 +574,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     uint32_t kph = 0, vph = 0;
     uint32_t qc[2] = {0u, 0u}, pc[2] = {0u, 0u}, oc[2] = {0u, 0u};
     auto issue_s = [&](int t) {                        // S_t = Q_t K^T from stage ks
-      const uint32_t qa = q_lo + t * (C::QB >> 4), ka = k_lo + ks * (C::IB >> 4);
+      const uint32_t qa = q_lo + (ALT ? 0 : t) * (C::QB >> 4), ka = k_lo + ks * (C::IB >> 4);
       const uint32_t d = tbase + t * 256;
       if (tc05::elect_one()) {
 #pragma unroll
@@ -569,8 +591,46 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     };
     bool ok = true;
     Segment sg;
-    while (ok && walk_next(e, w, sg)) {
+    while (ok && walk_next<ALT>(e, w, sg)) {
       const int n = sg.jb - sg.ja;
+      if (ALT) {
+        // block j belongs to stream j mod 2: O_t += P_t V_j, then S_t of block j + 2 over P_t
+        auto issue_next = [&](int j) {                 // S of block j
+          ok = wait_warp(&bars->k_full[ks], kph, abort);
+          if (!ok) return;
+          tc05::fence_after_sync();
+          issue_s(j & 1);
+          commit_one(&bars->k_empty[ks]);
+          if (++ks == NK) ks = 0, kph ^= 1u;
+          if (j == n - 1) commit_one(&bars->q_empty[0]);
+        };
+        ok = wait_warp(&bars->q_full[0], qc[0] & 1u, abort);
+        ++qc[0];
+        for (int j = 0; j < min(n, 2) && ok; ++j) issue_next(j);
+        for (int j = 0; ok && j < n; ++j) {
+          const int t = j & 1;
+          ok = wait_warp(&bars->v_full[vst], vph, abort);
+          if (ok) ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
+          ++pc[t];
+          // the last segment's O is read out by both streams together
+          if (ok && j == 0 && oc[0] > 0) ok = wait_warp(&bars->o_free[0], (oc[0] - 1u) & 1u, abort);
+          if (!ok) break;
+          tc05::fence_after_sync();
+          const uint32_t va = v_lo + vst * (C::IB >> 4), pa = tbase + t * 256, od = tbase + t * 256 + 128;
+          if (tc05::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kTKeys / 16; ++k)
+              tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2 * C::GB >> 4), HIB), idO, j > 1 || k > 0);
+            if (j + 2 >= n) tc05::commit(&bars->pv_done[t]);
+          }
+          __syncwarp();
+          commit_one(&bars->v_empty[vst]);
+          if (++vst == NV) vst = 0, vph ^= 1u;
+          if (j + 2 < n) issue_next(j + 2);
+        }
+        ++oc[0];
+        continue;
+      }
       ok = wait_warp(&bars->k_full[ks], kph, abort);
       for (int t = 0; t < 2 && ok; ++t) {
         if (sg.nt[t] == 0) continue;
@@ -628,17 +688,16 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     if (!ok && lane == 0) give_up(c.err, abort);
     commit_one(&bars->mma_final);
     if (lane == 0) drain(&bars->mma_final, 0);
-  } else if (warp < 4) {
+  } else if (warp < 4 || idle) {
     // ----------------------------------------------------------- the V stages
     int u = 0;
     uint32_t dir_ph = 0;                               // bit s: parity of v_dir[s]'s next phase
-    const int half = warp - 2;                         // this warp's pages: those of its parity
     bool ok = true;
     Segment sg;
     Items it = w.it;
     Seq sq = w.sq;
     int b = w.b;
-    while (ok && walk_next(e, w, sg)) {
+    while (ok && walk_next<ALT>(e, w, sg)) {
       const int klo = it.lo(sg.i), khi = it.hi(sg.i);
       for (int j = sg.ja; j < sg.jb && ok; ++j, ++u) {
         const int vs = u % NV, rs = u % NR;
@@ -656,20 +715,20 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const int z0 = max(0, klo - j * kTKeys), z1 = min(kTKeys, khi - j * kTKeys);   // seen: [z0, z1)
         const bool edge = z0 > 0 || z1 < kTKeys;
         if (VM == kXFP16 || VM == kXMixed) {
-          if (dmask && half == 0) {
+          if (dmask && vi == 0) {
             uint64_t* bar = edge ? &bars->v_dir[vs] : &bars->v_full[vs];
             if (lane == 0) {
               if (edge) mbar_arrive_expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
               else expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
             }
             __syncwarp();
-            if (dir) tma_load_5d(dv + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + sg.h * p.v16_head, bar);
+            if (dir) tma_load_5d(dv + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + h * p.v16_head, bar);
           }
         }
         if (VM != kXFP16) {
           // 16 codes of one token become two 16-byte chunks; the lanes of the second slab write
           // theirs in the other order, so that eight lanes never meet in a bank
-          for (int pg = half; pg < kTPages; pg += 2) {
+          for (int pg = vi; pg < kTPages; pg += nvw) {
             const int fl = __shfl_sync(0xffffffffu, flags, pg);
             if (fl == 0 || (fl & xs::kSkip)) continue;
             const uint8_t* src = sR + rs * C::RB + pg * (kPage * D);
@@ -719,13 +778,13 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (flags & xs::kSkip));
         if (edge || smask) {
-          for (int x = lane; x < kTKeys / 2 * (D / 8); x += 32) {
-            const int pg = half + 2 * (x / (kPage * (D / 8))), t = x / (D / 8) % kPage, ch = x % (D / 8);
-            const int key = pg * kPage + t;
-            if (key < z0 || key >= z1 || ((smask >> pg) & 1u))
-              *reinterpret_cast<uint4*>(dv + (key >> 3) * C::GB + (ch >> 3) * 1024 + (key & 7) * 128 + (ch & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          }
+          for (int pg = vi; pg < kTPages; pg += nvw)
+            for (int x = lane; x < kPage * (D / 8); x += 32) {
+              const int key = pg * kPage + x / (D / 8), ch = x % (D / 8);
+              if (key < z0 || key >= z1 || ((smask >> pg) & 1u))
+                *reinterpret_cast<uint4*>(dv + (key >> 3) * C::GB + (ch >> 3) * 1024 + (key & 7) * 128 + (ch & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
         }
         fence_async();                                 // written for the MMAs; the raw bytes read for their refill
         __syncwarp();
@@ -749,17 +808,17 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const float qs = e.qscale;
     const float osc = p.scale_ptr ? __ldg(p.scale_ptr) : 1.f;   // one E4M3 scale for every code
     const uint32_t t_s = tbase + t * 256 + lanebase, t_o = tbase + t * 256 + 128 + lanebase;
-    uint32_t sc = 0, pvc = 0;
+    uint32_t sc = 0, pvc = 0, seg = 0;                 // phases: s_full, pv_done; segments
     int u = 0;
     bool ok = true;
     Segment sg;
     Items it = w.it;
     Seq sq = w.sq;
     const int tok_t = r / e.G, g = r % e.G;            // this thread's token within the tile, and head
-    while (ok && walk_next(e, w, sg)) {
+    while (ok && walk_next<ALT>(e, w, sg)) {
       const int nmine = sg.nt[t], u0 = u;
       u += sg.jb - sg.ja;
-      const int first = (2 * sg.i + t) * TT;           // the tile's first token
+      const int first = (ALT ? sg.i : 2 * sg.i + t) * TT;   // the tile's first token
       const int tok = first + tok_t;
       const bool valid = tok_t < TT && tok < it.n;
       const int pos = it.t0 + tok, lo = max(pos - e.window, -1);   // keys lo + 1 .. pos
@@ -768,13 +827,14 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       float m_ref = -INFINITY, l = 0.f;
       bool bad = false;
       for (int jj = 0; jj < nmine; ++jj) {
+        const int blk = ALT ? 2 * jj + t : jj;         // block of the segment
         ok = wait_warp(&bars->s_full[t], sc & 1u, abort);
         ++sc;
-        if (ok) ok = wait_warp(&bars->meta_full[(u0 + jj) % NM], (uint32_t)((u0 + jj) / NM) & 1u, abort);
+        if (ok) ok = wait_warp(&bars->meta_full[(u0 + blk) % NM], (uint32_t)((u0 + blk) / NM) & 1u, abort);
         if (!ok) break;
         tc05::fence_after_sync();
-        const BlockMeta& mt = bars->meta[(u0 + jj) % NM];
-        const int k0 = (sg.ja + jj) * kTKeys;
+        const BlockMeta& mt = bars->meta[(u0 + blk) % NM];
+        const int k0 = (sg.ja + blk) * kTKeys;
         const int badp = mt.bad;
         uint32_t a[4][32];
         tc05::ld32(t_s, a[0]);
@@ -858,7 +918,83 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
       if (!ok) break;
-      const size_t prow = (size_t)sg.slot * (2 * kTRows) + t * kTRows + r;
+      const size_t prow = (size_t)sg.slot * (2 * kTRows) + (ALT ? 0 : t) * kTRows + r;
+      if (ALT) {
+        // join the streams: each posts (m, l) and reads the other's, and takes half of the columns of
+        // both O, which lie in its own tensor-memory lanes
+        if (nmine > 0) {
+          ok = wait_warp(&bars->pv_done[t], pvc & 1u, abort);
+          ++pvc;
+          if (!ok) break;
+        }
+        // the other stream has read what the last segment posted (it arrived here afterwards)
+        if (seg > 0) ok = wait_warp(&bars->o_free[0], (seg - 1u) & 1u, abort);
+        if (!ok) break;
+        float2 (&xch)[2][ALT ? kTRows : 1] = bars->xch;
+        xch[t][r] = make_float2(m_ref, bad ? kBadRecord : l);
+        tc05::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->x_full[t]);
+        ok = wait_warp(&bars->x_full[1 - t], seg & 1u, abort);
+        ++seg;
+        if (!ok) break;
+        tc05::fence_after_sync();
+        const float2 other = xch[1 - t][r];
+        bad = bad || other.y < 0.f;
+        const float M = fmaxf(m_ref, other.x);
+        float w0 = l > 0.f ? xs::ex2(m_ref - M) : 0.f, w1 = other.y > 0.f ? xs::ex2(other.x - M) : 0.f;
+        const float L = fmaf(l, w0, fmaxf(other.y, 0.f) * w1);
+        if (t == 1) {                                  // w0 weighs stream 0
+          const float x = w0;
+          w0 = w1;
+          w1 = x;
+        }
+        const bool none = bad || !(L > 0.f);
+        const float inv = none ? 0.f : osc / L;
+        const size_t orow = (size_t)(sq.q0 + tok) * c.Hq + h * e.G + g;
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          const int col = t * (D / 2) + 32 * x;
+          uint32_t o0[32], o1[32];
+          tc05::ld32(tbase + 128 + lanebase + col, o0);
+          tc05::ld32(tbase + 384 + lanebase + col, o1);
+          tc05::wait_ld();
+          if (x == D / 64 - 1) {
+            tc05::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->o_free[0]);
+          }
+#pragma unroll
+          for (int y = 0; y < 32; ++y) {               // (a stream without blocks left no O: weight 0)
+            const float a0 = w0 > 0.f ? __uint_as_float(o0[y]) * w0 : 0.f;
+            o0[y] = __float_as_uint(w1 > 0.f ? fmaf(__uint_as_float(o1[y]), w1, a0) : a0);
+          }
+          if (valid && sg.whole) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint4 q;
+              q.x = pack2(__uint_as_float(o0[8 * y + 0]) * inv, __uint_as_float(o0[8 * y + 1]) * inv);
+              q.y = pack2(__uint_as_float(o0[8 * y + 2]) * inv, __uint_as_float(o0[8 * y + 3]) * inv);
+              q.z = pack2(__uint_as_float(o0[8 * y + 4]) * inv, __uint_as_float(o0[8 * y + 5]) * inv);
+              q.w = pack2(__uint_as_float(o0[8 * y + 6]) * inv, __uint_as_float(o0[8 * y + 7]) * inv);
+              if (none) q = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(e.out + orow * D + col + 8 * y) = q;
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              *reinterpret_cast<uint4*>(p.part_acc + prow * D + col + 4 * y) =
+                  make_uint4(o0[4 * y], o0[4 * y + 1], o0[4 * y + 2], o0[4 * y + 3]);
+          }
+        }
+        if (valid && t == 0) {
+          if (!sg.whole) p.part_ml[prow] = make_float2(M, bad ? kBadRecord : L);
+          else if (e.lse) e.lse[orow] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        }
+        it = w.it;
+        sq = w.sq;
+        continue;
+      }
       if (nmine == 0) {
         if (!sg.whole && valid) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
         it = w.it;
@@ -871,7 +1007,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       tc05::fence_after_sync();
       const bool none = bad || !(l > 0.f);
       const float inv = none ? 0.f : osc / l;
-      const size_t orow = (size_t)(sq.q0 + tok) * c.Hq + sg.h * e.G + g;
+      const size_t orow = (size_t)(sq.q0 + tok) * c.Hq + h * e.G + g;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
         uint32_t o[32];
@@ -919,7 +1055,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 
 // Joins the items that crossed CTAs: block (x, y) takes rows 32 y .. 32 y + 31 of the item that
 // begins in CTA x and ends in a later one, a warp per row.
-template <int D>
+template <int D, bool ALT>
 __global__ void __launch_bounds__(256)
 extend_join_kernel(const ExtTcParams p) {
   griddep_wait();
@@ -934,9 +1070,9 @@ extend_join_kernel(const ExtTcParams p) {
   constexpr int C = D / 32;
   for (int x = threadIdx.x >> 5; x < 32; x += 8) {
     const int row = blockIdx.y * 32 + x, t = row / kTRows, r = row % kTRows;
-    const int tok = (2 * s.i + t) * TT + r / e.G;
+    const int tok = (ALT ? s.i : 2 * s.i + t) * TT + r / e.G;
     if (r >= TT * e.G || tok >= sq.n) continue;
-    auto at = [&](int i) { return (size_t)(i == 0 ? s.first : 2 * ((int)blockIdx.x + i)) * (2 * kTRows) + row; };
+    auto at = [&](int i) { return (size_t)(i == 0 ? s.first : 2 * ((int)blockIdx.x + i * e.c.Hkv)) * (2 * kTRows) + row; };
     // weights, 32 records at a time with a running maximum (the sums as everywhere)
     float M = -INFINITY, L = 0.f, acc[C];
     bool bad = false;
@@ -1016,17 +1152,17 @@ struct ExtTcMaps {
   CUtensorMap q, k, v16, v8;
 };
 
-template <int D, int VM, bool PS>
+template <int D, int VM, bool PS, bool ALT>
 cudaError_t launch_ext_tc(const ExtTcMaps& m, const ExtTcParams& p, int grid, cudaStream_t st) {
-  auto kern = extend_tc05_kernel<D, VM, PS>;
-  constexpr int smem = xt_smem_bytes<D, VM>();
+  auto kern = extend_tc05_kernel<D, VM, PS, ALT>;
+  constexpr int smem = xt_smem_bytes<D, VM, ALT>();
   static_assert(smem <= 232448, "shared memory of one CTA");
   cudaError_t err = set_smem_attr(reinterpret_cast<const void*>(kern), smem);
   if (err != cudaSuccess) return err;
   kern<<<grid, kT5Threads, smem, st>>>(m.q, m.k, m.v16, m.v8, p);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 2 * kTRows / 32);
+  cfg.gridDim = dim3(grid, ALT ? p.nw : 2 * kTRows / 32);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1034,18 +1170,24 @@ cudaError_t launch_ext_tc(const ExtTcMaps& m, const ExtTcParams& p, int grid, cu
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, extend_join_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, extend_join_kernel<D, ALT>, p);
+}
+
+template <int D, bool ALT>
+cudaError_t launch_ext_tc_alt(const ExtTcMaps& m, const ExtTcParams& p, int vm, int grid, cudaStream_t st) {
+  switch (vm) {
+    case kXFP16: return launch_ext_tc<D, kXFP16, false, ALT>(m, p, grid, st);
+    case kXE4M3:
+      return p.scale_ptr ? launch_ext_tc<D, kXE4M3, false, ALT>(m, p, grid, st)
+                         : launch_ext_tc<D, kXE4M3, true, ALT>(m, p, grid, st);
+    case kXMicro: return launch_ext_tc<D, kXMicro, false, ALT>(m, p, grid, st);
+    default: return launch_ext_tc<D, kXMixed, true, ALT>(m, p, grid, st);
+  }
 }
 
 template <int D>
 cudaError_t launch_ext_tc_d(const ExtTcMaps& m, const ExtTcParams& p, int vm, int grid, cudaStream_t st) {
-  switch (vm) {
-    case kXFP16: return launch_ext_tc<D, kXFP16, false>(m, p, grid, st);
-    case kXE4M3:
-      return p.scale_ptr ? launch_ext_tc<D, kXE4M3, false>(m, p, grid, st) : launch_ext_tc<D, kXE4M3, true>(m, p, grid, st);
-    case kXMicro: return launch_ext_tc<D, kXMicro, false>(m, p, grid, st);
-    default: return launch_ext_tc<D, kXMixed, true>(m, p, grid, st);
-  }
+  return p.nw > 0 ? launch_ext_tc_alt<D, true>(m, p, vm, grid, st) : launch_ext_tc_alt<D, false>(m, p, vm, grid, st);
 }
 
 }  // namespace ekv
