@@ -17,9 +17,10 @@
 //     each; an item that crosses a border leaves partial rows (m, l, O) in at most two slots a CTA, and
 //     a second kernel joins them. Long causal chunks so balance to a block, and one short chunk
 //     behind a long prefix still uses every SM.
-// Roles: warp 0 loads Q, K and raw values and checks the pages; warp 1 issues the MMAs; warps 2 and 3
-// make the V stages (warp 2 owns tensor memory); warps 4-7 and 8-11 are the softmax of tile 0 and
-// 1, a thread per row. Tensor memory of tile t: S and P at 256 t, O at 256 t + 128. The order of
+// Roles: warp 0 checks the pages and loads Q and K; warp 1 issues the MMAs; warp 2 loads raw value
+// pages (and owns tensor memory), warp 3 FP16 ones; warps 4-7 and 8-11 are the softmax of tile 0 and
+// 1, a thread per row; warps 12-15 make the V stages, with the softmax warps that have no rows. The
+// registers are split to match (setmaxnreg): 80, 176, 176 and 80 a thread, 512 = 4 x the 128 of launch. Tensor memory of tile t: S and P at 256 t, O at 256 t + 128. The order of
 // the MMAs and the lazily moved maximum are those of the prefill (prefill_tc05.cu). Every wait is
 // bounded; a timeout is reported and every role winds down.
 #pragma once
@@ -33,7 +34,7 @@ namespace ekv {
 constexpr int kTRows = 128;                 // rows of a query tile (MMA M)
 constexpr int kTKeys = 128;                 // keys of a block (N of S)
 constexpr int kTPages = kTKeys / kPage;
-constexpr int kT5Threads = 384;
+constexpr int kT5Threads = 512;
 constexpr int kItemCost = 1;                // an item's start (query load, epilogue) in blocks
 
 struct ExtTcSplit {                         // an item that crosses CTAs, for the joining kernel
@@ -198,7 +199,8 @@ __device__ __forceinline__ int floor_sum(int n, int m, int a, int b) {
 
 // The items of one sequence and KV head: pairs of tiles, `step` tokens each.
 struct Items {
-  int L, n, t0, step, np, window;
+  int n, t0, np;              // new tokens, position of the first, items
+  int step, window;
   // keys of item i: [lo, hi)
   __device__ __forceinline__ int lo(int i) const {
     const int first = t0 + i * step;
@@ -221,7 +223,6 @@ struct Items {
 template <bool ALT>
 __device__ __forceinline__ Items items_of(const ExtendParams& e, const Seq& s) {
   Items it;
-  it.L = s.L;
   it.n = s.n;
   it.t0 = s.L - s.n;
   it.step = (ALT ? 1 : 2) * (kTRows / e.G);
@@ -235,13 +236,15 @@ struct Walk {
   int b, i, j;              // next: sequence, item, block (j may lie kItemCost before the item's first)
   int budget;               // blocks left in the CTA's range
   int index;                // segments so far
-  Seq sq;
+  int q0;                   // the sequence's first row of q
   Items it;
 };
 struct Segment {
   int ja, jb;               // blocks
   int jlo, jhi;             // of the whole item
   int i, slot;
+  int b, q0, n, t0;         // the sequence: its index, first row of q, new tokens, position of the first
+  int lo, hi;               // keys that the item sees
   int nt[2];                // blocks that each tile takes part in, from ja on
   bool whole;
 };
@@ -252,6 +255,12 @@ __device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segmen
     sg.jlo = w.it.jlo(w.i);
     sg.jhi = w.it.jhi(w.i);
     sg.i = w.i;
+    sg.b = w.b;
+    sg.q0 = w.q0;
+    sg.n = w.it.n;
+    sg.t0 = w.it.t0;
+    sg.lo = w.it.lo(w.i);
+    sg.hi = w.it.hi(w.i);
     const int ja = w.j, jb = min(sg.jhi, w.j + w.budget);
     w.budget -= jb - ja;
     w.j = jb;
@@ -270,10 +279,14 @@ __device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segmen
     if (jb == sg.jhi) {                              // on to the next item
       if (++w.i == w.it.np) {
         w.i = 0;
+        Seq sq;
         do {
           ++w.b;
-        } while (w.b < e.c.batch && (!load_seq(e, w.b, w.sq) || !seq_ok(e, w.sq)));
-        if (w.b < e.c.batch) w.it = items_of<ALT>(e, w.sq);
+        } while (w.b < e.c.batch && (!load_seq(e, w.b, sq) || !seq_ok(e, sq)));
+        if (w.b < e.c.batch) {
+          w.q0 = sq.q0;
+          w.it = items_of<ALT>(e, sq);
+        }
       }
       if (w.b < e.c.batch) w.j = w.it.jlo(w.i) - kItemCost;
     }
@@ -284,6 +297,36 @@ __device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segmen
     }
   }
   return false;
+}
+
+// A walk in one register, a field per lane: for the softmax warps, whose registers hold their rows.
+__device__ __forceinline__ int pack_walk(const Walk& w) {
+  const int lane = threadIdx.x & 31;
+  int v = w.b;
+  v = lane == 1 ? w.i : v;
+  v = lane == 2 ? w.j : v;
+  v = lane == 3 ? w.budget : v;
+  v = lane == 4 ? w.index : v;
+  v = lane == 5 ? w.q0 : v;
+  v = lane == 6 ? w.it.n : v;
+  v = lane == 7 ? w.it.t0 : v;
+  v = lane == 8 ? w.it.np : v;
+  return lane == 9 ? w.it.step : v;
+}
+__device__ __forceinline__ Walk unpack_walk(const ExtendParams& e, int v) {
+  Walk w;
+  w.b = __shfl_sync(0xffffffffu, v, 0);
+  w.i = __shfl_sync(0xffffffffu, v, 1);
+  w.j = __shfl_sync(0xffffffffu, v, 2);
+  w.budget = __shfl_sync(0xffffffffu, v, 3);
+  w.index = __shfl_sync(0xffffffffu, v, 4);
+  w.q0 = __shfl_sync(0xffffffffu, v, 5);
+  w.it.n = __shfl_sync(0xffffffffu, v, 6);
+  w.it.t0 = __shfl_sync(0xffffffffu, v, 7);
+  w.it.np = __shfl_sync(0xffffffffu, v, 8);
+  w.it.step = __shfl_sync(0xffffffffu, v, 9);
+  w.it.window = e.window;
+  return w;
 }
 
 }  // namespace xt
@@ -320,9 +363,10 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   }
   // softmax warps per tile (ALT: those with rows), and the warps that make the V stages
   const int nw = ALT ? p.nw : kTRows / 32;
-  const int nvw = 2 + 2 * (4 - nw);
-  const bool idle = ALT && warp >= 4 && (warp & 3) >= nw;
-  const int vi = warp < 4 ? warp - 2 : 2 + (warp >> 2 == 1 ? 0 : 4 - nw) + (warp & 3) - nw;   // index among the latter
+  const int nvw = 4 + 2 * (4 - nw);
+  const bool idle = ALT && warp >= 4 && warp < 12 && (warp & 3) >= nw;
+  const int vi = warp >= 12 ? warp - 12 : 4 + (warp >> 2 == 1 ? 0 : 4 - nw) + (warp & 3) - nw;   // index among the latter
+  constexpr bool kDirect = VM == kXFP16 || VM == kXMixed, kRaw = VM != kXFP16;
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -336,7 +380,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     for (int s = 0; s < NK; ++s) mbar_init(&bars->k_full[s], 1), mbar_init(&bars->k_empty[s], 1);
     for (int s = 0; s < NR; ++s) mbar_init(&bars->raw_full[s], 1), mbar_init(&bars->raw_empty[s], nvw);
-    for (int s = 0; s < NV; ++s) mbar_init(&bars->v_full[s], nvw), mbar_init(&bars->v_empty[s], 1), mbar_init(&bars->v_dir[s], 1);
+    for (int s = 0; s < NV; ++s) mbar_init(&bars->v_full[s], nvw + (kDirect ? 1 : 0)), mbar_init(&bars->v_empty[s], 1), mbar_init(&bars->v_dir[s], 1);
     for (int s = 0; s < NM; ++s) mbar_init(&bars->meta_full[s], 1);
     mbar_init(&bars->mma_final, 1);
     bars->abort = 0;
@@ -433,135 +477,289 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   w.budget = w.b < 0 ? 0 : budget0;
   w.index = 0;
   if (w.budget > 0) {
-    load_seq(e, w.b, w.sq);
-    w.it = items_of<ALT>(e, w.sq);
+    Seq sq;
+    load_seq(e, w.b, sq);
+    w.q0 = sq.q0;
+    w.it = items_of<ALT>(e, sq);
   }
   const uint32_t tbase = bars->tmem_base;
   const int TT = kTRows / e.G;                         // tokens of a tile
   const int h_rows = TT * e.G;
 
-  if (warp == 0) {
-    // -------------------------------------------- producer: Q, page checks, K, raw values
-    int ks = 0, rs = 0, u = 0;
-    uint32_t kph = 0, rph = 0, ql[2] = {0u, 0u};
-    ExtTcSplit split;
-    split.n = 0;
+  // ------------------------------------------------------------- the V stages
+  auto make_v = [&]() {
+    int u = 0;
+    uint32_t dir_ph = 0;                               // bit s: parity of v_dir[s]'s next phase
     bool ok = true;
     Segment sg;
-    int b = w.b;
-    Seq sq = w.sq;
-    Items it = w.it;
     while (ok && walk_next<ALT>(e, w, sg)) {
-      for (int t = 0; t < C::NQ && ok; ++t) {
-        if (sg.nt[t] == 0) continue;
-        if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(h_rows * D * 2));
-          for (int s = 0; s < NB; ++s)
-            tma_load_5d(sQ + t * C::QB + s * (kTRows * 128), &tq, 0, 0, s, h, sq.q0 + (C::NQ * sg.i + t) * TT, &bars->q_full[t]);
-        }
-        ++ql[t];
-      }
-      if (!ok) break;
-      const int klo = it.lo(sg.i), khi = it.hi(sg.i);
-      const int plo = klo / kPage, phi = (khi + kPage - 1) / kPage;
-      // the ids of a block's pages are fetched a block ahead (their modes and scales depend on them)
-      int id = 0;
-      auto fetch = [&](int j) {
-        const int lp = j * kTPages + lane;
-        id = lane < kTPages && lp >= plo && lp < phi ? __ldg(c.block_table + (size_t)b * c.bt_stride + lp) : 0;
-      };
-      fetch(sg.ja);
+      const int klo = sg.lo, khi = sg.hi;
       for (int j = sg.ja; j < sg.jb && ok; ++j, ++u) {
-        const int lp = j * kTPages + lane;
-        const int page = id;
-        const bool in = lane < kTPages && lp >= plo && lp < phi;
-        int flags = xs::kSkip, detail = EKV_DETAIL_NONE;
-        float vs = 1.f;
-        if (in) {
-          flags = VM == kXE4M3 ? xs::kE4 : VM == kXMicro ? xs::kMx : 0;
-          if (page < 0 || page >= c.num_pages) detail = EKV_DETAIL_PAGE_ID;
-          if (!detail && VM == kXMixed) {
-            const int mode = c.page_mode ? (int)__ldg(c.page_mode + page) : c.uniform_mode;
-            flags = mode == EKV_MODE_COMPACT_E4M3 ? xs::kE4 : mode == EKV_MODE_BASE ? xs::kBs : mode == EKV_MODE_MICRO_FP4 ? xs::kMx : 0;
-            if (mode > EKV_MODE_MICRO_FP4) detail = EKV_DETAIL_PAGE_MODE;
+        const int vs = u % NV, rs = u % NR;
+        ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
+        if (ok && kRaw) ok = wait_warp(&bars->raw_full[rs], (uint32_t)(u / NR) & 1u, abort);
+        if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
+        if (!ok) break;
+        const BlockMeta& mt = bars->meta[u % NM];
+        uint8_t* dv = sV + vs * C::IB;
+        const int flags = lane < kTPages ? mt.flags[lane] : xs::kSkip;
+        const uint32_t dmask = kDirect ? __ballot_sync(0xffffffffu, flags == 0) : 0u;
+        // keys of the block that no row of the item sees: zero rows, whatever the pages hold
+        const int z0 = max(0, klo - j * kTKeys), z1 = min(kTKeys, khi - j * kTKeys);   // seen: [z0, z1)
+        const bool edge = z0 > 0 || z1 < kTKeys;
+        if (VM != kXFP16) {
+          // 16 codes of one token become two 16-byte chunks; the lanes of the second slab write
+          // theirs in the other order, so that eight lanes never meet in a bank
+          for (int pg = vi; pg < kTPages; pg += nvw) {
+            const int fl = __shfl_sync(0xffffffffu, flags, pg);
+            if (fl == 0 || (fl & xs::kSkip)) continue;
+            const uint8_t* src = sR + rs * C::RB + pg * (kPage * D);
+#pragma unroll 4
+            for (int x = lane; x < kPage * D / 16; x += 32) {
+              const int t = x / (D / 16), ch = x % (D / 16);
+              uint4 lo, hi;
+              if (fl & xs::kMx) {
+                const uint2 codes = *reinterpret_cast<const uint2*>(src + t * (D / 2) + ch * 8);
+                uint32_t sb = src[micro_scale_off(D) + t * (D / kMicroBlock) + ch / 2];
+                if (!micro_scale_ok(sb)) {
+                  const int key = j * kTKeys + pg * kPage + t;
+                  if (key >= klo && key < khi) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SCALE, sg.b);
+                  sb = 0;
+                }
+                const __half2 s2 = micro_scale_h2(sb);
+                lo = micro_decode8(codes.x, s2);
+                hi = micro_decode8(codes.y, s2);
+              } else {
+                const uint32_t off = D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16);
+                const uint4 q = *reinterpret_cast<const uint4*>(src + off);
+                if (fl & xs::kBs) {
+                  lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
+                                  __byte_perm(q.y, 0u, 0x3424));
+                  hi = make_uint4(__byte_perm(q.z, 0u, 0x1404), __byte_perm(q.z, 0u, 0x3424), __byte_perm(q.w, 0u, 0x1404),
+                                  __byte_perm(q.w, 0u, 0x3424));
+                } else {
+                  lo = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.x)), xs::bits(e4m3x2_to_half2((uint16_t)(q.x >> 16))),
+                                  xs::bits(e4m3x2_to_half2((uint16_t)q.y)), xs::bits(e4m3x2_to_half2((uint16_t)(q.y >> 16))));
+                  hi = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.z)), xs::bits(e4m3x2_to_half2((uint16_t)(q.z >> 16))),
+                                  xs::bits(e4m3x2_to_half2((uint16_t)q.w)), xs::bits(e4m3x2_to_half2((uint16_t)(q.w >> 16))));
+                }
+              }
+              const int c0 = 2 * (ch & 3), slab = ch >> 2, r = t & 7;
+              uint8_t* row = dv + (pg * 2 + (t >> 3)) * C::GB + slab * 1024 + r * 128;
+              const bool swap = slab & 1;
+              *reinterpret_cast<uint4*>(row + ((c0 + (swap ? 1 : 0)) ^ r) * 16) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(row + ((c0 + (swap ? 0 : 1)) ^ r) * 16) = swap ? lo : hi;
+            }
           }
-          if (!detail && (VM == kXE4M3 || VM == kXMixed) && (flags & xs::kE4)) {
-            vs = !c.v_scales ? 0.f : __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)page * c.Hkv + h));
-            if (!scale_ok(vs)) detail = EKV_DETAIL_SCALE;
-          }
-          if (detail) {
-            report_error(c.err, EKV_ERR_DEVICE_CHECK, detail, b);
-            flags = xs::kSkip;
-            vs = 1.f;
-          }
+          __syncwarp();
         }
-        if (j + 1 < sg.jb) fetch(j + 1);
-        const uint32_t bad = __ballot_sync(0xffffffffu, detail != EKV_DETAIL_NONE);
-        const uint32_t loads = __ballot_sync(0xffffffffu, !(flags & xs::kSkip));
-        BlockMeta& mt = bars->meta[u % NM];
-        // K stage first: its wait bounds how far this warp runs ahead, so the description
-        // that block u - NM left is no longer read
+        if (dmask && edge) {
+          ok = wait_warp(&bars->v_dir[vs], (dir_ph >> vs) & 1u, abort);
+          dir_ph ^= 1u << vs;
+          if (!ok) break;
+        }
+        const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (flags & xs::kSkip));
+        if (edge || smask) {
+          for (int pg = vi; pg < kTPages; pg += nvw)
+            for (int x = lane; x < kPage * (D / 8); x += 32) {
+              const int key = pg * kPage + x / (D / 8), ch = x % (D / 8);
+              if (key < z0 || key >= z1 || ((smask >> pg) & 1u))
+                *reinterpret_cast<uint4*>(dv + (key >> 3) * C::GB + (ch >> 3) * 1024 + (key & 7) * 128 + (ch & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        fence_async();                                 // written for the MMAs; the raw bytes read for their refill
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->v_full[vs]);
+          if (kRaw) mbar_arrive(&bars->raw_empty[rs]);
+        }
+      }
+    }
+    if (!ok && lane == 0) give_up(c.err, abort);
+  };
+
+  // (each register split stands at the head of its roles' code)
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if (warp == 0) {
+    // ------------------------------------------- producer: page checks, Q, K
+    // Pages are looked up in batches of four blocks, a page per lane: a batch's ids are fetched
+    // two batches ahead and its modes and scales one ahead, across segments.
+    int ks = 0, u = 0;
+    uint32_t kph = 0, ql[2] = {0u, 0u};
+    ExtTcSplit split;
+    split.n = 0;
+    struct Batch {
+      int b, j0, nb, plo, phi, qtok, nt0, nt1;         // nt0 < 0: not a segment's first batch
+    };
+    Segment sg;
+    sg.ja = sg.jb = 0;
+    auto next_batch = [&](Batch& x) {
+      x.nt0 = -1;
+      x.nb = 0;
+      if (sg.ja >= sg.jb) {
+        if (!walk_next<ALT>(e, w, sg)) return;
+        x.qtok = sg.q0 + C::NQ * sg.i * TT;
+        x.nt0 = sg.nt[0];
+        x.nt1 = sg.nt[1];
+        if (sg.ja == sg.jlo && sg.jb < sg.jhi) {       // the item goes on in later CTAs
+          split.n = 1 + (int)((sg.jhi - sg.jb + per - 1) / per);
+          split.first = sg.slot;
+          split.b = sg.b;
+          split.h = h;
+          split.i = sg.i;
+        }
+      }
+      x.b = sg.b;
+      x.j0 = sg.ja;
+      x.nb = min(32 / kTPages, sg.jb - sg.ja);
+      x.plo = sg.lo / kPage;
+      x.phi = (sg.hi + kPage - 1) / kPage;
+      sg.ja += x.nb;
+    };
+    auto in_batch = [&](const Batch& x) {
+      const int lp = x.j0 * kTPages + lane;
+      return lane < x.nb * kTPages && lp >= x.plo && lp < x.phi;
+    };
+    auto ids = [&](const Batch& x) {
+      return in_batch(x) ? __ldg(c.block_table + (size_t)x.b * c.bt_stride + x.j0 * kTPages + lane) : 0;
+    };
+    auto lookup = [&](const Batch& x, int id, int& mode, float& vs) {
+      mode = VM == kXFP16 ? EKV_MODE_TARGET_FP16 : VM == kXE4M3 ? EKV_MODE_COMPACT_E4M3 : VM == kXMicro ? EKV_MODE_MICRO_FP4 : c.uniform_mode;
+      vs = 0.f;
+      if (!in_batch(x) || id < 0 || id >= c.num_pages) return;
+      if (VM == kXMixed && c.page_mode) mode = (int)__ldg(c.page_mode + id);
+      if ((VM == kXE4M3 || VM == kXMixed) && c.v_scales)
+        vs = __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)id * c.Hkv + h));
+    };
+    Batch b0, b1, b2;
+    next_batch(b0);
+    next_batch(b1);
+    next_batch(b2);
+    int id0 = ids(b0), id1 = ids(b1), mode0, mode1;
+    float vs0, vs1;
+    lookup(b0, id0, mode0, vs0);
+    bool ok = true;
+    while (ok && b0.nb > 0) {
+      // this batch's pages
+      int flags = xs::kSkip, detail = EKV_DETAIL_NONE;
+      float vs = 1.f;
+      if (in_batch(b0)) {
+        flags = mode0 == EKV_MODE_COMPACT_E4M3 ? xs::kE4 : mode0 == EKV_MODE_BASE ? xs::kBs : mode0 == EKV_MODE_MICRO_FP4 ? xs::kMx : 0;
+        if (id0 < 0 || id0 >= c.num_pages) detail = EKV_DETAIL_PAGE_ID;
+        else if (mode0 > EKV_MODE_MICRO_FP4) detail = EKV_DETAIL_PAGE_MODE;
+        else if ((flags & xs::kE4) && !scale_ok(vs0)) detail = EKV_DETAIL_SCALE;
+        else if (flags & xs::kE4) vs = vs0;
+        if (detail) {
+          report_error(c.err, EKV_ERR_DEVICE_CHECK, detail, b0.b);
+          flags = xs::kSkip;
+        }
+      }
+      const float lsc = log2f(vs), ivs = 1.f / vs;
+      const uint32_t bad = __ballot_sync(0xffffffffu, detail != EKV_DETAIL_NONE);
+      const uint32_t loads = __ballot_sync(0xffffffffu, !(flags & xs::kSkip));
+      lookup(b1, id1, mode1, vs1);                     // the next one's, and the ids after
+      const int id2 = ids(b2);
+      if (b0.nt0 >= 0) {                               // a segment begins: its query tiles
+        for (int t = 0; t < C::NQ && ok; ++t) {
+          if ((t == 0 ? b0.nt0 : b0.nt1) == 0) continue;
+          if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(h_rows * D * 2));
+            for (int s = 0; s < NB; ++s)
+              tma_load_5d(sQ + t * C::QB + s * (kTRows * 128), &tq, 0, 0, s, h, b0.qtok + t * TT, &bars->q_full[t]);
+          }
+          ++ql[t];
+        }
+      }
+      for (int i = 0; i < b0.nb && ok; ++i, ++u) {
+        // the K stage first: its wait bounds how far this warp runs ahead (see NM)
         if (u >= NK) ok = wait_warp(&bars->k_empty[ks], kph ^ 1u, abort);
         if (!ok) break;
-        if (lane < kTPages) {
-          mt.page[lane] = page;
-          mt.flags[lane] = (uint8_t)flags;
-          mt.lsc[lane] = log2f(vs);
-          mt.ivs[lane] = 1.f / vs;
-          if (lane == 0) mt.bad = (int)bad;
+        BlockMeta& mt = bars->meta[u % NM];
+        const int pg = lane & (kTPages - 1);
+        const bool mine = lane / kTPages == i;
+        if (mine) {
+          mt.page[pg] = id0;
+          mt.flags[pg] = (uint8_t)flags;
+          mt.lsc[pg] = lsc;
+          mt.ivs[pg] = ivs;
+          if (pg == 0) mt.bad = (int)((bad >> (i * kTPages)) & 0xffu);
         }
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&bars->meta_full[u % NM]);
-          mbar_arrive_expect_tx(&bars->k_full[ks], (uint32_t)__popc(loads) * (kPage * D * 2));
+          mbar_arrive_expect_tx(&bars->k_full[ks], (uint32_t)__popc((loads >> (i * kTPages)) & 0xffu) * (kPage * D * 2));
         }
         __syncwarp();
-        if (!(flags & xs::kSkip))
-          tma_load_5d(sK + ks * C::IB + lane * (2 * C::GB), &tk, 0, 0, 0, 0, page * kPage * c.Hkv + h, &bars->k_full[ks]);
-        if (++ks == NK) {
-          ks = 0;
-          kph ^= 1u;
-        }
-        if (VM != kXFP16) {
-          if (u >= NR) ok = wait_warp(&bars->raw_empty[rs], rph ^ 1u, abort);
-          if (!ok) break;
-          const bool mx = flags & xs::kMx, by = flags & (xs::kE4 | xs::kBs);
-          uint32_t bytes = mx ? micro_head_bytes(D) : by ? kPage * D : 0;
-          uint32_t sum = bytes;
-#pragma unroll
-          for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[rs], sum);
-          __syncwarp();
-          uint8_t* dst = sR + rs * C::RB + lane * (kPage * D);
-          if (mx) bulk_load(dst, c.v_pages + (size_t)page * c.v_page_stride + h * micro_head_bytes(D), bytes, &bars->raw_full[rs]);
-          else if (by) tma_load_4d(dst, &tv8, 0, h, 0, page, &bars->raw_full[rs]);
-          if (++rs == NR) {
-            rs = 0;
-            rph ^= 1u;
-          }
-        }
+        if (mine && !(flags & xs::kSkip))
+          tma_load_5d(sK + ks * C::IB + pg * (2 * C::GB), &tk, 0, 0, 0, 0, id0 * kPage * c.Hkv + h, &bars->k_full[ks]);
+        if (++ks == NK) ks = 0, kph ^= 1u;
       }
-      if (sg.ja == sg.jlo && sg.jb < sg.jhi) {         // the item goes on in later CTAs
-        split.n = 1 + (int)((sg.jhi - sg.jb + per - 1) / per);
-        split.first = sg.slot;
-        split.b = b;
-        split.h = h;
-        split.i = sg.i;
-      }
-      b = w.b;
-      sq = w.sq;
-      it = w.it;
+      b0 = b1;
+      id0 = id1;
+      mode0 = mode1;
+      vs0 = vs1;
+      b1 = b2;
+      id1 = id2;
+      next_batch(b2);
     }
     if (!ok && lane == 0) give_up(c.err, abort);
     if (lane == 0) p.split[blockIdx.x] = split;
     // the copies still in flight land before the CTA can exit
     for (int v = max(0, u - NK); v < u; ++v) drain(&bars->k_full[v % NK], (v / NK) & 1);
-    if (VM != kXFP16)
-      for (int v = max(0, u - NR); v < u; ++v) drain(&bars->raw_full[v % NR], (v / NR) & 1);
     for (int t = 0; t < 2; ++t)
       if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
+  } else if (warp == 2 || warp == 3) {
+    // --------------------------- value loaders: raw pages (warp 2), FP16 pages (warp 3)
+    int u = 0;
+    bool ok = warp == 2 ? kRaw : kDirect;
+    const bool run = ok;
+    Segment sg;
+    while (ok && walk_next<ALT>(e, w, sg)) {
+      for (int j = sg.ja; j < sg.jb && ok; ++j, ++u) {
+        ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
+        if (!ok) break;
+        const BlockMeta& mt = bars->meta[u % NM];
+        const int flags = lane < kTPages ? mt.flags[lane] : xs::kSkip;
+        const int page = lane < kTPages ? mt.page[lane] : 0;
+        if (warp == 2) {
+          const int rs = u % NR;
+          if (u >= NR) ok = wait_warp(&bars->raw_empty[rs], (uint32_t)(u / NR - 1) & 1u, abort);
+          if (!ok) break;
+          const bool mx = flags & xs::kMx, by = flags & (xs::kE4 | xs::kBs);
+          const uint32_t nmx = __popc(__ballot_sync(0xffffffffu, mx)), nby = __popc(__ballot_sync(0xffffffffu, by));
+          if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[rs], nmx * micro_head_bytes(D) + nby * (kPage * D));
+          __syncwarp();
+          uint8_t* dst = sR + rs * C::RB + lane * (kPage * D);
+          if (mx)
+            bulk_load(dst, c.v_pages + (size_t)page * c.v_page_stride + h * micro_head_bytes(D), micro_head_bytes(D), &bars->raw_full[rs]);
+          else if (by)
+            tma_load_4d(dst, &tv8, 0, h, 0, page, &bars->raw_full[rs]);
+        } else {
+          const int vs = u % NV;
+          if (u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
+          if (!ok) break;
+          // a stage with rows to zero is announced on a barrier of its own; they are zeroed once it has landed
+          const bool edge = sg.lo > j * kTKeys || sg.hi < (j + 1) * kTKeys;
+          const uint32_t dmask = __ballot_sync(0xffffffffu, flags == 0);
+          uint64_t* bar = edge ? &bars->v_dir[vs] : &bars->v_full[vs];
+          if (lane == 0) {
+            if (edge) mbar_arrive(&bars->v_full[vs]);
+            if (!edge || dmask) mbar_arrive_expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
+          }
+          __syncwarp();
+          if (flags == 0) tma_load_5d(sV + vs * C::IB + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + h * p.v16_head, bar);
+        }
+      }
+    }
+    if (!ok && run && lane == 0) give_up(c.err, abort);
+    if (run && warp == 2)
+      for (int v = max(0, u - NR); v < u; ++v) drain(&bars->raw_full[v % NR], (uint32_t)(v / NR) & 1u);
+    if (run && warp == 3)
+      for (int v = max(0, u - NV); v < u; ++v) drain(&bars->v_full[v % NV], (uint32_t)(v / NV) & 1u);
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer
     constexpr uint32_t idS = tc05::idesc_f16_f32(kTRows, kTKeys, false);
@@ -688,120 +886,15 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     if (!ok && lane == 0) give_up(c.err, abort);
     commit_one(&bars->mma_final);
     if (lane == 0) drain(&bars->mma_final, 0);
-  } else if (warp < 4 || idle) {
-    // ----------------------------------------------------------- the V stages
-    int u = 0;
-    uint32_t dir_ph = 0;                               // bit s: parity of v_dir[s]'s next phase
-    bool ok = true;
-    Segment sg;
-    Items it = w.it;
-    Seq sq = w.sq;
-    int b = w.b;
-    while (ok && walk_next<ALT>(e, w, sg)) {
-      const int klo = it.lo(sg.i), khi = it.hi(sg.i);
-      for (int j = sg.ja; j < sg.jb && ok; ++j, ++u) {
-        const int vs = u % NV, rs = u % NR;
-        ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
-        if (ok && VM != kXFP16) ok = wait_warp(&bars->raw_full[rs], (uint32_t)(u / NR) & 1u, abort);
-        if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
-        if (!ok) break;
-        const BlockMeta& mt = bars->meta[u % NM];
-        uint8_t* dv = sV + vs * C::IB;
-        const int flags = lane < kTPages ? mt.flags[lane] : xs::kSkip;
-        const int page = lane < kTPages ? mt.page[lane] : 0;
-        const bool dir = VM == kXFP16 ? flags == 0 : VM == kXMixed && flags == 0;
-        const uint32_t dmask = __ballot_sync(0xffffffffu, dir);
-        // keys of the block that no row of the item sees: zero rows, whatever the pages hold
-        const int z0 = max(0, klo - j * kTKeys), z1 = min(kTKeys, khi - j * kTKeys);   // seen: [z0, z1)
-        const bool edge = z0 > 0 || z1 < kTKeys;
-        if (VM == kXFP16 || VM == kXMixed) {
-          if (dmask && vi == 0) {
-            uint64_t* bar = edge ? &bars->v_dir[vs] : &bars->v_full[vs];
-            if (lane == 0) {
-              if (edge) mbar_arrive_expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
-              else expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
-            }
-            __syncwarp();
-            if (dir) tma_load_5d(dv + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + h * p.v16_head, bar);
-          }
-        }
-        if (VM != kXFP16) {
-          // 16 codes of one token become two 16-byte chunks; the lanes of the second slab write
-          // theirs in the other order, so that eight lanes never meet in a bank
-          for (int pg = vi; pg < kTPages; pg += nvw) {
-            const int fl = __shfl_sync(0xffffffffu, flags, pg);
-            if (fl == 0 || (fl & xs::kSkip)) continue;
-            const uint8_t* src = sR + rs * C::RB + pg * (kPage * D);
-#pragma unroll 4
-            for (int x = lane; x < kPage * D / 16; x += 32) {
-              const int t = x / (D / 16), ch = x % (D / 16);
-              uint4 lo, hi;
-              if (fl & xs::kMx) {
-                const uint2 codes = *reinterpret_cast<const uint2*>(src + t * (D / 2) + ch * 8);
-                uint32_t sb = src[micro_scale_off(D) + t * (D / kMicroBlock) + ch / 2];
-                if (!micro_scale_ok(sb)) {
-                  const int key = j * kTKeys + pg * kPage + t;
-                  if (key >= klo && key < khi) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SCALE, b);
-                  sb = 0;
-                }
-                const __half2 s2 = micro_scale_h2(sb);
-                lo = micro_decode8(codes.x, s2);
-                hi = micro_decode8(codes.y, s2);
-              } else {
-                const uint32_t off = D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16);
-                const uint4 q = *reinterpret_cast<const uint4*>(src + off);
-                if (fl & xs::kBs) {
-                  lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
-                                  __byte_perm(q.y, 0u, 0x3424));
-                  hi = make_uint4(__byte_perm(q.z, 0u, 0x1404), __byte_perm(q.z, 0u, 0x3424), __byte_perm(q.w, 0u, 0x1404),
-                                  __byte_perm(q.w, 0u, 0x3424));
-                } else {
-                  lo = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.x)), xs::bits(e4m3x2_to_half2((uint16_t)(q.x >> 16))),
-                                  xs::bits(e4m3x2_to_half2((uint16_t)q.y)), xs::bits(e4m3x2_to_half2((uint16_t)(q.y >> 16))));
-                  hi = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.z)), xs::bits(e4m3x2_to_half2((uint16_t)(q.z >> 16))),
-                                  xs::bits(e4m3x2_to_half2((uint16_t)q.w)), xs::bits(e4m3x2_to_half2((uint16_t)(q.w >> 16))));
-                }
-              }
-              const int c0 = 2 * (ch & 3), slab = ch >> 2, r = t & 7;
-              uint8_t* row = dv + (pg * 2 + (t >> 3)) * C::GB + slab * 1024 + r * 128;
-              const bool swap = slab & 1;
-              *reinterpret_cast<uint4*>(row + ((c0 + (swap ? 1 : 0)) ^ r) * 16) = swap ? hi : lo;
-              *reinterpret_cast<uint4*>(row + ((c0 + (swap ? 0 : 1)) ^ r) * 16) = swap ? lo : hi;
-            }
-          }
-          __syncwarp();
-        }
-        if ((VM == kXFP16 || VM == kXMixed) && dmask && edge) {
-          ok = wait_warp(&bars->v_dir[vs], (dir_ph >> vs) & 1u, abort);
-          dir_ph ^= 1u << vs;
-          if (!ok) break;
-        }
-        const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (flags & xs::kSkip));
-        if (edge || smask) {
-          for (int pg = vi; pg < kTPages; pg += nvw)
-            for (int x = lane; x < kPage * (D / 8); x += 32) {
-              const int key = pg * kPage + x / (D / 8), ch = x % (D / 8);
-              if (key < z0 || key >= z1 || ((smask >> pg) & 1u))
-                *reinterpret_cast<uint4*>(dv + (key >> 3) * C::GB + (ch >> 3) * 1024 + (key & 7) * 128 + (ch & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
-        fence_async();                                 // written for the MMAs; the raw bytes read for their refill
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->v_full[vs]);
-          if (VM != kXFP16) mbar_arrive(&bars->raw_empty[rs]);
-        }
-      }
-      it = w.it;
-      sq = w.sq;
-      b = w.b;
-    }
-    if (!ok && lane == 0) give_up(c.err, abort);
-    // direct copies in flight (a V stage whose product never came is drained here)
-    if (VM == kXFP16 || VM == kXMixed)
-      for (int v = max(0, u - NV); v < u; ++v) drain(&bars->v_full[v % NV], (uint32_t)(v / NV) & 1u);
+  }
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    make_v();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    if (idle) {
+      make_v();
+    } else {
     // ------------------------------------------------------- softmax, tile t
     const int t = (warp - 4) >> 2, r = threadIdx.x - 128 - t * kTRows;
     const uint32_t lanebase = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -811,19 +904,31 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     uint32_t sc = 0, pvc = 0, seg = 0;                 // phases: s_full, pv_done; segments
     int u = 0;
     bool ok = true;
-    Segment sg;
-    Items it = w.it;
-    Seq sq = w.sq;
-    const int tok_t = r / e.G, g = r % e.G;            // this thread's token within the tile, and head
-    while (ok && walk_next<ALT>(e, w, sg)) {
-      const int nmine = sg.nt[t], u0 = u;
-      u += sg.jb - sg.ja;
-      const int first = (ALT ? sg.i : 2 * sg.i + t) * TT;   // the tile's first token
-      const int tok = first + tok_t;
-      const bool valid = tok_t < TT && tok < it.n;
-      const int pos = it.t0 + tok, lo = max(pos - e.window, -1);   // keys lo + 1 .. pos
-      // keys that every valid row sees: from the last row's window start to the first row's own
-      const int all_lo = it.t0 + min(first + TT, it.n) - 1 - e.window, all_hi = it.t0 + first;
+    const int tok_t = r / e.G;                         // this thread's token within the tile
+    int walk = pack_walk(w);
+    while (ok) {
+      // what the rows need of the segment; orow < 0: a row past the sequence
+      int nmine, u0 = u, ja, pos, lo, all_lo, all_hi, slot;
+      long long orow;
+      {
+        Segment sg;
+        Walk v = unpack_walk(e, walk);
+        if (!walk_next<ALT>(e, v, sg)) break;
+        walk = pack_walk(v);
+        nmine = sg.nt[t];
+        u += sg.jb - sg.ja;
+        ja = sg.ja;
+        const int first = (ALT ? sg.i : 2 * sg.i + t) * TT;   // the tile's first token
+        const int tok = first + tok_t;
+        pos = sg.t0 + tok;
+        lo = max(pos - e.window, -1);                  // the row sees keys lo + 1 .. pos
+        // keys that every valid row sees: from the last row's window start to the first row's own
+        all_lo = sg.t0 + min(first + TT, sg.n) - 1 - e.window;
+        all_hi = sg.t0 + first;
+        slot = sg.whole ? -1 : sg.slot;
+        orow = tok_t < TT && tok < sg.n ? (long long)(sg.q0 + tok) * c.Hq + h * e.G + r % e.G : -1;
+      }
+      const bool valid = orow >= 0, whole = slot < 0;
       float m_ref = -INFINITY, l = 0.f;
       bool bad = false;
       for (int jj = 0; jj < nmine; ++jj) {
@@ -834,7 +939,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (!ok) break;
         tc05::fence_after_sync();
         const BlockMeta& mt = bars->meta[(u0 + blk) % NM];
-        const int k0 = (sg.ja + blk) * kTKeys;
+        const int k0 = (ja + blk) * kTKeys;
         const int badp = mt.bad;
         uint32_t a[4][32];
         tc05::ld32(t_s, a[0]);
@@ -918,7 +1023,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
       if (!ok) break;
-      const size_t prow = (size_t)sg.slot * (2 * kTRows) + (ALT ? 0 : t) * kTRows + r;
+      const size_t prow = (size_t)max(slot, 0) * (2 * kTRows) + (ALT ? 0 : t) * kTRows + r;
       if (ALT) {
         // join the streams: each posts (m, l) and reads the other's, and takes half of the columns of
         // both O, which lie in its own tensor-memory lanes
@@ -951,7 +1056,6 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         const bool none = bad || !(L > 0.f);
         const float inv = none ? 0.f : osc / L;
-        const size_t orow = (size_t)(sq.q0 + tok) * c.Hq + h * e.G + g;
 #pragma unroll
         for (int x = 0; x < D / 64; ++x) {
           const int col = t * (D / 2) + 32 * x;
@@ -969,7 +1073,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             const float a0 = w0 > 0.f ? __uint_as_float(o0[y]) * w0 : 0.f;
             o0[y] = __float_as_uint(w1 > 0.f ? fmaf(__uint_as_float(o1[y]), w1, a0) : a0);
           }
-          if (valid && sg.whole) {
+          if (valid && whole) {
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               uint4 q;
@@ -988,17 +1092,13 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           }
         }
         if (valid && t == 0) {
-          if (!sg.whole) p.part_ml[prow] = make_float2(M, bad ? kBadRecord : L);
+          if (!whole) p.part_ml[prow] = make_float2(M, bad ? kBadRecord : L);
           else if (e.lse) e.lse[orow] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
         }
-        it = w.it;
-        sq = w.sq;
         continue;
       }
       if (nmine == 0) {
-        if (!sg.whole && valid) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
-        it = w.it;
-        sq = w.sq;
+        if (!whole && valid) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
         continue;
       }
       ok = wait_warp(&bars->pv_done[t], pvc & 1u, abort);
@@ -1007,7 +1107,6 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       tc05::fence_after_sync();
       const bool none = bad || !(l > 0.f);
       const float inv = none ? 0.f : osc / l;
-      const size_t orow = (size_t)(sq.q0 + tok) * c.Hq + h * e.G + g;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
         uint32_t o[32];
@@ -1018,7 +1117,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->o_free[t]);
         }
-        if (valid && sg.whole) {
+        if (valid && whole) {
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             uint4 q;
@@ -1037,13 +1136,12 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
       }
       if (valid) {
-        if (!sg.whole) p.part_ml[prow] = make_float2(m_ref, bad ? kBadRecord : l);
+        if (!whole) p.part_ml[prow] = make_float2(m_ref, bad ? kBadRecord : l);
         else if (e.lse) e.lse[orow] = none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
       }
-      it = w.it;
-      sq = w.sq;
     }
     if (!ok && lane == 0) give_up(c.err, abort);
+  }
   }
   tc05::fence_before_sync();
   __syncthreads();
