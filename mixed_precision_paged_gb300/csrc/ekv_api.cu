@@ -728,9 +728,10 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
     x.part_acc = c->ext_acc;
     x.part_ml = c->ext_ml;
     x.split = c->ext_split;
+    // few rows: one tile, its key blocks alternating between the softmax groups
     const long long rows = (long long)p.G * max_q;
-    x.nw = max_q <= kTRows / p.G ? (int)((rows + 31) / 32) : 0;
-    if (vm == kXE4M3 && scale_mode == EKV_SCALE_PER_TENSOR) x.scale_ptr = v_scales;
+    x.nw = rows <= kAltRows ? (int)((rows + 31) / 32) : 0;
+    x.e.tile_tokens = (x.nw > 0 ? 32 * x.nw : kTRows) / p.G;
     // one coordinate for (page, head): in units that divide both the page stride and a head's row
     int unit = 2 * D;
     while (v_page_stride_bytes % unit) unit /= 2;
@@ -738,7 +739,7 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
     if ((long long)num_pages * kPage * Hkv > 0x7fffffffLL || places > 0x7fffffffLL) return EKV_ERR_UNSUPPORTED;
     x.v16_mul = (int)(v_page_stride_bytes / unit);
     x.v16_head = 2 * D / unit;
-    if (!encode_query_map(&m.q, q, D, Hkv, p.G, total_q) ||
+    if (!encode_query_map(&m.q, q, D, Hkv, p.G, total_q, x.e.tile_tokens) ||
         !encode_group_map(&m.k, k_pages, D, Hkv, (unsigned long long)num_pages * kPage * Hkv, 2 * D))
       return EKV_ERR_INVALID_ARG;
     if ((vm == kXFP16 || vm == kXMixed) && !encode_group_map(&m.v16, v_pages, D, Hkv, places, unit)) return EKV_ERR_INVALID_ARG;

@@ -10,16 +10,17 @@
 //     rows, and one tile's softmax runs while the other's products do.
 //   * blocks: 8 pages by one TMA box each, 8-token groups of [D / 64][8 rows][128 B] (128B swizzle),
 //     which serve as K-major B of S and, for V, as N-major B of the second product.
-//   * values: FP16 pages land in a V stage directly. E4M3, BASE and microscaled pages land raw in a
-//     ring of their own and two warps expand them into the V stage, exactly; E4M3 scales join the
+//   * values: FP16 pages land in a V stage directly. E4M3, BASE and microscaled pages land raw, each
+//     maker warp's in a ring of its own, and are expanded into the V stage, exactly; E4M3 scales join the
 //     exponent as in the split kernel (extend_split.cuh), or the output when one scale serves all.
 //   * split: the blocks of all items form one stream, cut into equal ranges, one persistent CTA
 //     each; an item that crosses a border leaves partial rows (m, l, O) in at most two slots a CTA, and
 //     a second kernel joins them. Long causal chunks so balance to a block, and one short chunk
 //     behind a long prefix still uses every SM.
-// Roles: warp 0 checks the pages and loads Q and K; warp 1 issues the MMAs; warp 2 loads raw value
-// pages (and owns tensor memory), warp 3 FP16 ones; warps 4-7 and 8-11 are the softmax of tile 0 and
-// 1, a thread per row; warps 12-15 make the V stages, with the softmax warps that have no rows. The
+// Roles: warp 0 checks the pages and loads Q and K; warp 1 issues the MMAs; warp 2 owns tensor
+// memory; warp 3 loads FP16 value pages; warps 4-7 and 8-11 are the softmax of tile 0 and
+// 1, a thread per row; warps 12-15 load and
+// expand the other pages (ALT: eight warps, on other schedulers than the softmax where they can). The
 // registers are split to match (setmaxnreg): 80, 176, 176 and 80 a thread, 512 = 4 x the 128 of launch. Tensor memory of tile t: S and P at 256 t, O at 256 t + 128. The order of
 // the MMAs and the lazily moved maximum are those of the prefill (prefill_tc05.cu). Every wait is
 // bounded; a timeout is reported and every role winds down.
@@ -35,6 +36,8 @@ constexpr int kTRows = 128;                 // rows of a query tile (MMA M)
 constexpr int kTKeys = 128;                 // keys of a block (N of S)
 constexpr int kTPages = kTKeys / kPage;
 constexpr int kT5Threads = 512;
+constexpr int kAltRows = 64;                // rows of a sequence and KV head up to which blocks alternate
+constexpr int kMetaAhead = 2;               // blocks that page lookups are ahead of the K loads
 constexpr int kItemCost = 1;                // an item's start (query load, epilogue) in blocks
 
 struct ExtTcSplit {                         // an item that crosses CTAs, for the joining kernel
@@ -57,17 +60,19 @@ template <int D, int VM, bool ALT>
 struct XT {
   static constexpr int NB = D / 64;                    // 64-value slabs of a row
   static constexpr int GB = NB * 1024;                 // bytes of an 8-token group
-  static constexpr int QB = kTRows * D * 2;            // a query tile
+  static constexpr int QB = (ALT ? kAltRows : kTRows) * D * 2;   // a query tile (ALT: or two of half the rows)
   static constexpr int IB = kTKeys * D * 2;            // a K or V block
   static constexpr int RB = VM == kXFP16 ? 0 : kTKeys * D;   // a raw block: a page at every 16 * D bytes
   static constexpr int NQ = ALT ? 1 : 2;               // query tiles
   static constexpr int NK = (VM == kXFP16 || ALT ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 4)) + (ALT && D == 64 ? 1 : 0);
   static constexpr int NV = (D == 128 ? 2 : 4) + (ALT && VM == kXFP16 ? 1 : 0);
-  static constexpr int NR = D == 128 ? 2 : 4;
-  // block descriptions. The producer writes one once the K stage NK blocks back is free, so once
-  // that block's S is issued, which is behind the product of the block before (ALT: two before)
-  static constexpr int NM = D == 128 ? (ALT ? 5 : 4) : 8;
-  static_assert(NM >= NK + (ALT ? 2 : 1), "a description is read until its block's weights are handed over");
+  static constexpr int NR = (D == 128 ? 2 : 4) + (ALT ? 1 : 0);
+  static constexpr int MK = ALT ? 8 : 4;               // maker warps
+  static constexpr int PPW = kTPages / MK;             // pages of a block each
+  // Block descriptions. One is written once the K stage NK + kMetaAhead + 1 blocks back is free, so
+  // once that block's S is issued, which is behind the product of the block before (ALT: two before).
+  static constexpr int NM = D == 128 ? 8 : 12;
+  static_assert(NM >= NK + kMetaAhead + (ALT ? 3 : 2), "a description is read until its block's weights are handed over");
 };
 
 struct BlockMeta {
@@ -75,7 +80,10 @@ struct BlockMeta {
   float lsc[kTPages];                       // log2 of the scale
   float ivs[kTPages];                       // and its reciprocal
   int bad;                                  // bit per page that failed its checks
+  int qtok;                                 // a segment's first block: first row of its queries; else -1
   uint8_t flags[kTPages];                   // xs::kSkip: not loaded
+  uint8_t tiles;                            // bit per tile with blocks in the segment
+  uint8_t last;                             // the CTA's last block
 };
 
 template <int D, int VM, bool ALT>
@@ -83,14 +91,14 @@ struct XTBars {
   using C = XT<D, VM, ALT>;
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[C::NK], k_empty[C::NK];
-  uint64_t raw_full[C::NR], raw_empty[C::NR];
+  uint64_t raw_full[C::NR][C::MK];
   uint64_t v_full[C::NV], v_empty[C::NV];
   uint64_t v_dir[C::NV];                    // FP16 pages of a stage whose edge rows are zeroed after they land
   uint64_t meta_full[C::NM];
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t mma_final;
   uint64_t x_full[2];                       // ALT: a stream's (m, l) of the segment posted
-  float2 xch[2][ALT ? kTRows : 1];
+  float2 xch[2][ALT ? kAltRows : 1];
   BlockMeta meta[C::NM];
   long long red[kT5Threads / 32];
   int st_b, st_i, st_j;               // where this CTA's range begins
@@ -110,16 +118,42 @@ using xs::Seq;
 using xs::load_seq;
 using xs::seq_ok;
 
+// try_wait with a suspend-time hint: the warp sleeps in hardware until the phase ends instead of
+// polling. A dozen warps of a CTA wait at any time, and their polls cost the others' shared-memory
+// accesses: without the hint a 32 x 8K decode step took 197 us instead of XXX us.
+__device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (sleep_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > kWaitTimeoutNs)) return false;
+  while (true) {
+    if (sleep_wait(bar, parity)) return true;
+    if (*abort || globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
   }
 }
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
+}
+// For the MMA and softmax warps, whose wake-up is on the critical path: without the hint.
+__device__ __forceinline__ bool wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+      if ((ok = mbar_try_wait(bar, parity))) break;
+      if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > kWaitTimeoutNs)) break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void give_up(int* err, volatile int* abort) {
   if (!*abort) report_error(err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_TIMEOUT, -1);
@@ -225,7 +259,7 @@ __device__ __forceinline__ Items items_of(const ExtendParams& e, const Seq& s) {
   Items it;
   it.n = s.n;
   it.t0 = s.L - s.n;
-  it.step = (ALT ? 1 : 2) * (kTRows / e.G);
+  it.step = (ALT ? 1 : 2) * e.tile_tokens;
   it.np = (s.n + it.step - 1) / it.step;
   it.window = e.window;
   return it;
@@ -361,11 +395,11 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     return;
   }
-  // softmax warps per tile (ALT: those with rows), and the warps that make the V stages
+  // softmax warps per tile (ALT: those with rows), and the maker warps
   const int nw = ALT ? p.nw : kTRows / 32;
-  const int nvw = 4 + 2 * (4 - nw);
-  const bool idle = ALT && warp >= 4 && warp < 12 && (warp & 3) >= nw;
-  const int vi = warp >= 12 ? warp - 12 : 4 + (warp >> 2 == 1 ? 0 : 4 - nw) + (warp & 3) - nw;   // index among the latter
+  int vi = warp - 12;                                  // index among the makers, < 0: none
+  if (ALT && nw == 1) vi = warp >= 12 ? warp - 13 : warp >= 10 ? warp - 4 : warp >= 5 && warp < 8 ? warp - 2 : -1;
+  if (ALT && nw == 2) vi = warp >= 14 ? warp - 14 : warp >= 12 ? warp - 6 : warp >= 10 ? warp - 6 : warp == 6 || warp == 7 ? warp - 4 : -1;
   constexpr bool kDirect = VM == kXFP16 || VM == kXMixed, kRaw = VM != kXFP16;
 
   if (threadIdx.x == 0) {
@@ -379,8 +413,9 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       mbar_init(&bars->x_full[t], nw);
     }
     for (int s = 0; s < NK; ++s) mbar_init(&bars->k_full[s], 1), mbar_init(&bars->k_empty[s], 1);
-    for (int s = 0; s < NR; ++s) mbar_init(&bars->raw_full[s], 1), mbar_init(&bars->raw_empty[s], nvw);
-    for (int s = 0; s < NV; ++s) mbar_init(&bars->v_full[s], nvw + (kDirect ? 1 : 0)), mbar_init(&bars->v_empty[s], 1), mbar_init(&bars->v_dir[s], 1);
+    for (int s = 0; s < NR; ++s)
+      for (int x = 0; x < C::MK; ++x) mbar_init(&bars->raw_full[s][x], 1);
+    for (int s = 0; s < NV; ++s) mbar_init(&bars->v_full[s], C::MK + (kDirect ? 1 : 0)), mbar_init(&bars->v_empty[s], 1), mbar_init(&bars->v_dir[s], 1);
     for (int s = 0; s < NM; ++s) mbar_init(&bars->meta_full[s], 1);
     mbar_init(&bars->mma_final, 1);
     bars->abort = 0;
@@ -483,34 +518,61 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     w.it = items_of<ALT>(e, sq);
   }
   const uint32_t tbase = bars->tmem_base;
-  const int TT = kTRows / e.G;                         // tokens of a tile
+  const int TT = e.tile_tokens;                        // tokens of a tile
+  const int nqb = ALT ? 2 / nw : 2;                    // query buffers: tiles, or (ALT, few rows) segments in turn
+  const int q_slab = (ALT ? 32 * nw : kTRows) * 128, q_buf = NB * q_slab;
   const int h_rows = TT * e.G;
 
-  // ------------------------------------------------------------- the V stages
+
+  // ------------------------------------------- the V stages (other pages than FP16 ones)
   auto make_v = [&]() {
-    int u = 0;
+    int u = 0, issued = 0;
     uint32_t dir_ph = 0;                               // bit s: parity of v_dir[s]'s next phase
-    bool ok = true;
+    bool ok = true, last = false;
+    // this warp's raw pages of the next block that has none in flight: a ring of its own
+    auto issue = [&]() {
+      ok = wait_warp(&bars->meta_full[issued % NM], (uint32_t)(issued / NM) & 1u, abort);
+      if (!ok) return;
+      const BlockMeta& mt = bars->meta[issued % NM];
+      last = mt.last;
+      const int rs = issued % NR, pg = vi + (lane & (C::PPW - 1)) * C::MK;
+      uint64_t* bar = &bars->raw_full[rs][vi];
+      const int flags = lane < C::PPW ? mt.flags[pg] : xs::kSkip;
+      const bool mx = flags & xs::kMx, by = flags & (xs::kE4 | xs::kBs);
+      const uint32_t nmx = __popc(__ballot_sync(0xffffffffu, mx)), nby = __popc(__ballot_sync(0xffffffffu, by));
+      if (lane == 0) mbar_arrive_expect_tx(bar, nmx * micro_head_bytes(D) + nby * (kPage * D));
+      __syncwarp();
+      uint8_t* dst = sR + rs * C::RB + pg * (kPage * D);
+      if (mx)
+        bulk_load(dst, c.v_pages + (size_t)mt.page[pg] * c.v_page_stride + h * micro_head_bytes(D), micro_head_bytes(D), bar);
+      else if (by)
+        tma_load_4d(dst, &tv8, 0, h, 0, mt.page[pg], bar);
+      ++issued;
+    };
     Segment sg;
     while (ok && walk_next<ALT>(e, w, sg)) {
       const int klo = sg.lo, khi = sg.hi;
+      if (kRaw && issued == 0)
+        while (ok && !last && issued < NR) issue();
       for (int j = sg.ja; j < sg.jb && ok; ++j, ++u) {
         const int vs = u % NV, rs = u % NR;
         ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
-        if (ok && kRaw) ok = wait_warp(&bars->raw_full[rs], (uint32_t)(u / NR) & 1u, abort);
+        if (ok && kRaw) ok = wait_warp(&bars->raw_full[rs][vi], (uint32_t)(u / NR) & 1u, abort);
         if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
         if (!ok) break;
         const BlockMeta& mt = bars->meta[u % NM];
         uint8_t* dv = sV + vs * C::IB;
         const int flags = lane < kTPages ? mt.flags[lane] : xs::kSkip;
         const uint32_t dmask = kDirect ? __ballot_sync(0xffffffffu, flags == 0) : 0u;
+        const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (flags & xs::kSkip));
         // keys of the block that no row of the item sees: zero rows, whatever the pages hold
         const int z0 = max(0, klo - j * kTKeys), z1 = min(kTKeys, khi - j * kTKeys);   // seen: [z0, z1)
         const bool edge = z0 > 0 || z1 < kTKeys;
-        if (VM != kXFP16) {
+        if (kRaw) {
           // 16 codes of one token become two 16-byte chunks; the lanes of the second slab write
           // theirs in the other order, so that eight lanes never meet in a bank
-          for (int pg = vi; pg < kTPages; pg += nvw) {
+          for (int i = 0; i < C::PPW; ++i) {
+            const int pg = vi + i * C::MK;
             const int fl = __shfl_sync(0xffffffffu, flags, pg);
             if (fl == 0 || (fl & xs::kSkip)) continue;
             const uint8_t* src = sR + rs * C::RB + pg * (kPage * D);
@@ -518,7 +580,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             for (int x = lane; x < kPage * D / 16; x += 32) {
               const int t = x / (D / 16), ch = x % (D / 16);
               uint4 lo, hi;
-              if (fl & xs::kMx) {
+              if (VM == kXMicro || (VM == kXMixed && (fl & xs::kMx))) {
                 const uint2 codes = *reinterpret_cast<const uint2*>(src + t * (D / 2) + ch * 8);
                 uint32_t sb = src[micro_scale_off(D) + t * (D / kMicroBlock) + ch / 2];
                 if (!micro_scale_ok(sb)) {
@@ -532,7 +594,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               } else {
                 const uint32_t off = D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16);
                 const uint4 q = *reinterpret_cast<const uint4*>(src + off);
-                if (fl & xs::kBs) {
+                if (VM == kXMixed && (fl & xs::kBs)) {
                   lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
                                   __byte_perm(q.y, 0u, 0x3424));
                   hi = make_uint4(__byte_perm(q.z, 0u, 0x1404), __byte_perm(q.z, 0u, 0x3424), __byte_perm(q.w, 0u, 0x1404),
@@ -558,11 +620,10 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           dir_ph ^= 1u << vs;
           if (!ok) break;
         }
-        const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (flags & xs::kSkip));
         if (edge || smask) {
-          for (int pg = vi; pg < kTPages; pg += nvw)
+          for (int i = 0; i < C::PPW; ++i)
             for (int x = lane; x < kPage * (D / 8); x += 32) {
-              const int key = pg * kPage + x / (D / 8), ch = x % (D / 8);
+              const int pg = vi + i * C::MK, key = pg * kPage + x / (D / 8), ch = x % (D / 8);
               if (key < z0 || key >= z1 || ((smask >> pg) & 1u))
                 *reinterpret_cast<uint4*>(dv + (key >> 3) * C::GB + (ch >> 3) * 1024 + (key & 7) * 128 + (ch & 7) * 16) =
                     make_uint4(0u, 0u, 0u, 0u);
@@ -570,13 +631,13 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         fence_async();                                 // written for the MMAs; the raw bytes read for their refill
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->v_full[vs]);
-          if (kRaw) mbar_arrive(&bars->raw_empty[rs]);
-        }
+        if (lane == 0) mbar_arrive(&bars->v_full[vs]);
+        if (kRaw && !last) issue();
       }
     }
     if (!ok && lane == 0) give_up(c.err, abort);
+    if (kRaw)
+      for (int v = max(0, issued - NR); v < issued; ++v) drain(&bars->raw_full[v % NR][vi], (uint32_t)(v / NR) & 1u);
   };
 
   // (each register split stands at the head of its roles' code)
@@ -584,25 +645,26 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   if (warp == 0) {
     // ------------------------------------------- producer: page checks, Q, K
-    // Pages are looked up in batches of four blocks, a page per lane: a batch's ids are fetched
-    // two batches ahead and its modes and scales one ahead, across segments.
-    int ks = 0, u = 0;
-    uint32_t kph = 0, ql[2] = {0u, 0u};
+    // Pages are looked up in batches of four blocks, a page per lane: a batch's ids are fetched two
+    // batches ahead and its modes and scales one ahead, across segments. A block's description is
+    // posted kMetaAhead blocks before its keys are loaded, for the makers, whose loads take as long.
+    int u = 0, k = 0;                                  // blocks described, blocks whose keys were loaded
+    uint32_t ql[2] = {0u, 0u}, qseg = 0;
     ExtTcSplit split;
     split.n = 0;
     struct Batch {
-      int b, j0, nb, plo, phi, qtok, nt0, nt1;         // nt0 < 0: not a segment's first batch
+      int b, j0, nb, plo, phi, qtok, tiles;            // qtok < 0: not a segment's first batch
     };
     Segment sg;
     sg.ja = sg.jb = 0;
     auto next_batch = [&](Batch& x) {
-      x.nt0 = -1;
+      x.qtok = -1;
+      x.tiles = 0;
       x.nb = 0;
       if (sg.ja >= sg.jb) {
         if (!walk_next<ALT>(e, w, sg)) return;
         x.qtok = sg.q0 + C::NQ * sg.i * TT;
-        x.nt0 = sg.nt[0];
-        x.nt1 = sg.nt[1];
+        x.tiles = (sg.nt[0] > 0 ? 1 : 0) | (sg.nt[1] > 0 ? 2 : 0);
         if (sg.ja == sg.jlo && sg.jb < sg.jhi) {       // the item goes on in later CTAs
           split.n = 1 + (int)((sg.jhi - sg.jb + per - 1) / per);
           split.first = sg.slot;
@@ -633,6 +695,36 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       if ((VM == kXE4M3 || VM == kXMixed) && c.v_scales)
         vs = __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)id * c.Hkv + h));
     };
+    bool ok = true;
+    // the queries (first block of a segment) and keys of block k
+    auto load_k = [&]() {
+      const BlockMeta& mt = bars->meta[k % NM];
+      if (mt.qtok >= 0) {
+        const int tiles = ALT ? 1 << (qseg % nqb) : mt.tiles;
+        ++qseg;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (!((tiles >> t) & 1)) continue;
+          if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
+          if (!ok) return;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(h_rows * D * 2));
+            for (int s = 0; s < NB; ++s)
+              tma_load_5d(sQ + t * q_buf + s * q_slab, &tq, 0, 0, s, h, mt.qtok + (ALT ? 0 : t * TT), &bars->q_full[t]);
+          }
+          ++ql[t];
+        }
+      }
+      const int ks = k % NK;
+      if (k >= NK) ok = wait_warp(&bars->k_empty[ks], (uint32_t)(k / NK - 1) & 1u, abort);
+      if (!ok) return;
+      const bool load = lane < kTPages && !(mt.flags[lane & (kTPages - 1)] & xs::kSkip);
+      const int n = __popc(__ballot_sync(0xffffffffu, load));
+      if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[ks], (uint32_t)n * (kPage * D * 2));
+      __syncwarp();
+      if (load)
+        tma_load_5d(sK + ks * C::IB + lane * (2 * C::GB), &tk, 0, 0, 0, 0, mt.page[lane] * kPage * c.Hkv + h, &bars->k_full[ks]);
+      ++k;
+    };
     Batch b0, b1, b2;
     next_batch(b0);
     next_batch(b1);
@@ -640,7 +732,6 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     int id0 = ids(b0), id1 = ids(b1), mode0, mode1;
     float vs0, vs1;
     lookup(b0, id0, mode0, vs0);
-    bool ok = true;
     while (ok && b0.nb > 0) {
       // this batch's pages
       int flags = xs::kSkip, detail = EKV_DETAIL_NONE;
@@ -658,45 +749,26 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       }
       const float lsc = log2f(vs), ivs = 1.f / vs;
       const uint32_t bad = __ballot_sync(0xffffffffu, detail != EKV_DETAIL_NONE);
-      const uint32_t loads = __ballot_sync(0xffffffffu, !(flags & xs::kSkip));
-      lookup(b1, id1, mode1, vs1);                     // the next one's, and the ids after
+      lookup(b1, id1, mode1, vs1);                     // the next batch's, and the ids after
       const int id2 = ids(b2);
-      if (b0.nt0 >= 0) {                               // a segment begins: its query tiles
-        for (int t = 0; t < C::NQ && ok; ++t) {
-          if ((t == 0 ? b0.nt0 : b0.nt1) == 0) continue;
-          if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(h_rows * D * 2));
-            for (int s = 0; s < NB; ++s)
-              tma_load_5d(sQ + t * C::QB + s * (kTRows * 128), &tq, 0, 0, s, h, b0.qtok + t * TT, &bars->q_full[t]);
-          }
-          ++ql[t];
-        }
-      }
       for (int i = 0; i < b0.nb && ok; ++i, ++u) {
-        // the K stage first: its wait bounds how far this warp runs ahead (see NM)
-        if (u >= NK) ok = wait_warp(&bars->k_empty[ks], kph ^ 1u, abort);
-        if (!ok) break;
         BlockMeta& mt = bars->meta[u % NM];
         const int pg = lane & (kTPages - 1);
-        const bool mine = lane / kTPages == i;
-        if (mine) {
+        if (lane / kTPages == i) {
           mt.page[pg] = id0;
           mt.flags[pg] = (uint8_t)flags;
           mt.lsc[pg] = lsc;
           mt.ivs[pg] = ivs;
-          if (pg == 0) mt.bad = (int)((bad >> (i * kTPages)) & 0xffu);
+          if (pg == 0) {
+            mt.bad = (int)((bad >> (i * kTPages)) & 0xffu);
+            mt.qtok = i == 0 ? b0.qtok : -1;
+            mt.tiles = (uint8_t)b0.tiles;
+            mt.last = i + 1 == b0.nb && b1.nb == 0;
+          }
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->meta_full[u % NM]);
-          mbar_arrive_expect_tx(&bars->k_full[ks], (uint32_t)__popc((loads >> (i * kTPages)) & 0xffu) * (kPage * D * 2));
-        }
-        __syncwarp();
-        if (mine && !(flags & xs::kSkip))
-          tma_load_5d(sK + ks * C::IB + pg * (2 * C::GB), &tk, 0, 0, 0, 0, id0 * kPage * c.Hkv + h, &bars->k_full[ks]);
-        if (++ks == NK) ks = 0, kph ^= 1u;
+        if (lane == 0) mbar_arrive(&bars->meta_full[u % NM]);
+        if (u >= kMetaAhead) load_k();
       }
       b0 = b1;
       id0 = id1;
@@ -706,59 +778,41 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       id1 = id2;
       next_batch(b2);
     }
+    while (ok && k < u) load_k();
     if (!ok && lane == 0) give_up(c.err, abort);
     if (lane == 0) p.split[blockIdx.x] = split;
     // the copies still in flight land before the CTA can exit
-    for (int v = max(0, u - NK); v < u; ++v) drain(&bars->k_full[v % NK], (v / NK) & 1);
+    for (int v = max(0, k - NK); v < k; ++v) drain(&bars->k_full[v % NK], (v / NK) & 1);
     for (int t = 0; t < 2; ++t)
       if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
-  } else if (warp == 2 || warp == 3) {
-    // --------------------------- value loaders: raw pages (warp 2), FP16 pages (warp 3)
+  } else if (warp == 3) {
+    // ------------------------------------------------ loads of FP16 value pages
     int u = 0;
-    bool ok = warp == 2 ? kRaw : kDirect;
-    const bool run = ok;
+    bool ok = kDirect;
     Segment sg;
     while (ok && walk_next<ALT>(e, w, sg)) {
       for (int j = sg.ja; j < sg.jb && ok; ++j, ++u) {
+        const int vs = u % NV;
         ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
+        if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
         if (!ok) break;
         const BlockMeta& mt = bars->meta[u % NM];
         const int flags = lane < kTPages ? mt.flags[lane] : xs::kSkip;
         const int page = lane < kTPages ? mt.page[lane] : 0;
-        if (warp == 2) {
-          const int rs = u % NR;
-          if (u >= NR) ok = wait_warp(&bars->raw_empty[rs], (uint32_t)(u / NR - 1) & 1u, abort);
-          if (!ok) break;
-          const bool mx = flags & xs::kMx, by = flags & (xs::kE4 | xs::kBs);
-          const uint32_t nmx = __popc(__ballot_sync(0xffffffffu, mx)), nby = __popc(__ballot_sync(0xffffffffu, by));
-          if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[rs], nmx * micro_head_bytes(D) + nby * (kPage * D));
-          __syncwarp();
-          uint8_t* dst = sR + rs * C::RB + lane * (kPage * D);
-          if (mx)
-            bulk_load(dst, c.v_pages + (size_t)page * c.v_page_stride + h * micro_head_bytes(D), micro_head_bytes(D), &bars->raw_full[rs]);
-          else if (by)
-            tma_load_4d(dst, &tv8, 0, h, 0, page, &bars->raw_full[rs]);
-        } else {
-          const int vs = u % NV;
-          if (u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
-          if (!ok) break;
-          // a stage with rows to zero is announced on a barrier of its own; they are zeroed once it has landed
-          const bool edge = sg.lo > j * kTKeys || sg.hi < (j + 1) * kTKeys;
-          const uint32_t dmask = __ballot_sync(0xffffffffu, flags == 0);
-          uint64_t* bar = edge ? &bars->v_dir[vs] : &bars->v_full[vs];
-          if (lane == 0) {
-            if (edge) mbar_arrive(&bars->v_full[vs]);
-            if (!edge || dmask) mbar_arrive_expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
-          }
-          __syncwarp();
-          if (flags == 0) tma_load_5d(sV + vs * C::IB + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + h * p.v16_head, bar);
+        // a stage with rows to zero is announced on a barrier of its own; they are zeroed once it has landed
+        const bool edge = sg.lo > j * kTKeys || sg.hi < (j + 1) * kTKeys;
+        const uint32_t dmask = __ballot_sync(0xffffffffu, flags == 0);
+        uint64_t* bar = edge ? &bars->v_dir[vs] : &bars->v_full[vs];
+        if (lane == 0) {
+          if (edge) mbar_arrive(&bars->v_full[vs]);
+          if (!edge || dmask) mbar_arrive_expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
         }
+        __syncwarp();
+        if (flags == 0) tma_load_5d(sV + vs * C::IB + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + h * p.v16_head, bar);
       }
     }
-    if (!ok && run && lane == 0) give_up(c.err, abort);
-    if (run && warp == 2)
-      for (int v = max(0, u - NR); v < u; ++v) drain(&bars->raw_full[v % NR], (uint32_t)(v / NR) & 1u);
-    if (run && warp == 3)
+    if (!ok && kDirect && lane == 0) give_up(c.err, abort);
+    if (kDirect)
       for (int v = max(0, u - NV); v < u; ++v) drain(&bars->v_full[v % NV], (uint32_t)(v / NV) & 1u);
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer
@@ -768,16 +822,16 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const uint32_t q_lo = tc05::sdesc_lo(smem_u32(sQ), 16);
     const uint32_t k_lo = tc05::sdesc_lo(smem_u32(sK), 16);
     const uint32_t v_lo = tc05::sdesc_lo(smem_u32(sV), 1024);     // the next 64 columns lie 1024 B on
-    int ks = 0, vst = 0;
+    int ks = 0, vst = 0, qbuf = 0;                     // qbuf (ALT): the segment's query buffer
     uint32_t kph = 0, vph = 0;
     uint32_t qc[2] = {0u, 0u}, pc[2] = {0u, 0u}, oc[2] = {0u, 0u};
     auto issue_s = [&](int t) {                        // S_t = Q_t K^T from stage ks
-      const uint32_t qa = q_lo + (ALT ? 0 : t) * (C::QB >> 4), ka = k_lo + ks * (C::IB >> 4);
+      const uint32_t qa = q_lo + (ALT ? qbuf : t) * (q_buf >> 4), ka = k_lo + ks * (C::IB >> 4);
       const uint32_t d = tbase + t * 256;
       if (tc05::elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          tc05::mma_ss(d, tc05::sdesc_join(qa + (((k >> 2) * (kTRows * 128) + (k & 3) * 32) >> 4), HIQ),
+          tc05::mma_ss(d, tc05::sdesc_join(qa + (((k >> 2) * q_slab + (k & 3) * 32) >> 4), HIQ),
                        tc05::sdesc_join(ka + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), HIB), idS, k > 0);
         tc05::commit(&bars->s_full[t]);
       }
@@ -794,24 +848,24 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       if (ALT) {
         // block j belongs to stream j mod 2: O_t += P_t V_j, then S_t of block j + 2 over P_t
         auto issue_next = [&](int j) {                 // S of block j
-          ok = wait_warp(&bars->k_full[ks], kph, abort);
+          ok = wait_spin(&bars->k_full[ks], kph, abort);
           if (!ok) return;
           tc05::fence_after_sync();
           issue_s(j & 1);
           commit_one(&bars->k_empty[ks]);
           if (++ks == NK) ks = 0, kph ^= 1u;
-          if (j == n - 1) commit_one(&bars->q_empty[0]);
+          if (j == n - 1) commit_one(&bars->q_empty[qbuf]);
         };
-        ok = wait_warp(&bars->q_full[0], qc[0] & 1u, abort);
-        ++qc[0];
+        ok = wait_spin(&bars->q_full[qbuf], qc[qbuf] & 1u, abort);
+        ++qc[qbuf];
         for (int j = 0; j < min(n, 2) && ok; ++j) issue_next(j);
         for (int j = 0; ok && j < n; ++j) {
           const int t = j & 1;
-          ok = wait_warp(&bars->v_full[vst], vph, abort);
-          if (ok) ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
+          ok = wait_spin(&bars->v_full[vst], vph, abort);
+          if (ok) ok = wait_spin(&bars->p_full[t], pc[t] & 1u, abort);
           ++pc[t];
           // the last segment's O is read out by both streams together
-          if (ok && j == 0 && oc[0] > 0) ok = wait_warp(&bars->o_free[0], (oc[0] - 1u) & 1u, abort);
+          if (ok && j == 0 && oc[0] > 0) ok = wait_spin(&bars->o_free[0], (oc[0] - 1u) & 1u, abort);
           if (!ok) break;
           tc05::fence_after_sync();
           const uint32_t va = v_lo + vst * (C::IB >> 4), pa = tbase + t * 256, od = tbase + t * 256 + 128;
@@ -827,12 +881,13 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           if (j + 2 < n) issue_next(j + 2);
         }
         ++oc[0];
+        if (++qbuf == nqb) qbuf = 0;
         continue;
       }
-      ok = wait_warp(&bars->k_full[ks], kph, abort);
+      ok = wait_spin(&bars->k_full[ks], kph, abort);
       for (int t = 0; t < 2 && ok; ++t) {
         if (sg.nt[t] == 0) continue;
-        ok = wait_warp(&bars->q_full[t], qc[t] & 1u, abort);
+        ok = wait_spin(&bars->q_full[t], qc[t] & 1u, abort);
         ++qc[t];
         if (!ok) break;
         tc05::fence_after_sync();
@@ -843,16 +898,16 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       commit_one(&bars->k_empty[ks]);
       if (++ks == NK) ks = 0, kph ^= 1u;
       for (int j = 0; ok && j < n; ++j) {
-        ok = wait_warp(&bars->v_full[vst], vph, abort);
+        ok = wait_spin(&bars->v_full[vst], vph, abort);
         if (!ok) break;
         tc05::fence_after_sync();
         const uint32_t va = v_lo + vst * (C::IB >> 4);
         bool k_ready = false;
         for (int t = 0; t < 2 && ok; ++t) {
           if (j >= sg.nt[t]) continue;
-          ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
+          ok = wait_spin(&bars->p_full[t], pc[t] & 1u, abort);
           ++pc[t];
-          if (ok && j == 0 && oc[t] > 0) ok = wait_warp(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
+          if (ok && j == 0 && oc[t] > 0) ok = wait_spin(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
           if (!ok) break;
           tc05::fence_after_sync();
           const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
@@ -864,7 +919,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           }
           __syncwarp();
           if (j + 1 < sg.nt[t]) {                      // the next S overwrites P, behind its product
-            ok = k_ready || wait_warp(&bars->k_full[ks], kph, abort);
+            ok = k_ready || wait_spin(&bars->k_full[ks], kph, abort);
             if (!ok) break;
             k_ready = true;
             tc05::fence_after_sync();
@@ -889,11 +944,11 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   }
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    make_v();
+    if (vi >= 0) make_v();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-    if (idle) {
-      make_v();
+    if (ALT && (warp & 3) >= nw) {                     // no rows
+      if (vi >= 0) make_v();
     } else {
     // ------------------------------------------------------- softmax, tile t
     const int t = (warp - 4) >> 2, r = threadIdx.x - 128 - t * kTRows;
@@ -933,9 +988,9 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       bool bad = false;
       for (int jj = 0; jj < nmine; ++jj) {
         const int blk = ALT ? 2 * jj + t : jj;         // block of the segment
-        ok = wait_warp(&bars->s_full[t], sc & 1u, abort);
+        ok = wait_spin(&bars->s_full[t], sc & 1u, abort);
         ++sc;
-        if (ok) ok = wait_warp(&bars->meta_full[(u0 + blk) % NM], (uint32_t)((u0 + blk) / NM) & 1u, abort);
+        if (ok) ok = wait_spin(&bars->meta_full[(u0 + blk) % NM], (uint32_t)((u0 + blk) / NM) & 1u, abort);
         if (!ok) break;
         tc05::fence_after_sync();
         const BlockMeta& mt = bars->meta[(u0 + blk) % NM];
@@ -1028,19 +1083,19 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         // join the streams: each posts (m, l) and reads the other's, and takes half of the columns of
         // both O, which lie in its own tensor-memory lanes
         if (nmine > 0) {
-          ok = wait_warp(&bars->pv_done[t], pvc & 1u, abort);
+          ok = wait_spin(&bars->pv_done[t], pvc & 1u, abort);
           ++pvc;
           if (!ok) break;
         }
         // the other stream has read what the last segment posted (it arrived here afterwards)
-        if (seg > 0) ok = wait_warp(&bars->o_free[0], (seg - 1u) & 1u, abort);
+        if (seg > 0) ok = wait_spin(&bars->o_free[0], (seg - 1u) & 1u, abort);
         if (!ok) break;
-        float2 (&xch)[2][ALT ? kTRows : 1] = bars->xch;
+        float2 (&xch)[2][ALT ? kAltRows : 1] = bars->xch;
         xch[t][r] = make_float2(m_ref, bad ? kBadRecord : l);
         tc05::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->x_full[t]);
-        ok = wait_warp(&bars->x_full[1 - t], seg & 1u, abort);
+        ok = wait_spin(&bars->x_full[1 - t], seg & 1u, abort);
         ++seg;
         if (!ok) break;
         tc05::fence_after_sync();
@@ -1101,7 +1156,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (!whole && valid) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
         continue;
       }
-      ok = wait_warp(&bars->pv_done[t], pvc & 1u, abort);
+      ok = wait_spin(&bars->pv_done[t], pvc & 1u, abort);
       ++pvc;
       if (!ok) break;
       tc05::fence_after_sync();
@@ -1152,7 +1207,9 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 }
 
 // Joins the items that crossed CTAs: block (x, y) takes rows 32 y .. 32 y + 31 of the item that
-// begins in CTA x and ends in a later one, a warp per row.
+// begins in CTA x and ends in a later one, eight threads a row with D / 8 columns each: first the
+// row's maxima and sums, then its records, every load independent of the others.
+//   M = max m_i,  L = sum l_i 2^(m_i - M),  out = sum acc_i 2^(m_i - M) / L
 template <int D, bool ALT>
 __global__ void __launch_bounds__(256)
 extend_join_kernel(const ExtTcParams p) {
@@ -1160,59 +1217,52 @@ extend_join_kernel(const ExtTcParams p) {
   const ExtTcSplit s = p.split[blockIdx.x];
   if (s.n == 0) return;
   const ExtendParams& e = p.e;
-  const int lane = threadIdx.x & 31;
-  xs::Seq sq;
-  xs::load_seq(e, s.b, sq);
-  const int TT = kTRows / e.G;
-  const float osc = p.scale_ptr ? __ldg(p.scale_ptr) : 1.f;
-  constexpr int C = D / 32;
-  for (int x = threadIdx.x >> 5; x < 32; x += 8) {
-    const int row = blockIdx.y * 32 + x, t = row / kTRows, r = row % kTRows;
-    const int tok = (ALT ? s.i : 2 * s.i + t) * TT + r / e.G;
-    if (r >= TT * e.G || tok >= sq.n) continue;
-    auto at = [&](int i) { return (size_t)(i == 0 ? s.first : 2 * ((int)blockIdx.x + i * e.c.Hkv)) * (2 * kTRows) + row; };
-    // weights, 32 records at a time with a running maximum (the sums as everywhere)
-    float M = -INFINITY, L = 0.f, acc[C];
-    bool bad = false;
-#pragma unroll
-    for (int y = 0; y < C; ++y) acc[y] = 0.f;
-    for (int i0 = 0; i0 < s.n; i0 += 32) {
-      const float2 ml = i0 + lane < s.n ? p.part_ml[at(i0 + lane)] : make_float2(-INFINITY, 0.f);
-      bad |= ml.y < 0.f;
-      float mx = ml.y > 0.f ? ml.x : -INFINITY;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float mn = fmaxf(M, mx);
-      const float a = mn == -INFINITY ? 1.f : exp2f(M - mn);
-      const float w = ml.y > 0.f ? exp2f(ml.x - mn) : 0.f;
-      float li = w * fmaxf(ml.y, 0.f);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) li += __shfl_xor_sync(0xffffffffu, li, o);
-      L = fmaf(L, a, li);
-      M = mn;
-#pragma unroll
-      for (int y = 0; y < C; ++y) acc[y] *= a;
-      const int n = min(32, s.n - i0);
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        if (wi > 0.f) {
-          const float* src = p.part_acc + at(i0 + i) * D + lane * C;
-#pragma unroll
-          for (int y = 0; y < C; ++y) acc[y] = fmaf(wi, src[y], acc[y]);
-        }
-      }
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    const size_t o = (size_t)(sq.q0 + tok) * e.c.Hq + s.h * e.G + r % e.G;
-    const bool none = bad || !(L > 0.f);
-    const float inv = none ? 0.f : osc / L;
-#pragma unroll
-    for (int y = 0; y < C; y += 2)
-      *reinterpret_cast<__half2*>(e.out + o * D + lane * C + y) =
-          none ? __floats2half2_rn(0.f, 0.f) : __floats2half2_rn(acc[y] * inv, acc[y + 1] * inv);
-    if (lane == 0 && e.lse) e.lse[o] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+  constexpr int C = D / 8;
+  const int row = blockIdx.y * 32 + (threadIdx.x >> 3), c0 = (threadIdx.x & 7) * C;
+  const int TT = e.tile_tokens, t = row / kTRows, r = row % kTRows;
+  const int q0 = __ldg(e.c.cu_q + s.b), n = __ldg(e.c.cu_q + s.b + 1) - q0;
+  const int tok = (ALT ? s.i : 2 * s.i + t) * TT + r / e.G;
+  if (r >= TT * e.G || tok >= n) return;
+  auto at = [&](int i) { return (size_t)(i == 0 ? s.first : 2 * ((int)blockIdx.x + i * e.c.Hkv)) * (2 * kTRows) + row; };
+  float M = -INFINITY, L = 0.f, acc[C];
+  bool bad = false;
+#pragma unroll 4
+  for (int i = 0; i < s.n; ++i) {
+    const float2 ml = p.part_ml[at(i)];
+    bad |= ml.y < 0.f;
+    if (ml.y > 0.f) M = fmaxf(M, ml.x);
   }
+#pragma unroll
+  for (int y = 0; y < C; ++y) acc[y] = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < s.n; ++i) {
+    const float2 ml = p.part_ml[at(i)];
+    const float4* src = reinterpret_cast<const float4*>(p.part_acc + at(i) * D + c0);
+    float4 v[C / 4];
+#pragma unroll
+    for (int y = 0; y < C / 4; ++y) v[y] = src[y];
+    if (!(ml.y > 0.f)) continue;                       // (a record without keys holds no sums)
+    const float w = exp2f(ml.x - M);
+    L = fmaf(w, ml.y, L);
+#pragma unroll
+    for (int y = 0; y < C / 4; ++y) {
+      acc[4 * y] = fmaf(w, v[y].x, acc[4 * y]);
+      acc[4 * y + 1] = fmaf(w, v[y].y, acc[4 * y + 1]);
+      acc[4 * y + 2] = fmaf(w, v[y].z, acc[4 * y + 2]);
+      acc[4 * y + 3] = fmaf(w, v[y].w, acc[4 * y + 3]);
+    }
+  }
+  const size_t o = (size_t)(q0 + tok) * e.c.Hq + s.h * e.G + r % e.G;
+  const bool none = bad || !(L > 0.f);
+  const float inv = none ? 0.f : (p.scale_ptr ? __ldg(p.scale_ptr) : 1.f) / L;
+#pragma unroll
+  for (int y = 0; y < C; y += 8) {
+    uint4 q = make_uint4(xt::pack2(acc[y] * inv, acc[y + 1] * inv), xt::pack2(acc[y + 2] * inv, acc[y + 3] * inv),
+                         xt::pack2(acc[y + 4] * inv, acc[y + 5] * inv), xt::pack2(acc[y + 6] * inv, acc[y + 7] * inv));
+    if (none) q = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(e.out + o * D + c0 + y) = q;
+  }
+  if (c0 == 0 && e.lse) e.lse[o] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------------- host
@@ -1234,12 +1284,12 @@ inline bool encode_group_map(CUtensorMap* tm, const void* base, int D, int Hkv, 
 
 // Query rows: 5-D view (d mod 64, g, d / 64, KV head, token) of q [T][Hq][D]; the box {64, G, 1, 1, TT}
 // lands TT * G rows of 128 B, row = token * G + g. Tokens past T read as zeros.
-inline bool encode_query_map(CUtensorMap* tm, const void* q, int D, int Hkv, int G, int T) {
+inline bool encode_query_map(CUtensorMap* tm, const void* q, int D, int Hkv, int G, int T, int tile_tokens) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[5] = {64, (cuuint64_t)G, (cuuint64_t)(D / 64), (cuuint64_t)Hkv, (cuuint64_t)T};
   cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)G * D * 2, (cuuint64_t)Hkv * G * D * 2};
-  cuuint32_t box[5] = {64, (cuuint32_t)G, 1, 1, (cuuint32_t)(kTRows / G)};
+  cuuint32_t box[5] = {64, (cuuint32_t)G, 1, 1, (cuuint32_t)tile_tokens};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(q), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
