@@ -20,7 +20,7 @@
 // Roles: warp 0 checks the pages and loads Q and K; warp 1 issues the MMAs; warp 2 owns tensor
 // memory; warp 3 loads FP16 value pages; warps 4-7 and 8-11 are the softmax of tile 0 and
 // 1, a thread per row; warps 12-15 load and
-// expand the other pages (ALT: eight warps, on other schedulers than the softmax where they can). The
+// expand the other pages. The
 // registers are split to match (setmaxnreg): 80, 176, 176 and 80 a thread, 512 = 4 x the 128 of launch. Tensor memory of tile t: S and P at 256 t, O at 256 t + 128. The order of
 // the MMAs and the lazily moved maximum are those of the prefill (prefill_tc05.cu). Every wait is
 // bounded; a timeout is reported and every role winds down.
@@ -67,7 +67,7 @@ struct XT {
   static constexpr int NK = (VM == kXFP16 || ALT ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 4)) + (ALT && D == 64 ? 1 : 0);
   static constexpr int NV = (D == 128 ? 2 : 4) + (ALT && VM == kXFP16 ? 1 : 0);
   static constexpr int NR = (D == 128 ? 2 : 4) + (ALT ? 1 : 0);
-  static constexpr int MK = ALT ? 8 : 4;               // maker warps
+  static constexpr int MK = 4;                         // maker warps
   static constexpr int PPW = kTPages / MK;             // pages of a block each
   // Block descriptions. One is written once the K stage NK + kMetaAhead + 1 blocks back is free, so
   // once that block's S is issued, which is behind the product of the block before (ALT: two before).
@@ -84,6 +84,7 @@ struct BlockMeta {
   uint8_t flags[kTPages];                   // xs::kSkip: not loaded
   uint8_t tiles;                            // bit per tile with blocks in the segment
   uint8_t last;                             // the CTA's last block
+  uint8_t z0, z1;                           // keys of the block that some row of the item sees: [z0, z1)
 };
 
 template <int D, int VM, bool ALT>
@@ -244,8 +245,10 @@ struct Items {
   __device__ __forceinline__ int jlo(int i) const { return lo(i) / kTKeys; }
   __device__ __forceinline__ int jhi(int i) const { return (hi(i) + kTKeys - 1) / kTKeys; }
   // blocks, and kItemCost each, of the items before i
+  template <bool ALT>
   __device__ __forceinline__ int before(int i) const {
     if (i <= 0) return 0;
+    if (ALT) return kItemCost + jhi(0) - jlo(0);      // (one item)
     const int full = i == np ? np - 1 : i;            // the last item may be short
     int s = kItemCost * i + floor_sum(full, kTKeys, step, t0 + step + kTKeys - 1);
     if (i == np) s += jhi(np - 1);
@@ -395,11 +398,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     return;
   }
-  // softmax warps per tile (ALT: those with rows), and the maker warps
-  const int nw = ALT ? p.nw : kTRows / 32;
-  int vi = warp - 12;                                  // index among the makers, < 0: none
-  if (ALT && nw == 1) vi = warp >= 12 ? warp - 13 : warp >= 10 ? warp - 4 : warp >= 5 && warp < 8 ? warp - 2 : -1;
-  if (ALT && nw == 2) vi = warp >= 14 ? warp - 14 : warp >= 12 ? warp - 6 : warp >= 10 ? warp - 6 : warp == 6 || warp == 7 ? warp - 4 : -1;
+  const int nw = ALT ? p.nw : kTRows / 32;             // softmax warps per tile (ALT: those with rows)
   constexpr bool kDirect = VM == kXFP16 || VM == kXMixed, kRaw = VM != kXFP16;
 
   if (threadIdx.x == 0) {
@@ -433,7 +432,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     Seq s;
     if (b >= c.batch || !load_seq(e, b, s) || !seq_ok(e, s)) return 0;
     const Items it = items_of<ALT>(e, s);
-    return it.before(it.np);
+    return it.before<ALT>(it.np);
   };
   const int tid = threadIdx.x;
   long long total = 0;
@@ -495,12 +494,12 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       int lo = 0, hi = it.np - 1;                      // the last item that begins at or before `off`
       while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (it.before(mid) <= off) lo = mid;
+        if (it.before<ALT>(mid) <= off) lo = mid;
         else hi = mid - 1;
       }
       bars->st_b = b0 + tid;
       bars->st_i = lo;
-      bars->st_j = it.jlo(lo) - kItemCost + off - it.before(lo);
+      bars->st_j = it.jlo(lo) - kItemCost + off - it.before<ALT>(lo);
     }
     carry += chunk;
   }
@@ -511,11 +510,13 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   w.j = bars->st_j;
   w.budget = w.b < 0 ? 0 : budget0;
   w.index = 0;
+  bool any = false;                                    // a block in the range
   if (w.budget > 0) {
     Seq sq;
     load_seq(e, w.b, sq);
     w.q0 = sq.q0;
     w.it = items_of<ALT>(e, sq);
+    any = w.j + w.budget > w.it.jlo(w.i);
   }
   const uint32_t tbase = bars->tmem_base;
   const int TT = e.tile_tokens;                        // tokens of a tile
@@ -523,122 +524,6 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   const int q_slab = (ALT ? 32 * nw : kTRows) * 128, q_buf = NB * q_slab;
   const int h_rows = TT * e.G;
 
-
-  // ------------------------------------------- the V stages (other pages than FP16 ones)
-  auto make_v = [&]() {
-    int u = 0, issued = 0;
-    uint32_t dir_ph = 0;                               // bit s: parity of v_dir[s]'s next phase
-    bool ok = true, last = false;
-    // this warp's raw pages of the next block that has none in flight: a ring of its own
-    auto issue = [&]() {
-      ok = wait_warp(&bars->meta_full[issued % NM], (uint32_t)(issued / NM) & 1u, abort);
-      if (!ok) return;
-      const BlockMeta& mt = bars->meta[issued % NM];
-      last = mt.last;
-      const int rs = issued % NR, pg = vi + (lane & (C::PPW - 1)) * C::MK;
-      uint64_t* bar = &bars->raw_full[rs][vi];
-      const int flags = lane < C::PPW ? mt.flags[pg] : xs::kSkip;
-      const bool mx = flags & xs::kMx, by = flags & (xs::kE4 | xs::kBs);
-      const uint32_t nmx = __popc(__ballot_sync(0xffffffffu, mx)), nby = __popc(__ballot_sync(0xffffffffu, by));
-      if (lane == 0) mbar_arrive_expect_tx(bar, nmx * micro_head_bytes(D) + nby * (kPage * D));
-      __syncwarp();
-      uint8_t* dst = sR + rs * C::RB + pg * (kPage * D);
-      if (mx)
-        bulk_load(dst, c.v_pages + (size_t)mt.page[pg] * c.v_page_stride + h * micro_head_bytes(D), micro_head_bytes(D), bar);
-      else if (by)
-        tma_load_4d(dst, &tv8, 0, h, 0, mt.page[pg], bar);
-      ++issued;
-    };
-    Segment sg;
-    while (ok && walk_next<ALT>(e, w, sg)) {
-      const int klo = sg.lo, khi = sg.hi;
-      if (kRaw && issued == 0)
-        while (ok && !last && issued < NR) issue();
-      for (int j = sg.ja; j < sg.jb && ok; ++j, ++u) {
-        const int vs = u % NV, rs = u % NR;
-        ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
-        if (ok && kRaw) ok = wait_warp(&bars->raw_full[rs][vi], (uint32_t)(u / NR) & 1u, abort);
-        if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
-        if (!ok) break;
-        const BlockMeta& mt = bars->meta[u % NM];
-        uint8_t* dv = sV + vs * C::IB;
-        const int flags = lane < kTPages ? mt.flags[lane] : xs::kSkip;
-        const uint32_t dmask = kDirect ? __ballot_sync(0xffffffffu, flags == 0) : 0u;
-        const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (flags & xs::kSkip));
-        // keys of the block that no row of the item sees: zero rows, whatever the pages hold
-        const int z0 = max(0, klo - j * kTKeys), z1 = min(kTKeys, khi - j * kTKeys);   // seen: [z0, z1)
-        const bool edge = z0 > 0 || z1 < kTKeys;
-        if (kRaw) {
-          // 16 codes of one token become two 16-byte chunks; the lanes of the second slab write
-          // theirs in the other order, so that eight lanes never meet in a bank
-          for (int i = 0; i < C::PPW; ++i) {
-            const int pg = vi + i * C::MK;
-            const int fl = __shfl_sync(0xffffffffu, flags, pg);
-            if (fl == 0 || (fl & xs::kSkip)) continue;
-            const uint8_t* src = sR + rs * C::RB + pg * (kPage * D);
-#pragma unroll 4
-            for (int x = lane; x < kPage * D / 16; x += 32) {
-              const int t = x / (D / 16), ch = x % (D / 16);
-              uint4 lo, hi;
-              if (VM == kXMicro || (VM == kXMixed && (fl & xs::kMx))) {
-                const uint2 codes = *reinterpret_cast<const uint2*>(src + t * (D / 2) + ch * 8);
-                uint32_t sb = src[micro_scale_off(D) + t * (D / kMicroBlock) + ch / 2];
-                if (!micro_scale_ok(sb)) {
-                  const int key = j * kTKeys + pg * kPage + t;
-                  if (key >= klo && key < khi) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SCALE, sg.b);
-                  sb = 0;
-                }
-                const __half2 s2 = micro_scale_h2(sb);
-                lo = micro_decode8(codes.x, s2);
-                hi = micro_decode8(codes.y, s2);
-              } else {
-                const uint32_t off = D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16);
-                const uint4 q = *reinterpret_cast<const uint4*>(src + off);
-                if (VM == kXMixed && (fl & xs::kBs)) {
-                  lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
-                                  __byte_perm(q.y, 0u, 0x3424));
-                  hi = make_uint4(__byte_perm(q.z, 0u, 0x1404), __byte_perm(q.z, 0u, 0x3424), __byte_perm(q.w, 0u, 0x1404),
-                                  __byte_perm(q.w, 0u, 0x3424));
-                } else {
-                  lo = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.x)), xs::bits(e4m3x2_to_half2((uint16_t)(q.x >> 16))),
-                                  xs::bits(e4m3x2_to_half2((uint16_t)q.y)), xs::bits(e4m3x2_to_half2((uint16_t)(q.y >> 16))));
-                  hi = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.z)), xs::bits(e4m3x2_to_half2((uint16_t)(q.z >> 16))),
-                                  xs::bits(e4m3x2_to_half2((uint16_t)q.w)), xs::bits(e4m3x2_to_half2((uint16_t)(q.w >> 16))));
-                }
-              }
-              const int c0 = 2 * (ch & 3), slab = ch >> 2, r = t & 7;
-              uint8_t* row = dv + (pg * 2 + (t >> 3)) * C::GB + slab * 1024 + r * 128;
-              const bool swap = slab & 1;
-              *reinterpret_cast<uint4*>(row + ((c0 + (swap ? 1 : 0)) ^ r) * 16) = swap ? hi : lo;
-              *reinterpret_cast<uint4*>(row + ((c0 + (swap ? 0 : 1)) ^ r) * 16) = swap ? lo : hi;
-            }
-          }
-          __syncwarp();
-        }
-        if (dmask && edge) {
-          ok = wait_warp(&bars->v_dir[vs], (dir_ph >> vs) & 1u, abort);
-          dir_ph ^= 1u << vs;
-          if (!ok) break;
-        }
-        if (edge || smask) {
-          for (int i = 0; i < C::PPW; ++i)
-            for (int x = lane; x < kPage * (D / 8); x += 32) {
-              const int pg = vi + i * C::MK, key = pg * kPage + x / (D / 8), ch = x % (D / 8);
-              if (key < z0 || key >= z1 || ((smask >> pg) & 1u))
-                *reinterpret_cast<uint4*>(dv + (key >> 3) * C::GB + (ch >> 3) * 1024 + (key & 7) * 128 + (ch & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
-        fence_async();                                 // written for the MMAs; the raw bytes read for their refill
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->v_full[vs]);
-        if (kRaw && !last) issue();
-      }
-    }
-    if (!ok && lane == 0) give_up(c.err, abort);
-    if (kRaw)
-      for (int v = max(0, issued - NR); v < issued; ++v) drain(&bars->raw_full[v % NR][vi], (uint32_t)(v / NR) & 1u);
-  };
 
   // (each register split stands at the head of its roles' code)
   if (warp < 4) {
@@ -653,7 +538,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     ExtTcSplit split;
     split.n = 0;
     struct Batch {
-      int b, j0, nb, plo, phi, qtok, tiles;            // qtok < 0: not a segment's first batch
+      int b, j0, nb, lo, hi, qtok, tiles;              // keys [lo, hi); qtok < 0: not a segment's first batch
     };
     Segment sg;
     sg.ja = sg.jb = 0;
@@ -676,13 +561,13 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       x.b = sg.b;
       x.j0 = sg.ja;
       x.nb = min(32 / kTPages, sg.jb - sg.ja);
-      x.plo = sg.lo / kPage;
-      x.phi = (sg.hi + kPage - 1) / kPage;
+      x.lo = sg.lo;
+      x.hi = sg.hi;
       sg.ja += x.nb;
     };
     auto in_batch = [&](const Batch& x) {
-      const int lp = x.j0 * kTPages + lane;
-      return lane < x.nb * kTPages && lp >= x.plo && lp < x.phi;
+      const int k0 = x.j0 * kTKeys + lane * kPage;
+      return lane < x.nb * kTPages && k0 + kPage > x.lo && k0 < x.hi;
     };
     auto ids = [&](const Batch& x) {
       return in_batch(x) ? __ldg(c.block_table + (size_t)x.b * c.bt_stride + x.j0 * kTPages + lane) : 0;
@@ -764,6 +649,8 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             mt.qtok = i == 0 ? b0.qtok : -1;
             mt.tiles = (uint8_t)b0.tiles;
             mt.last = i + 1 == b0.nb && b1.nb == 0;
+            mt.z0 = (uint8_t)max(0, b0.lo - (b0.j0 + i) * kTKeys);
+            mt.z1 = (uint8_t)min(kTKeys, b0.hi - (b0.j0 + i) * kTKeys);
           }
         }
         __syncwarp();
@@ -788,31 +675,30 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   } else if (warp == 3) {
     // ------------------------------------------------ loads of FP16 value pages
     int u = 0;
-    bool ok = kDirect;
-    Segment sg;
-    while (ok && walk_next<ALT>(e, w, sg)) {
-      for (int j = sg.ja; j < sg.jb && ok; ++j, ++u) {
-        const int vs = u % NV;
-        ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
-        if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
-        if (!ok) break;
-        const BlockMeta& mt = bars->meta[u % NM];
-        const int flags = lane < kTPages ? mt.flags[lane] : xs::kSkip;
-        const int page = lane < kTPages ? mt.page[lane] : 0;
-        // a stage with rows to zero is announced on a barrier of its own; they are zeroed once it has landed
-        const bool edge = sg.lo > j * kTKeys || sg.hi < (j + 1) * kTKeys;
-        const uint32_t dmask = __ballot_sync(0xffffffffu, flags == 0);
-        uint64_t* bar = edge ? &bars->v_dir[vs] : &bars->v_full[vs];
-        if (lane == 0) {
-          if (edge) mbar_arrive(&bars->v_full[vs]);
-          if (!edge || dmask) mbar_arrive_expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
-        }
-        __syncwarp();
-        if (flags == 0) tma_load_5d(sV + vs * C::IB + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + h * p.v16_head, bar);
+    bool ok = kDirect && any;
+    const bool run = ok;
+    for (bool last = false; ok && !last; ++u) {
+      const int vs = u % NV;
+      ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
+      if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
+      if (!ok) break;
+      const BlockMeta& mt = bars->meta[u % NM];
+      last = mt.last;
+      const int flags = lane < kTPages ? mt.flags[lane] : xs::kSkip;
+      const int page = lane < kTPages ? mt.page[lane] : 0;
+      // a stage with rows to zero is announced on a barrier of its own; they are zeroed once it has landed
+      const bool edge = mt.z0 > 0 || mt.z1 < kTKeys;
+      const uint32_t dmask = __ballot_sync(0xffffffffu, flags == 0);
+      uint64_t* bar = edge ? &bars->v_dir[vs] : &bars->v_full[vs];
+      if (lane == 0) {
+        if (edge) mbar_arrive(&bars->v_full[vs]);
+        if (!edge || dmask) mbar_arrive_expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
       }
+      __syncwarp();
+      if (flags == 0) tma_load_5d(sV + vs * C::IB + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + h * p.v16_head, bar);
     }
-    if (!ok && kDirect && lane == 0) give_up(c.err, abort);
-    if (kDirect)
+    if (!ok && run && lane == 0) give_up(c.err, abort);
+    if (run)
       for (int v = max(0, u - NV); v < u; ++v) drain(&bars->v_full[v % NV], (uint32_t)(v / NV) & 1u);
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer
@@ -944,12 +830,116 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   }
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (vi >= 0) make_v();
+    // ------------------------------- the V stages: pages vi and vi + 4 of every block
+    const int vi = warp - 12;
+    int issued = 0;
+    uint32_t dir_ph = 0;                               // bit s: parity of v_dir[s]'s next phase
+    bool ok = any, more = any;                 // more: blocks left to issue
+    const bool run = ok;
+    const int pg = vi + (lane & 1) * C::MK;            // lane 0's and lane 1's page
+    // this warp's raw pages of the next block that has none in flight: a ring of its own
+    auto issue = [&]() {
+      ok = wait_warp(&bars->meta_full[issued % NM], (uint32_t)(issued / NM) & 1u, abort);
+      if (!ok) return;
+      const BlockMeta& mt = bars->meta[issued % NM];
+      more = !mt.last;
+      if (kRaw) {
+        const int rs = issued % NR;
+        uint64_t* bar = &bars->raw_full[rs][vi];
+        const int flags = lane < 2 ? mt.flags[pg] : xs::kSkip;
+        const bool mx = flags & xs::kMx, by = flags & (xs::kE4 | xs::kBs);
+        const uint32_t nmx = __popc(__ballot_sync(0xffffffffu, mx)), nby = __popc(__ballot_sync(0xffffffffu, by));
+        if (lane == 0) mbar_arrive_expect_tx(bar, nmx * micro_head_bytes(D) + nby * (kPage * D));
+        __syncwarp();
+        uint8_t* dst = sR + rs * C::RB + pg * (kPage * D);
+        if (mx)
+          bulk_load(dst, c.v_pages + (size_t)mt.page[pg] * c.v_page_stride + h * micro_head_bytes(D), micro_head_bytes(D), bar);
+        else if (by)
+          tma_load_4d(dst, &tv8, 0, h, 0, mt.page[pg], bar);
+      }
+      ++issued;
+    };
+    // 16 codes of one token become two 16-byte chunks; the lanes of the second slab write theirs in the
+    // other order, so that eight lanes never meet in a bank
+    const int ch = lane % (D / 16), t0 = lane / (D / 16);      // chunk of 16 codes, first token
+    const uint32_t swap = (ch >> 2) & 1, c0 = 2 * (ch & 3) + swap;
+    for (int u = 0; ok && (more || u < issued); ++u) {
+      while (ok && more && issued < u + (kRaw ? NR : 1)) issue();
+      const int vs = u % NV, rs = u % NR;
+      if (ok && kRaw) ok = wait_warp(&bars->raw_full[rs][vi], (uint32_t)(u / NR) & 1u, abort);
+      if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
+      if (!ok) break;
+      const BlockMeta& mt = bars->meta[u % NM];
+      const bool edge = mt.z0 > 0 || mt.z1 < kTKeys;
+#pragma unroll 1
+      for (int i = 0; i < C::PPW; ++i) {
+        const int page = vi + i * C::MK;
+        const int fl = mt.flags[page];
+        uint8_t* dv = sV + vs * C::IB + page * (2 * C::GB);
+        const uint8_t* src = sR + rs * C::RB + page * (kPage * D);
+        if (kRaw && (fl & (xs::kMx | xs::kE4 | xs::kBs))) {
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {
+            const int t = t0 + x * (512 / D), r = t & 7;
+            uint4 lo, hi;
+            if (VM == kXMicro || (VM == kXMixed && (fl & xs::kMx))) {
+              const uint2 codes = *reinterpret_cast<const uint2*>(src + t * (D / 2) + ch * 8);
+              uint32_t sb = src[micro_scale_off(D) + t * (D / kMicroBlock) + ch / 2];
+              if (!micro_scale_ok(sb)) {
+                if (page * kPage + t >= mt.z0 && page * kPage + t < mt.z1)
+                  report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SCALE, -1);
+                sb = 0;
+              }
+              const __half2 s2 = micro_scale_h2(sb);
+              lo = micro_decode8(codes.x, s2);
+              hi = micro_decode8(codes.y, s2);
+            } else {
+              const uint4 q = *reinterpret_cast<const uint4*>(src + (D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16)));
+              if (VM == kXMixed && (fl & xs::kBs)) {
+                lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
+                                __byte_perm(q.y, 0u, 0x3424));
+                hi = make_uint4(__byte_perm(q.z, 0u, 0x1404), __byte_perm(q.z, 0u, 0x3424), __byte_perm(q.w, 0u, 0x1404),
+                                __byte_perm(q.w, 0u, 0x3424));
+              } else {
+                lo = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.x)), xs::bits(e4m3x2_to_half2((uint16_t)(q.x >> 16))),
+                                xs::bits(e4m3x2_to_half2((uint16_t)q.y)), xs::bits(e4m3x2_to_half2((uint16_t)(q.y >> 16))));
+                hi = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.z)), xs::bits(e4m3x2_to_half2((uint16_t)(q.z >> 16))),
+                                xs::bits(e4m3x2_to_half2((uint16_t)q.w)), xs::bits(e4m3x2_to_half2((uint16_t)(q.w >> 16))));
+              }
+            }
+            uint8_t* row = dv + (t >> 3) * C::GB + (ch >> 2) * 1024 + r * 128;
+            *reinterpret_cast<uint4*>(row + (c0 ^ r) * 16) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(row + (c0 ^ 1 ^ r) * 16) = swap ? lo : hi;
+          }
+        }
+      }
+      if (kDirect && edge && __any_sync(0xffffffffu, lane < kTPages && mt.flags[lane & (kTPages - 1)] == 0)) {
+        ok = wait_warp(&bars->v_dir[vs], (dir_ph >> vs) & 1u, abort);
+        dir_ph ^= 1u << vs;
+        if (!ok) break;
+      }
+      // keys that no row of the item sees, and pages that were not loaded: zeros, whatever they hold
+      const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (mt.flags[lane & (kTPages - 1)] & xs::kSkip));
+      if (edge || smask) {
+        __syncwarp();
+        for (int i = 0; i < C::PPW; ++i)
+          for (int x = lane; x < kPage * (D / 8); x += 32) {
+            const int page = vi + i * C::MK, key = page * kPage + x / (D / 8), c8 = x % (D / 8);
+            if (key < mt.z0 || key >= mt.z1 || ((smask >> page) & 1u))
+              *reinterpret_cast<uint4*>(sV + vs * C::IB + (key >> 3) * C::GB + (c8 >> 3) * 1024 + (key & 7) * 128 + (c8 & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+      }
+      fence_async();                                   // written for the MMAs; the raw bytes read for their refill
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->v_full[vs]);
+    }
+    if (!ok && run && lane == 0) give_up(c.err, abort);
+    if (kRaw)
+      for (int v = max(0, issued - NR); v < issued; ++v) drain(&bars->raw_full[v % NR][vi], (uint32_t)(v / NR) & 1u);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-    if (ALT && (warp & 3) >= nw) {                     // no rows
-      if (vi >= 0) make_v();
-    } else {
+    if (!ALT || (warp & 3) < nw) {                     // (the others have no rows)
     // ------------------------------------------------------- softmax, tile t
     const int t = (warp - 4) >> 2, r = threadIdx.x - 128 - t * kTRows;
     const uint32_t lanebase = static_cast<uint32_t>((warp & 3) * 32) << 16;
