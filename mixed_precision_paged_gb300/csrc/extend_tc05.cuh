@@ -17,10 +17,10 @@
 //     each; an item that crosses a border leaves partial rows (m, l, O) in at most two slots a CTA, and
 //     a second kernel joins them. Long causal chunks so balance to a block, and one short chunk
 //     behind a long prefix still uses every SM.
-// Roles: warp 0 checks the pages and loads Q and K; warp 1 issues the MMAs; warp 2 owns tensor
-// memory; warp 3 loads FP16 value pages; warps 4-7 and 8-11 are the softmax of tile 0 and
-// 1, a thread per row; warps 12-15 load and
-// expand the other pages. The
+// Roles: warp 0 checks the pages and loads Q and K; warp 1 issues the MMAs; warp 3 loads FP16 value
+// pages (warp 2 owns tensor memory); warps 4-7 and 8-11 are the softmax of tile 0 and
+// 1, a thread per row; the other warps load
+// and expand the other pages. The
 // registers are split to match (setmaxnreg): 80, 176, 176 and 80 a thread, 512 = 4 x the 128 of launch. Tensor memory of tile t: S and P at 256 t, O at 256 t + 128. The order of
 // the MMAs and the lazily moved maximum are those of the prefill (prefill_tc05.cu). Every wait is
 // bounded; a timeout is reported and every role winds down.
@@ -67,8 +67,9 @@ struct XT {
   static constexpr int NK = (VM == kXFP16 || ALT ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 4)) + (ALT && D == 64 ? 1 : 0);
   static constexpr int NV = (D == 128 ? 2 : 4) + (ALT && VM == kXFP16 ? 1 : 0);
   static constexpr int NR = (D == 128 ? 2 : 4) + (ALT ? 1 : 0);
-  static constexpr int MK = 4;                         // maker warps
-  static constexpr int PPW = kTPages / MK;             // pages of a block each
+  // maker warps: warps 2 and 13-15, warp 3 where no FP16 pages are to be loaded, and warp 12 where
+  // its scheduler does not have all of the softmax (ALT)
+  static constexpr int MK = VM == kXFP16 || VM == kXMixed ? 4 : ALT ? 5 : 6;
   // Block descriptions. One is written once the K stage NK + kMetaAhead + 1 blocks back is free, so
   // once that block's S is issued, which is behind the product of the block before (ALT: two before).
   static constexpr int NM = D == 128 ? 8 : 12;
@@ -526,7 +527,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 
 
   // (each register split stands at the head of its roles' code)
-  if (warp < 4) {
+  if (warp < 4 || warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   if (warp == 0) {
     // ------------------------------------------- producer: page checks, Q, K
@@ -672,10 +673,10 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     for (int v = max(0, k - NK); v < k; ++v) drain(&bars->k_full[v % NK], (v / NK) & 1);
     for (int t = 0; t < 2; ++t)
       if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
-  } else if (warp == 3) {
+  } else if (kDirect && warp == 3) {
     // ------------------------------------------------ loads of FP16 value pages
     int u = 0;
-    bool ok = kDirect && any;
+    bool ok = any;
     const bool run = ok;
     for (bool last = false; ok && !last; ++u) {
       const int vs = u % NV;
@@ -827,16 +828,18 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     if (!ok && lane == 0) give_up(c.err, abort);
     commit_one(&bars->mma_final);
     if (lane == 0) drain(&bars->mma_final, 0);
-  }
-  } else if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    // ------------------------------- the V stages: pages vi and vi + 4 of every block
-    const int vi = warp - 12;
+  } else if (C::MK == 6 || warp != 12) {
+    // ---------------------------- the V stages: pages vi, vi + MK of every block
+    // (index: C::MK 6: warps 2, 3, 12-15; 5: 13, 2, 3, 14, 15; 4: 13, 14, 15, 2)
+    const int vi = C::MK == 6 ? (warp < 4 ? warp - 2 : warp - 10)
+                   : C::MK == 5 ? (warp == 13 ? 0 : warp < 4 ? warp - 1 : warp - 11)
+                                : (warp < 4 ? 3 : warp - 13);
     int issued = 0;
     uint32_t dir_ph = 0;                               // bit s: parity of v_dir[s]'s next phase
     bool ok = any, more = any;                 // more: blocks left to issue
     const bool run = ok;
-    const int pg = vi + (lane & 1) * C::MK;            // lane 0's and lane 1's page
+    const int pg = min(vi + (lane & 1) * C::MK, kTPages - 1);   // lane 0's and lane 1's page
+    const bool two = vi + C::MK < kTPages;
     // this warp's raw pages of the next block that has none in flight: a ring of its own
     auto issue = [&]() {
       ok = wait_warp(&bars->meta_full[issued % NM], (uint32_t)(issued / NM) & 1u, abort);
@@ -846,7 +849,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       if (kRaw) {
         const int rs = issued % NR;
         uint64_t* bar = &bars->raw_full[rs][vi];
-        const int flags = lane < 2 ? mt.flags[pg] : xs::kSkip;
+        const int flags = lane == 0 || (lane == 1 && two) ? mt.flags[pg] : xs::kSkip;
         const bool mx = flags & xs::kMx, by = flags & (xs::kE4 | xs::kBs);
         const uint32_t nmx = __popc(__ballot_sync(0xffffffffu, mx)), nby = __popc(__ballot_sync(0xffffffffu, by));
         if (lane == 0) mbar_arrive_expect_tx(bar, nmx * micro_head_bytes(D) + nby * (kPage * D));
@@ -872,8 +875,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       const BlockMeta& mt = bars->meta[u % NM];
       const bool edge = mt.z0 > 0 || mt.z1 < kTKeys;
 #pragma unroll 1
-      for (int i = 0; i < C::PPW; ++i) {
-        const int page = vi + i * C::MK;
+      for (int page = vi; page < kTPages; page += C::MK) {
         const int fl = mt.flags[page];
         uint8_t* dv = sV + vs * C::IB + page * (2 * C::GB);
         const uint8_t* src = sR + rs * C::RB + page * (kPage * D);
@@ -922,9 +924,9 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (mt.flags[lane & (kTPages - 1)] & xs::kSkip));
       if (edge || smask) {
         __syncwarp();
-        for (int i = 0; i < C::PPW; ++i)
+        for (int page = vi; page < kTPages; page += C::MK)
           for (int x = lane; x < kPage * (D / 8); x += 32) {
-            const int page = vi + i * C::MK, key = page * kPage + x / (D / 8), c8 = x % (D / 8);
+            const int key = page * kPage + x / (D / 8), c8 = x % (D / 8);
             if (key < mt.z0 || key >= mt.z1 || ((smask >> page) & 1u))
               *reinterpret_cast<uint4*>(sV + vs * C::IB + (key >> 3) * C::GB + (c8 >> 3) * 1024 + (key & 7) * 128 + (c8 & 7) * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
@@ -937,6 +939,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     if (!ok && run && lane == 0) give_up(c.err, abort);
     if (kRaw)
       for (int v = max(0, issued - NR); v < issued; ++v) drain(&bars->raw_full[v % NR][vi], (uint32_t)(v / NR) & 1u);
+  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     if (!ALT || (warp & 3) < nw) {                     // (the others have no rows)
