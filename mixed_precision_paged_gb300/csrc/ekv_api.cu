@@ -702,7 +702,7 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
                  : uniform_mode == EKV_MODE_COMPACT_E4M3    ? kXE4M3
                                                             : kXMicro;
   cudaError_t e;
-  if ((long long)p.G * max_q <= (getenv("EKV_SPLIT") ? kXRows : 0)) {          // few query rows: the stream over the cache
+  if ((long long)p.G * max_q <= (getenv("EKV_SPLIT") ? atoi(getenv("EKV_SPLIT")) : 8)) {          // few query rows: the stream over the cache
     const int map_mode = vm == kXMixed ? kVMixed : vm == kXE4M3 ? kVE4M3 : kVFP16;
     CUtensorMap tm[3];
     // (a microscaled pool has small slots: no map over its values)

@@ -180,7 +180,7 @@ __device__ __forceinline__ int plan(const ExtendParams& e, int* cu, int* warp_to
 // One page per lane for 32 consecutive pages of the warp's range.
 struct Meta {
   int page, lp, b, flags;
-  float scale;
+  float lsc, ivs;          // log2 of an E4M3 page's scale, and its reciprocal
 };
 constexpr int kSkip = 1, kE4 = 2, kBs = 4, kMx = 8;
 
@@ -188,7 +188,8 @@ __device__ __forceinline__ void meta_ids(const ExtendParams& e, const int* cu, i
   m.page = m.lp = 0;
   m.flags = kSkip;
   m.b = -1;
-  m.scale = 1.f;
+  m.lsc = 0.f;
+  m.ivs = 1.f;
   if (k < n_my) {
     const int j = start + k;
     const int b = upper_bound_i(cu, e.c.batch + 1, j) - 1;
@@ -216,10 +217,12 @@ __device__ __forceinline__ void meta_mode(const ExtendParams& e, int h, Meta& m)
     if (mode > EKV_MODE_MICRO_FP4) {
       detail = EKV_DETAIL_PAGE_MODE;
     } else if (mode == EKV_MODE_COMPACT_E4M3) {
-      m.scale = !c.v_scales ? 0.f
-                            : __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)m.page * c.Hkv + h));
-      if (!scale_ok(m.scale)) detail = EKV_DETAIL_SCALE;
+      const float s = !c.v_scales ? 0.f
+                                  : __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)m.page * c.Hkv + h));
+      if (!scale_ok(s)) detail = EKV_DETAIL_SCALE;
       m.flags = kE4;
+      m.lsc = log2f(s);
+      m.ivs = 1.f / s;
     } else {
       m.flags = mode == EKV_MODE_BASE ? kBs : mode == EKV_MODE_MICRO_FP4 ? kMx : 0;
     }
@@ -265,10 +268,11 @@ __device__ __forceinline__ void fill(const ExtendParams& e, const Ring& ring, in
 
 // ---------------------------------------------------------------------- joining
 // Merges `nrec` records of KV head h, rows < n_b * G: record 0 at `first`, record i at rec0 + i * step;
-// to the record `dst`, or to the output when dst < 0. One warp; a row's records are staged by
-// 16-byte asynchronous copies in `buf` (its ring), up to 32 at a time.
+// to the record `dst`, or to the output when dst < 0.
 //   M = max m_i,  L = sum l_i 2^(m_i - M),  out = sum acc_i 2^(m_i - M) / L,  lse = (M + log2 L) ln 2.
-constexpr int kJoinMost = 128;                     // records of one call: groups of 1,216 ranges are 76
+// One warp. Several rows at a time, as many as their records fit `buf` (its ring): the acc rows by 16-byte
+// asynchronous copies and the (m, l) pairs by plain loads, all under way before any is used, so a
+// wave costs one round trip to L2. A row of more records than fit is taken in pieces with a running maximum.
 template <int D>
 __device__ void join(const ExtSplitParams& p, int h, const Seq& s, int first, int rec0, int step, int nrec, int dst,
                      uint8_t* buf, int buf_bytes) {
@@ -277,89 +281,102 @@ __device__ void join(const ExtSplitParams& p, int h, const Seq& s, int first, in
   const int R = s.n * e.G;
   constexpr int kRowB = D * 4;
   constexpr int C = D / 32;                        // columns per lane
-  constexpr int W = kJoinMost / 32;
-  const int cap = min(buf_bytes / kRowB, 32);
-  for (int row = 0; row < R; ++row) {
-    auto at = [&](int i) { return ((size_t)(i == 0 ? first : rec0 + i * step) * e.c.Hkv + h) * kXRows + row; };
-    float2 ml[W];
-    float M = -INFINITY, L = 0.f, w[W];
+  const int cap = min(buf_bytes / (kRowB + 8), 64);
+  float2* mls = reinterpret_cast<float2*>(buf + cap * kRowB);
+  const int rows = max(1, cap / nrec);             // rows of a wave
+  for (int row0 = 0; row0 < R; row0 += rows) {
+    const int nr = min(rows, R - row0);
+    float acc[C], M = -INFINITY, L = 0.f;
     bool bad = false;
+    for (int i0 = 0; i0 < nrec; i0 += cap) {       // (one piece, except for a row of many records)
+      const int ni = min(cap, nrec - i0), np = nr * ni;
+      auto at = [&](int q) {
+        const int i = i0 + q % ni;
+        return ((size_t)(i == 0 ? first : rec0 + i * step) * e.c.Hkv + h) * kXRows + row0 + q / ni;
+      };
+      float2 v[2];
 #pragma unroll
-    for (int y = 0; y < W; ++y) {
-      const int i = lane + 32 * y;
-      ml[y] = i < nrec ? __ldcg(p.part_ml + at(i)) : make_float2(-INFINITY, 0.f);
-    }
+      for (int y = 0; y < 2; ++y) v[y] = lane + 32 * y < np ? __ldcg(p.part_ml + at(lane + 32 * y)) : make_float2(0.f, 0.f);
+      for (int o = lane; o < np * (kRowB / 16); o += 32)
+        cp_async_16(buf + o * 16, reinterpret_cast<const uint8_t*>(p.part_acc + at(o / (kRowB / 16)) * D) + (o % (kRowB / 16)) * 16);
 #pragma unroll
-    for (int y = 0; y < W; ++y) {
-      bad |= ml[y].y < 0.f;
-      if (ml[y].y > 0.f) M = fmaxf(M, ml[y].x);
-    }
-    bad = __any_sync(0xffffffffu, bad);
+      for (int y = 0; y < 2; ++y)
+        if (lane + 32 * y < np) mls[lane + 32 * y] = v[y];
+      cp_async_wait_all();
+      __syncwarp();
+      for (int r = 0; r < nr; ++r) {
+        if (i0 == 0) {
+          M = -INFINITY;
+          L = 0.f;
+          bad = false;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-#pragma unroll
-    for (int y = 0; y < W; ++y) {
-      w[y] = ml[y].y > 0.f ? exp2f(ml[y].x - M) : 0.f;
-      L = fmaf(w[y], fmaxf(ml[y].y, 0.f), L);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    float acc[C];
-#pragma unroll
-    for (int x = 0; x < C; ++x) acc[x] = 0.f;
-#pragma unroll
-    for (int y = 0; y < W; ++y) {
-      const int ny = min(32, nrec - 32 * y);
-      for (int i0 = 0; i0 < ny; i0 += cap) {
-        const int n = min(cap, ny - i0);
-        for (int o = lane; o < n * (kRowB / 16); o += 32)
-          cp_async_16(buf + o * 16, reinterpret_cast<const uint8_t*>(p.part_acc + at(32 * y + i0 + o / (kRowB / 16)) * D) +
-                                        (o % (kRowB / 16)) * 16);
-        cp_async_wait_all();
-        __syncwarp();
-        for (int i = 0; i < n; ++i) {
-          const float wi = __shfl_sync(0xffffffffu, w[y], i0 + i);
-          const float* src = reinterpret_cast<const float*>(buf + i * kRowB) + lane * C;
-          if (wi > 0.f) {
-#pragma unroll
-            for (int x = 0; x < C; ++x) acc[x] = fmaf(wi, src[x], acc[x]);
-          }
+          for (int x = 0; x < C; ++x) acc[x] = 0.f;
         }
-        __syncwarp();
+        float Mn = M;
+        for (int i = 0; i < ni; ++i) {
+          const float2 ml = mls[r * ni + i];
+          bad |= ml.y < 0.f;
+          if (ml.y > 0.f) Mn = fmaxf(Mn, ml.x);
+        }
+        const float a = Mn == -INFINITY ? 1.f : exp2f(M - Mn);
+        M = Mn;
+        L *= a;
+#pragma unroll
+        for (int x = 0; x < C; ++x) acc[x] *= a;
+        for (int i = 0; i < ni; ++i) {
+          const float2 ml = mls[r * ni + i];
+          if (!(ml.y > 0.f)) continue;             // (a record without keys holds no sums)
+          const float w = exp2f(ml.x - M);
+          L = fmaf(w, ml.y, L);
+          const float* src = reinterpret_cast<const float*>(buf + (r * ni + i) * kRowB) + lane * C;
+#pragma unroll
+          for (int x = 0; x < C; ++x) acc[x] = fmaf(w, src[x], acc[x]);
+        }
+        if (i0 + ni < nrec) continue;
+        const int row = row0 + r;
+        if (dst >= 0) {
+          const size_t o = ((size_t)dst * e.c.Hkv + h) * kXRows + row;
+#pragma unroll
+          for (int x = 0; x < C; x += 2)
+            *reinterpret_cast<float2*>(p.part_acc + o * D + lane * C + x) = make_float2(acc[x], acc[x + 1]);
+          if (lane == 0) p.part_ml[o] = make_float2(M, bad ? kBadRecord : L);
+        } else {
+          const size_t o = (size_t)(s.q0 + row / e.G) * e.c.Hq + h * e.G + row % e.G;
+          const bool none = bad || !(L > 0.f);
+          const float inv = none ? 0.f : 1.f / L;
+#pragma unroll
+          for (int x = 0; x < C; x += 2)
+            *reinterpret_cast<__half2*>(e.out + o * D + lane * C + x) =
+                none ? __floats2half2_rn(0.f, 0.f) : __floats2half2_rn(acc[x] * inv, acc[x + 1] * inv);
+          if (lane == 0 && e.lse) e.lse[o] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        }
       }
-    }
-    if (dst >= 0) {
-      const size_t o = ((size_t)dst * e.c.Hkv + h) * kXRows + row;
-#pragma unroll
-      for (int x = 0; x < C; x += 2)
-        *reinterpret_cast<float2*>(p.part_acc + o * D + lane * C + x) = make_float2(acc[x], acc[x + 1]);
-      if (lane == 0) p.part_ml[o] = make_float2(M, bad ? kBadRecord : L);
-    } else {
-      const size_t o = (size_t)(s.q0 + row / e.G) * e.c.Hq + h * e.G + row % e.G;
-      const bool none = bad || !(L > 0.f);
-      const float inv = none ? 0.f : 1.f / L;
-#pragma unroll
-      for (int x = 0; x < C; x += 2)
-        *reinterpret_cast<__half2*>(e.out + o * D + lane * C + x) =
-            none ? __floats2half2_rn(0.f, 0.f) : __floats2half2_rn(acc[x] * inv, acc[x + 1] * inv);
-      if (lane == 0 && e.lse) e.lse[o] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+      __syncwarp();                                // the buffer is read before the next wave lands in it
     }
   }
 }
 
-// Takes a ticket; true for the warp that took the last of n (the counter is left at zero).
-__device__ __forceinline__ bool last_ticket(int* t, int n) {
-  int last = 0;
+// Takes a ticket on each of two counters (null: none) at once; bit x: this warp took the last of n[x] (the
+// counter is left at zero). One fence and one round trip for both.
+__device__ __forceinline__ uint32_t last_tickets(int* t0, int n0, int* t1, int n1) {
+  uint32_t last = 0;
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
     fence_acq_rel_gpu();                           // this warp's records first
-    last = atomicAdd(t, 1) == n - 1;
-    if (last) {
-      *t = 0;
-      fence_acq_rel_gpu();                         // and the others' before they are read
+    int o0 = -1, o1 = -1;
+    if (t0) o0 = atomicAdd(t0, 1);
+    if (t1) o1 = atomicAdd(t1, 1);
+    if (t0 && o0 == n0 - 1) {
+      *t0 = 0;
+      last |= 1u;
     }
+    if (t1 && o1 == n1 - 1) {
+      *t1 = 0;
+      last |= 2u;
+    }
+    if (last) fence_acq_rel_gpu();                 // and the others' before they are read
   }
-  return __shfl_sync(0xffffffffu, last, 0) != 0;
+  return __shfl_sync(0xffffffffu, last, 0);
 }
 
 }  // namespace xs
@@ -415,6 +432,9 @@ extend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   const int q4 = lane & 3, r8 = lane >> 2;
   const int lm_t = (lane & 7) + ((lane >> 3) & 1) * 8, lm_c = lane >> 4;   // ldmatrix row and 16-byte chunk of this lane
 
+  // one scale for every code of the pool scales the output instead
+  const bool scaled = VM == kXMixed || (VM == kXE4M3 && c.scale_mode == EKV_SCALE_PER_PAGE_HEAD);
+  const float osc = VM == kXE4M3 && !scaled ? __ldg(c.v_scales) : 1.f;
   Meta cur, nxt, nxt2;
   meta_ids(e, cu, start, n_my, lane, cur);
   meta_ids(e, cu, start, n_my, 32 + lane, nxt);
@@ -496,7 +516,8 @@ extend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       }
       const int flags = __shfl_sync(0xffffffffu, cur.flags, k & 31);
       const int key0 = __shfl_sync(0xffffffffu, cur.lp, k & 31) * kPage;
-      const float vs = __shfl_sync(0xffffffffu, cur.scale, k & 31);
+      const float lsc = scaled ? __shfl_sync(0xffffffffu, cur.lsc, k & 31) : 0.f;
+      const float ivs = scaled ? __shfl_sync(0xffffffffu, cur.ivs, k & 31) : 1.f;
       const bool skip = (flags & kSkip) != 0;
       const bool e4 = VM == kXE4M3 || (VM == kXMixed && (flags & kE4));
       const bool bs = VM == kXMixed && (flags & kBs);
@@ -649,7 +670,6 @@ extend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
           }
       } else {
         // ---- scores in log2 units, E4M3 scale included; tokens r8 and r8 + 8
-        const float lsc = e4 ? log2f(vs) : 0.f;
         const bool partial = key0 < full_lo || key0 + kPage - 1 > full_hi;
         bool grows = false;
         float mxs[NT][2];
@@ -706,7 +726,6 @@ extend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             va[y][3] &= mhi;
           }
         }
-        const float ivs = e4 ? 1.f / vs : 1.f;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
           if (i >= nt) continue;
@@ -744,7 +763,7 @@ extend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
         const bool bad = (bad_rows >> (2 * i + x)) & 1u;
         if (whole) {
           const size_t o = (size_t)(sq.q0 + row / G) * c.Hq + h * G + row % G;
-          const float inv = bad || !(t > 0.f) ? 0.f : 1.f / t;
+          const float inv = bad || !(t > 0.f) ? 0.f : osc / t;
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
             uint2 u;
@@ -753,41 +772,56 @@ extend_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             if (bad) u = make_uint2(0u, 0u);
             *reinterpret_cast<uint2*>(e.out + o * D + 32 * j + 4 * r8) = u;
           }
-          if (r8 == 0 && e.lse) e.lse[o] = inv > 0.f ? (m[i][x] + log2f(t)) * 0.69314718055994531f : -INFINITY;
+          if (r8 == 0 && e.lse) e.lse[o] = !bad && t > 0.f ? (m[i][x] + log2f(t)) * 0.69314718055994531f : -INFINITY;
         } else {
           const size_t o = ((size_t)rec * Hkv + h) * kXRows + row;
 #pragma unroll
           for (int j = 0; j < D / 32; ++j)
             *reinterpret_cast<float4*>(p.part_acc + o * D + 32 * j + 4 * r8) =
-                make_float4(acc[i][2 * j][x], acc[i][2 * j][2 + x], acc[i][2 * j + 1][x], acc[i][2 * j + 1][2 + x]);
+                make_float4(acc[i][2 * j][x] * osc, acc[i][2 * j][2 + x] * osc, acc[i][2 * j + 1][x] * osc, acc[i][2 * j + 1][2 + x] * osc);
           if (r8 == 0) p.part_ml[o] = make_float2(m[i][x], bad ? kBadRecord : t);
         }
       }
     }
   }
   // ---- joining: the sequences that continue in other ranges (a range's first and last segment at most)
-  for (int side = 0; side < 2; ++side) {
-    const int b = side == 0 ? b_first : b_last;
-    if ((side == 1 && b_last == b_first) || cu[b] == cu[b + 1] || (cu[b] >= start && cu[b + 1] <= end)) continue;
-    Seq sq;
-    load_seq(e, b, sq);
-    int v0, n;
-    ranges_of(cu, b, per, v0, n);
+  struct Side {
+    int b, v0, n, first, gv, gn, gfirst;           // sequence, its ranges, its first record; this range's group
+    int* ticket;
+  } side[2];
+  auto open = [&](int b, Side& x) {
+    x.ticket = nullptr;
+    if (cu[b] == cu[b + 1] || (cu[b] >= start && cu[b + 1] <= end)) return;
+    x.b = b;
+    ranges_of(cu, b, per, x.v0, x.n);
     // range v0 may begin inside the sequence before: then b is its last segment there
-    const int first = 2 * v0 + (page_at(cu, batch, v0 * per) < cu[b] ? 1 : 0);
+    x.first = 2 * x.v0 + (page_at(cu, batch, x.v0 * per) < cu[b] ? 1 : 0);
+    const int g = x.n <= kJoin ? 0 : (v - x.v0) / kJoin;
+    x.gv = x.v0 + g * kJoin;
+    x.gn = min(kJoin, x.n - g * kJoin);
+    x.gfirst = g == 0 ? x.first : 2 * x.gv;
+    x.ticket = x.n <= kJoin ? p.ticket + b * kMaxKvHeads + h : p.group_ticket + (2 * x.gv + (g == 0 ? 1 : 0)) * Hkv + h;
+  };
+  open(b_first, side[0]);
+  if (b_last != b_first) open(b_last, side[1]);
+  else side[1].ticket = nullptr;
+  if (!side[0].ticket && !side[1].ticket) return;
+  const uint32_t last = last_tickets(side[0].ticket, side[0].ticket ? side[0].gn : 0, side[1].ticket, side[1].ticket ? side[1].gn : 0);
+  for (int x = 0; x < 2; ++x) {
+    if (!((last >> x) & 1u)) continue;
+    const Side& d = side[x];
+    Seq sq;
+    load_seq(e, d.b, sq);
     uint8_t* buf = ring.k;
     const int bytes = ring.nsl * S::kK;
-    if (n <= kJoin) {
-      if (last_ticket(p.ticket + b * kMaxKvHeads + h, n)) join<D>(p, h, sq, first, 2 * v0, 2, n, -1, buf, bytes);
+    if (d.n <= kJoin) {
+      join<D>(p, h, sq, d.first, 2 * d.v0, 2, d.n, -1, buf, bytes);
       continue;
     }
-    const int g = (v - v0) / kJoin, groups = (n + kJoin - 1) / kJoin;
-    const int gv = v0 + g * kJoin, gn = min(kJoin, n - g * kJoin);
-    const int gfirst = g == 0 ? first : 2 * gv;
-    if (!last_ticket(p.group_ticket + (2 * gv + (g == 0 ? 1 : 0)) * Hkv + h, gn)) continue;
-    join<D>(p, h, sq, gfirst, 2 * gv, 2, gn, gfirst, buf, bytes);
-    if (last_ticket(p.ticket + b * kMaxKvHeads + h, groups))
-      join<D>(p, h, sq, first, 2 * v0, 2 * kJoin, groups, -1, buf, bytes);
+    join<D>(p, h, sq, d.gfirst, 2 * d.gv, 2, d.gn, d.gfirst, buf, bytes);
+    const int groups = (d.n + kJoin - 1) / kJoin;
+    if (last_tickets(p.ticket + d.b * kMaxKvHeads + h, groups, nullptr, 0))
+      join<D>(p, h, sq, d.first, 2 * d.v0, 2 * kJoin, groups, -1, buf, bytes);
   }
 }
 
