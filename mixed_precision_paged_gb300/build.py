@@ -23,8 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libekv.so")
 TEST_LIB = os.path.join(HERE, "libekv_waittest.so")
-SOURCES = ["ekv_api.cu", "decode_simt.cu", "decode_mma.cu", "gather_demote.cu", "append_rope.cu", "extend_split_d64.cu", "extend_split_d128.cu", "extend_tc05_d64.cu",
-           "extend_tc05_d128.cu",
+SOURCES = ["ekv_api.cu", "decode_simt.cu", "decode_mma.cu", "gather_demote.cu", "append_rope.cu", "extend_tc05_d64.cu", "extend_tc05_d128.cu",
            "noalloc.cu", "prefill_mma.cu", "prefill_tc05.cu"]
 # translation units that see DecodeParams or the wait bound: rebuilt for the test library
 TEST_SOURCES = ["ekv_api.cu", "decode_simt.cu", "decode_mma.cu", "noalloc.cu"]

@@ -22,8 +22,6 @@ cudaError_t launch_split_simt(const CUtensorMap& tk, const CUtensorMap& t8, cons
 cudaError_t launch_split_mma(const CUtensorMap& tk, const CUtensorMap& t8, const CUtensorMap& t16,
                              const DecodeParams& p, int D, int vmode, int grid, size_t smem, cudaStream_t st);
 
-cudaError_t launch_extend_split_64(const CUtensorMap (&tm)[3], const ExtSplitParams& p, int vm, int grid, cudaStream_t st);
-cudaError_t launch_extend_split_128(const CUtensorMap (&tm)[3], const ExtSplitParams& p, int vm, int grid, cudaStream_t st);
 
 cudaError_t launch_extend_tc05_64(const ExtTcMaps& m, const ExtTcParams& p, int vm, int grid, cudaStream_t st);
 cudaError_t launch_extend_tc05_128(const ExtTcMaps& m, const ExtTcParams& p, int vm, int grid, cudaStream_t st);
@@ -70,10 +68,9 @@ struct ekv_ctx {
   float* part_acc = nullptr;
   float2* part_ml = nullptr;
   int* plan = nullptr;
-  // attention of new tokens: partial rows (two segments per range or CTA) and group tickets
+  // attention of new tokens: partial rows (two segments per CTA), and the items that cross CTAs
   float* ext_acc = nullptr;
   float2* ext_ml = nullptr;
-  int* ext_ticket = nullptr;
   ExtTcSplit* ext_split = nullptr;
   int* err = nullptr;
   cudaStream_t last_stream = nullptr;
@@ -128,10 +125,8 @@ int last_kernel(cudaStream_t st) {
 int g_inject_timeout_calls = 0;
 #endif
 
-// Rows of the partial results of ekv_extend_attention: two segments of kXRows rows per page range
-// and KV head (8 / H_kv ranges per CTA), and its group tickets.
-size_t ext_rows(const ekv_ctx* c) { return (size_t)c->split_ctas * 2 * kXWarps * kXRows; }
-size_t ext_tickets(const ekv_ctx* c) { return (size_t)c->split_ctas * 2 * kXWarps; }
+// Partial rows of ekv_extend_attention: two segments of a pair of query tiles per CTA.
+size_t ext_rows(const ekv_ctx* c) { return (size_t)c->split_ctas * 2 * 2 * kTRows; }
 
 bool supported_shape(int Hq, int Hkv, int D) {
   if (D != 64 && D != 128) return false;
@@ -182,9 +177,7 @@ ekv_status ekv_create(ekv_ctx** out, const ekv_config* cfg) {
             cudaMalloc(&c->plan, kPlanInts * sizeof(int)) == cudaSuccess &&
             cudaMalloc(&c->ext_acc, ext_rows(c) * cfg->head_dim * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&c->ext_ml, ext_rows(c) * sizeof(float2)) == cudaSuccess &&
-            cudaMalloc(&c->ext_ticket, ext_tickets(c) * sizeof(int)) == cudaSuccess &&
             cudaMalloc(&c->ext_split, c->split_ctas * sizeof(ExtTcSplit)) == cudaSuccess &&
-            cudaMemset(c->ext_ticket, 0, ext_tickets(c) * sizeof(int)) == cudaSuccess &&
             cudaMalloc(&c->err, 4 * sizeof(int)) == cudaSuccess &&
             cudaMemset(c->plan, 0, kPlanInts * sizeof(int)) == cudaSuccess &&
             cudaMemset(c->err, 0, 4 * sizeof(int)) == cudaSuccess &&
@@ -207,7 +200,6 @@ ekv_status ekv_destroy(ekv_ctx* c) {
   cudaFree(c->plan);
   cudaFree(c->ext_acc);
   cudaFree(c->ext_ml);
-  cudaFree(c->ext_ticket);
   cudaFree(c->ext_split);
   cudaFree(c->err);
   delete c;
@@ -701,52 +693,32 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
                  : uniform_mode == EKV_MODE_TARGET_FP16     ? kXFP16
                  : uniform_mode == EKV_MODE_COMPACT_E4M3    ? kXE4M3
                                                             : kXMicro;
-  cudaError_t e;
-  if ((long long)p.G * max_q <= (getenv("EKV_SPLIT") ? atoi(getenv("EKV_SPLIT")) : 8)) {          // few query rows: the stream over the cache
-    const int map_mode = vm == kXMixed ? kVMixed : vm == kXE4M3 ? kVE4M3 : kVFP16;
-    CUtensorMap tm[3];
-    // (a microscaled pool has small slots: no map over its values)
-    if (!decode_pool_maps(&tm[0], &tm[1], &tm[2], k_pages, v_pages, D, Hkv, num_pages,
-                          vm == kXMicro ? 2ll * kPage * Hkv * D : v_page_stride_bytes, map_mode))
-      return EKV_ERR_INVALID_ARG;
-    ExtSplitParams x;
-    memset(&x, 0, sizeof(x));
-    x.e = p;
-    x.part_acc = c->ext_acc;
-    x.part_ml = c->ext_ml;
-    x.ticket = c->plan + kPlanTicket;
-    x.group_ticket = c->ext_ticket;
-    x.NG = c->NG;
-    e = D == 128 ? launch_extend_split_128(tm, x, vm, c->split_ctas, st)
-                 : launch_extend_split_64(tm, x, vm, c->split_ctas, st);
-  } else {
-    ExtTcMaps m;
-    memset(&m, 0, sizeof(m));
-    ExtTcParams x;
-    memset(&x, 0, sizeof(x));
-    x.e = p;
-    x.part_acc = c->ext_acc;
-    x.part_ml = c->ext_ml;
-    x.split = c->ext_split;
-    // few rows: one tile, its key blocks alternating between the softmax groups
-    const long long rows = (long long)p.G * max_q;
-    x.nw = rows <= kAltRows ? (int)((rows + 31) / 32) : 0;
-    x.e.tile_tokens = (x.nw > 0 ? 32 * x.nw : kTRows) / p.G;
-    // one coordinate for (page, head): in units that divide both the page stride and a head's row
-    int unit = 2 * D;
-    while (v_page_stride_bytes % unit) unit /= 2;
-    const long long places = (long long)num_pages * (v_page_stride_bytes / unit);
-    if ((long long)num_pages * kPage * Hkv > 0x7fffffffLL || places > 0x7fffffffLL) return EKV_ERR_UNSUPPORTED;
-    x.v16_mul = (int)(v_page_stride_bytes / unit);
-    x.v16_head = 2 * D / unit;
-    if (!encode_query_map(&m.q, q, D, Hkv, p.G, total_q, x.e.tile_tokens) ||
-        !encode_group_map(&m.k, k_pages, D, Hkv, (unsigned long long)num_pages * kPage * Hkv, 2 * D))
-      return EKV_ERR_INVALID_ARG;
-    if ((vm == kXFP16 || vm == kXMixed) && !encode_group_map(&m.v16, v_pages, D, Hkv, places, unit)) return EKV_ERR_INVALID_ARG;
-    if ((vm == kXE4M3 || vm == kXMixed) && !encode_e4m3_slice_map(&m.v8, v_pages, D, Hkv, num_pages, v_page_stride_bytes))
-      return EKV_ERR_INVALID_ARG;
-    e = D == 128 ? launch_extend_tc05_128(m, x, vm, c->split_ctas, st) : launch_extend_tc05_64(m, x, vm, c->split_ctas, st);
-  }
+  ExtTcMaps m;
+  memset(&m, 0, sizeof(m));
+  ExtTcParams x;
+  memset(&x, 0, sizeof(x));
+  x.e = p;
+  x.part_acc = c->ext_acc;
+  x.part_ml = c->ext_ml;
+  x.split = c->ext_split;
+  // few rows: one tile, its key blocks alternating between the softmax groups
+  const long long rows = (long long)p.G * max_q;
+  x.nw = rows <= kAltRows ? (int)((rows + 31) / 32) : 0;
+  x.e.tile_tokens = (x.nw > 0 ? 32 * x.nw : kTRows) / p.G;
+  // one coordinate for (page, head): in units that divide both the page stride and a head's row
+  int unit = 2 * D;
+  while (v_page_stride_bytes % unit) unit /= 2;
+  const long long places = (long long)num_pages * (v_page_stride_bytes / unit);
+  if ((long long)num_pages * kPage * Hkv > 0x7fffffffLL || places > 0x7fffffffLL) return EKV_ERR_UNSUPPORTED;
+  x.v16_mul = (int)(v_page_stride_bytes / unit);
+  x.v16_head = 2 * D / unit;
+  if (!encode_query_map(&m.q, q, D, Hkv, p.G, total_q, x.e.tile_tokens) ||
+      !encode_group_map(&m.k, k_pages, D, Hkv, (unsigned long long)num_pages * kPage * Hkv, 2 * D))
+    return EKV_ERR_INVALID_ARG;
+  if ((vm == kXFP16 || vm == kXMixed) && !encode_group_map(&m.v16, v_pages, D, Hkv, places, unit)) return EKV_ERR_INVALID_ARG;
+  if ((vm == kXE4M3 || vm == kXMixed) && !encode_e4m3_slice_map(&m.v8, v_pages, D, Hkv, num_pages, v_page_stride_bytes))
+    return EKV_ERR_INVALID_ARG;
+  const cudaError_t e = D == 128 ? launch_extend_tc05_128(m, x, vm, c->split_ctas, st) : launch_extend_tc05_64(m, x, vm, c->split_ctas, st);
   if (e != cudaSuccess) return EKV_ERR_CUDA;
   note_launch(st, kAfterReader);
   return EKV_OK;
@@ -801,7 +773,6 @@ ekv_status ekv_get_error(ekv_ctx* c, int* code, int* detail) {
   // a clean plan buffer: no stale tickets. Only the context's stream is synchronised.
   if (cudaStreamSynchronize(st) != cudaSuccess) return EKV_ERR_CUDA;
   if (h[0] != 0 && (cudaMemsetAsync(c->plan, 0, kPlanInts * sizeof(int), st) != cudaSuccess ||
-                    cudaMemsetAsync(c->ext_ticket, 0, ext_tickets(c) * sizeof(int), st) != cudaSuccess ||
                     cudaStreamSynchronize(st) != cudaSuccess))
     return EKV_ERR_CUDA;
   if (code) *code = h[0];

@@ -1,5 +1,5 @@
-// extend_tc05.cuh -- attention of many new tokens per sequence over the paged cache (prompt
-// chunks behind a cached prefix) on the fifth-generation tensor cores.
+// extend_tc05.cuh -- attention of new tokens over the paged cache (decode steps, draft
+// verification, prompt chunks behind a cached prefix) on the fifth-generation tensor cores.
 //
 // For a block of 128 keys and a tile of 128 query rows the work is two products,
 //   S = Q K^T,  O += P V,  P = 2^(S sm_scale log2 e - m),
@@ -12,7 +12,10 @@
 //     which serve as K-major B of S and, for V, as N-major B of the second product.
 //   * values: FP16 pages land in a V stage directly. E4M3, BASE and microscaled pages land raw, each
 //     maker warp's in a ring of its own, and are expanded into the V stage, exactly; E4M3 scales join the
-//     exponent as in the split kernel (extend_split.cuh), or the output when one scale serves all.
+//     exponent, p' = 2^(score + log2 scale - m) with the maximum m over the scaled scores, and the sum
+//     takes p' / scale: so codes enter the product exactly as they are, and p' is rounded to fp16
+//     once relative to the largest contribution, whatever the scales; one scale for all codes
+//     scales the output instead. A microscaled value is code * 2^k, exact in fp16.
 //   * split: the blocks of all items form one stream, cut into equal ranges, one persistent CTA
 //     each; an item that crosses a border leaves partial rows (m, l, O) in at most two slots a CTA, and
 //     a second kernel joins them. Long causal chunks so balance to a block, and one short chunk
@@ -26,12 +29,16 @@
 // bounded; a timeout is reported and every role winds down.
 #pragma once
 
-#include "extend_split.cuh"
+#include "extend.cuh"
+#include "micro.cuh"
 #include "pool_maps.h"
 #include "tc05.cuh"
 
 namespace ekv {
 
+enum ExtVMode { kXFP16 = 0, kXE4M3 = 1, kXMicro = 2, kXMixed = 3 };   // forms of a launch's value pages
+
+constexpr float kBadRecord = -1.f;          // l of a row that saw a page which failed its checks
 constexpr int kTRows = 128;                 // rows of a query tile (MMA M)
 constexpr int kTKeys = 128;                 // keys of a block (N of S)
 constexpr int kTPages = kTKeys / kPage;
@@ -82,7 +89,7 @@ struct BlockMeta {
   float ivs[kTPages];                       // and its reciprocal
   int bad;                                  // bit per page that failed its checks
   int qtok;                                 // a segment's first block: first row of its queries; else -1
-  uint8_t flags[kTPages];                   // xs::kSkip: not loaded
+  uint8_t flags[kTPages];                   // kSkip: not loaded
   uint8_t tiles;                            // bit per tile with blocks in the segment
   uint8_t last;                             // the CTA's last block
   uint8_t z0, z1;                           // keys of the block that some row of the item sees: [z0, z1)
@@ -102,7 +109,7 @@ struct XTBars {
   uint64_t x_full[2];                       // ALT: a stream's (m, l) of the segment posted
   float2 xch[2][ALT ? kAltRows : 1];
   BlockMeta meta[C::NM];
-  long long red[kT5Threads / 32];
+  long long red[kT5Threads / 32], rest[kT5Threads / 32];
   int st_b, st_i, st_j;               // where this CTA's range begins
   uint32_t tmem_base;
   int abort;
@@ -116,9 +123,42 @@ constexpr int xt_smem_bytes() {
 
 namespace xt {
 
-using xs::Seq;
-using xs::load_seq;
-using xs::seq_ok;
+constexpr int kSkip = 1, kE4 = 2, kBs = 4, kMx = 8;   // a page's flags: not loaded; its form (FP16: 0)
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// One sequence's part in the plan.
+struct Seq {
+  int L, n, q0;            // tokens, new tokens, first row of q
+};
+
+// Reads sequence b; false (nothing to attend) when it is empty or fails its checks.
+__device__ __forceinline__ bool load_seq(const ExtendParams& e, int b, Seq& s) {
+  const CacheView& c = e.c;
+  s.q0 = __ldg(c.cu_q + b);
+  s.n = __ldg(c.cu_q + b + 1) - s.q0;
+  s.L = __ldg(c.seq_lens + b);
+  return s.n != 0;
+}
+__device__ __forceinline__ bool seq_ok(const ExtendParams& e, const Seq& s) {
+  return s.n > 0 && s.n <= s.L && s.n <= e.max_q && s.q0 >= 0 && (long long)s.q0 + s.n <= e.c.total_q &&
+         (long long)s.L <= (long long)e.c.bt_stride * kPage;
+}
+
+// Zero rows and -inf lse of sequence b's new tokens.
+__device__ __forceinline__ void zero_rows(const ExtendParams& e, const Seq& s) {
+  const CacheView& c = e.c;
+  const int r0 = max(s.q0, 0), r1 = (int)min((long long)s.q0 + s.n, (long long)c.total_q);
+  const long long n = (long long)max(0, r1 - r0) * c.Hq;
+  for (long long i = threadIdx.x; i < n * c.D; i += blockDim.x) e.out[(long long)r0 * c.Hq * c.D + i] = __float2half(0.f);
+  if (e.lse)
+    for (long long i = threadIdx.x; i < n; i += blockDim.x) e.lse[(long long)r0 * c.Hq + i] = -INFINITY;
+}
 
 // try_wait with a suspend-time hint: the warp sleeps in hardware until the phase ends instead of
 // polling. A dozen warps of a CTA wait at any time, and their polls cost the others' shared-memory
@@ -414,7 +454,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     for (int s = 0; s < NK; ++s) mbar_init(&bars->k_full[s], 1), mbar_init(&bars->k_empty[s], 1);
     for (int s = 0; s < NR; ++s)
-      for (int x = 0; x < C::MK; ++x) mbar_init(&bars->raw_full[s][x], 1);
+      for (int x = 0; x < C::MK; ++x) mbar_init(&bars->raw_full[s][x], x + C::MK < kTPages ? 2 : 1);
     for (int s = 0; s < NV; ++s) mbar_init(&bars->v_full[s], C::MK + (kDirect ? 1 : 0)), mbar_init(&bars->v_empty[s], 1), mbar_init(&bars->v_dir[s], 1);
     for (int s = 0; s < NM; ++s) mbar_init(&bars->meta_full[s], 1);
     mbar_init(&bars->mma_final, 1);
@@ -428,36 +468,46 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   }
   if (warp == 2) tc05::tmem_alloc(&bars->tmem_base, 512);
 
-  // ---- plan: the blocks of all items, in equal ranges (see the top)
+  // ---- plan: the blocks of all items, in equal ranges (see the top). The costs of the first kT5Threads
+  // sequences are kept: a batch no larger is read once and planned with one barrier.
+  const int tid = threadIdx.x;
+  bool fails = false;
   auto cost = [&](int b) -> long long {
     Seq s;
-    if (b >= c.batch || !load_seq(e, b, s) || !seq_ok(e, s)) return 0;
-    const Items it = items_of<ALT>(e, s);
-    return it.before<ALT>(it.np);
-  };
-  const int tid = threadIdx.x;
-  long long total = 0;
-  bool fails = false;
-  for (int b = tid; b < c.batch; b += kT5Threads) {
-    total += cost(b);
-    Seq s;
-    if (load_seq(e, b, s) && !seq_ok(e, s)) {
-      fails = true;
-      if (blockIdx.x == 0) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SEQ_LEN, b);
+    if (b >= c.batch || !load_seq(e, b, s)) return 0;
+    if (seq_ok(e, s)) {
+      const Items it = items_of<ALT>(e, s);
+      return it.before<ALT>(it.np);
     }
-  }
+    fails = true;
+    return 0;
+  };
+  auto warp_incl = [&](long long x) {                  // inclusive prefix sum over the warp
 #pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) bars->red[warp] = total;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += v;
+    }
+    return x;
+  };
+  long long mine = cost(tid), incl = warp_incl(mine), total = 0;
+  for (int b = tid + kT5Threads; b < c.batch; b += kT5Threads) total += cost(b);
+  if (c.batch > kT5Threads) total = __shfl_sync(0xffffffffu, warp_incl(total), 31);
+  if (lane == 31) {
+    bars->red[warp] = incl;
+    bars->rest[warp] = total;
+  }
   tc05::fence_before_sync();
   const int any_fails = __syncthreads_or(fails);
   tc05::fence_after_sync();
   total = 0;
-  for (int w = 0; w < kT5Threads / 32; ++w) total += bars->red[w];
-  if (any_fails && blockIdx.x == 0) {
+  for (int w = 0; w < kT5Threads / 32; ++w) total += bars->red[w] + bars->rest[w];
+  if (any_fails && blockIdx.x == 0) {                  // reported and zeroed once
     for (int b = 0; b < c.batch; ++b) {
       Seq s;
-      if (load_seq(e, b, s) && !seq_ok(e, s)) xs::zero_rows(e, s);
+      if (!load_seq(e, b, s) || seq_ok(e, s)) continue;
+      if (tid == 0) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SEQ_LEN, b);
+      zero_rows(e, s);
     }
   }
   // CTA x works on KV head x mod H_kv and range x / H_kv: the heads of a page are read at about the
@@ -467,24 +517,21 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   if (per < 2) per = 2;
   const long long start = (int)blockIdx.x / c.Hkv < ranges ? per * ((int)blockIdx.x / c.Hkv) : total;
   const int budget0 = (int)max(0ll, min(per, total - start));
-  // the sequence, head, item and block of position `start`
+  // the sequence, item and block of position `start`
   long long carry = 0;
-  for (int b0 = 0; b0 < c.batch && budget0 > 0 && carry <= start; b0 += kT5Threads) {
-    const long long mine = cost(b0 + tid);
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+  for (int b0 = 0; budget0 > 0; b0 += kT5Threads) {
+    if (b0 > 0) {
+      mine = cost(b0 + tid);
+      incl = warp_incl(mine);
+      __syncthreads();                                 // the last use of red is behind
+      if (lane == 31) bars->red[warp] = incl;
+      __syncthreads();
     }
-    __syncthreads();                                   // the last use of red is behind
-    if (lane == 31) bars->red[warp] = incl;
-    __syncthreads();
-    long long before = carry, chunk = 0;
+    long long before = carry;
     for (int w = 0; w < kT5Threads / 32; ++w) {
       const long long v = bars->red[w];
       if (w < warp) before += v;
-      chunk += v;
+      carry += v;
     }
     const long long at = start - (before + incl - mine);
     if (mine > 0 && at >= 0 && at < mine) {
@@ -502,7 +549,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       bars->st_i = lo;
       bars->st_j = it.jlo(lo) - kItemCost + off - it.before<ALT>(lo);
     }
-    carry += chunk;
+    if (carry > start || b0 + kT5Threads >= c.batch) break;
   }
   __syncthreads();
   Walk w;
@@ -603,7 +650,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       const int ks = k % NK;
       if (k >= NK) ok = wait_warp(&bars->k_empty[ks], (uint32_t)(k / NK - 1) & 1u, abort);
       if (!ok) return;
-      const bool load = lane < kTPages && !(mt.flags[lane & (kTPages - 1)] & xs::kSkip);
+      const bool load = lane < kTPages && !(mt.flags[lane & (kTPages - 1)] & kSkip);
       const int n = __popc(__ballot_sync(0xffffffffu, load));
       if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[ks], (uint32_t)n * (kPage * D * 2));
       __syncwarp();
@@ -620,17 +667,17 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     lookup(b0, id0, mode0, vs0);
     while (ok && b0.nb > 0) {
       // this batch's pages
-      int flags = xs::kSkip, detail = EKV_DETAIL_NONE;
+      int flags = kSkip, detail = EKV_DETAIL_NONE;
       float vs = 1.f;
       if (in_batch(b0)) {
-        flags = mode0 == EKV_MODE_COMPACT_E4M3 ? xs::kE4 : mode0 == EKV_MODE_BASE ? xs::kBs : mode0 == EKV_MODE_MICRO_FP4 ? xs::kMx : 0;
+        flags = mode0 == EKV_MODE_COMPACT_E4M3 ? kE4 : mode0 == EKV_MODE_BASE ? kBs : mode0 == EKV_MODE_MICRO_FP4 ? kMx : 0;
         if (id0 < 0 || id0 >= c.num_pages) detail = EKV_DETAIL_PAGE_ID;
         else if (mode0 > EKV_MODE_MICRO_FP4) detail = EKV_DETAIL_PAGE_MODE;
-        else if ((flags & xs::kE4) && !scale_ok(vs0)) detail = EKV_DETAIL_SCALE;
-        else if (flags & xs::kE4) vs = vs0;
+        else if ((flags & kE4) && !scale_ok(vs0)) detail = EKV_DETAIL_SCALE;
+        else if (flags & kE4) vs = vs0;
         if (detail) {
           report_error(c.err, EKV_ERR_DEVICE_CHECK, detail, b0.b);
-          flags = xs::kSkip;
+          flags = kSkip;
         }
       }
       const float lsc = log2f(vs), ivs = 1.f / vs;
@@ -685,7 +732,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       if (!ok) break;
       const BlockMeta& mt = bars->meta[u % NM];
       last = mt.last;
-      const int flags = lane < kTPages ? mt.flags[lane] : xs::kSkip;
+      const int flags = lane < kTPages ? mt.flags[lane] : kSkip;
       const int page = lane < kTPages ? mt.page[lane] : 0;
       // a stage with rows to zero is announced on a barrier of its own; they are zeroed once it has landed
       const bool edge = mt.z0 > 0 || mt.z1 < kTKeys;
@@ -849,23 +896,28 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       if (kRaw) {
         const int rs = issued % NR;
         uint64_t* bar = &bars->raw_full[rs][vi];
-        const int flags = lane == 0 || (lane == 1 && two) ? mt.flags[pg] : xs::kSkip;
-        const bool mx = flags & xs::kMx, by = flags & (xs::kE4 | xs::kBs);
-        const uint32_t nmx = __popc(__ballot_sync(0xffffffffu, mx)), nby = __popc(__ballot_sync(0xffffffffu, by));
-        if (lane == 0) mbar_arrive_expect_tx(bar, nmx * micro_head_bytes(D) + nby * (kPage * D));
+        // lane 0's page and, where there is one, lane 1's: an arrival and its bytes each
+        if (lane < (two ? 2 : 1)) {
+          const int flags = mt.flags[pg];
+          uint8_t* dst = sR + rs * C::RB + pg * (kPage * D);
+          const bool mx = VM == kXMicro ? !(flags & kSkip) : VM == kXMixed && (flags & kMx);
+          const bool by = flags & (kE4 | kBs);
+          mbar_arrive_expect_tx(bar, mx ? micro_head_bytes(D) : by ? kPage * D : 0);
+          if (mx)
+            bulk_load(dst, c.v_pages + (size_t)mt.page[pg] * c.v_page_stride + h * micro_head_bytes(D), micro_head_bytes(D), bar);
+          else if (by)
+            tma_load_4d(dst, &tv8, 0, h, 0, mt.page[pg], bar);
+        }
         __syncwarp();
-        uint8_t* dst = sR + rs * C::RB + pg * (kPage * D);
-        if (mx)
-          bulk_load(dst, c.v_pages + (size_t)mt.page[pg] * c.v_page_stride + h * micro_head_bytes(D), micro_head_bytes(D), bar);
-        else if (by)
-          tma_load_4d(dst, &tv8, 0, h, 0, mt.page[pg], bar);
       }
       ++issued;
     };
-    // 16 codes of one token become two 16-byte chunks; the lanes of the second slab write theirs in the
-    // other order, so that eight lanes never meet in a bank
-    const int ch = lane % (D / 16), t0 = lane / (D / 16);      // chunk of 16 codes, first token
-    const uint32_t swap = (ch >> 2) & 1, c0 = 2 * (ch & 3) + swap;
+    // A lane's 16 E4M3 codes of a row become the 16-byte chunks 2 c and 2 c + 1, its 32 microscaled ones chunks
+    // 4 c .. 4 c + 3. The lanes are dealt over chunks, rows and slabs such that the eight that store at a
+    // time meet eight chunk places (chunk ^ row): rows r, r ^ 1 with four c each, or four rows with two.
+    const int c8 = lane & 3, s8 = D == 128 ? (lane >> 3) & 1 : 0;
+    const int t8 = D == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2;
+    const int c4 = lane & 1, t4 = D == 128 ? ((lane >> 1) & 3) | ((lane >> 4) << 2) : lane >> 1;
     for (int u = 0; ok && (more || u < issued); ++u) {
       while (ok && more && issued < u + (kRaw ? NR : 1)) issue();
       const int vs = u % NV, rs = u % NR;
@@ -879,39 +931,44 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const int fl = mt.flags[page];
         uint8_t* dv = sV + vs * C::IB + page * (2 * C::GB);
         const uint8_t* src = sR + rs * C::RB + page * (kPage * D);
-        if (kRaw && (fl & (xs::kMx | xs::kE4 | xs::kBs))) {
+        if (VM == kXMicro ? !(fl & kSkip) : VM == kXMixed && (fl & kMx)) {
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            const int t = t0 + x * (512 / D), r = t & 7;
-            uint4 lo, hi;
-            if (VM == kXMicro || (VM == kXMixed && (fl & xs::kMx))) {
-              const uint2 codes = *reinterpret_cast<const uint2*>(src + t * (D / 2) + ch * 8);
-              uint32_t sb = src[micro_scale_off(D) + t * (D / kMicroBlock) + ch / 2];
-              if (!micro_scale_ok(sb)) {
-                if (page * kPage + t >= mt.z0 && page * kPage + t < mt.z1)
-                  report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SCALE, -1);
-                sb = 0;
-              }
-              const __half2 s2 = micro_scale_h2(sb);
-              lo = micro_decode8(codes.x, s2);
-              hi = micro_decode8(codes.y, s2);
-            } else {
-              const uint4 q = *reinterpret_cast<const uint4*>(src + (D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16)));
-              if (VM == kXMixed && (fl & xs::kBs)) {
-                lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
-                                __byte_perm(q.y, 0u, 0x3424));
-                hi = make_uint4(__byte_perm(q.z, 0u, 0x1404), __byte_perm(q.z, 0u, 0x3424), __byte_perm(q.w, 0u, 0x1404),
-                                __byte_perm(q.w, 0u, 0x3424));
-              } else {
-                lo = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.x)), xs::bits(e4m3x2_to_half2((uint16_t)(q.x >> 16))),
-                                xs::bits(e4m3x2_to_half2((uint16_t)q.y)), xs::bits(e4m3x2_to_half2((uint16_t)(q.y >> 16))));
-                hi = make_uint4(xs::bits(e4m3x2_to_half2((uint16_t)q.z)), xs::bits(e4m3x2_to_half2((uint16_t)(q.z >> 16))),
-                                xs::bits(e4m3x2_to_half2((uint16_t)q.w)), xs::bits(e4m3x2_to_half2((uint16_t)(q.w >> 16))));
-              }
+          for (int x = 0; x < D / 64; ++x) {
+            const int t = t4 + x * (1024 / D), r = t & 7, q = 2 * s8 + c4;
+            const uint4 codes = *reinterpret_cast<const uint4*>(src + t * (D / 2) + q * 16);
+            uint32_t sb = src[micro_scale_off(D) + t * (D / kMicroBlock) + q];
+            if (!micro_scale_ok(sb)) {
+              if (page * kPage + t >= mt.z0 && page * kPage + t < mt.z1)
+                report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SCALE, -1);
+              sb = 0;
             }
-            uint8_t* row = dv + (t >> 3) * C::GB + (ch >> 2) * 1024 + r * 128;
-            *reinterpret_cast<uint4*>(row + (c0 ^ r) * 16) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(row + (c0 ^ 1 ^ r) * 16) = swap ? lo : hi;
+            const __half2 s2 = micro_scale_h2(sb);
+            uint8_t* row = dv + (t >> 3) * C::GB + s8 * 1024 + r * 128;
+            *reinterpret_cast<uint4*>(row + ((4 * c4) ^ r) * 16) = micro_decode8(codes.x, s2);
+            *reinterpret_cast<uint4*>(row + ((4 * c4 + 1) ^ r) * 16) = micro_decode8(codes.y, s2);
+            *reinterpret_cast<uint4*>(row + ((4 * c4 + 2) ^ r) * 16) = micro_decode8(codes.z, s2);
+            *reinterpret_cast<uint4*>(row + ((4 * c4 + 3) ^ r) * 16) = micro_decode8(codes.w, s2);
+          }
+        } else if (kRaw && (fl & (kE4 | kBs))) {
+#pragma unroll (VM == kXMixed ? 2 : D / 32)
+          for (int x = 0; x < D / 32; ++x) {
+            const int t = t8 + x * (512 / D), r = t & 7, ch = 4 * s8 + c8;
+            uint4 lo, hi;
+            const uint4 q = *reinterpret_cast<const uint4*>(src + (D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16)));
+            if (VM == kXMixed && (fl & kBs)) {
+              lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
+                              __byte_perm(q.y, 0u, 0x3424));
+              hi = make_uint4(__byte_perm(q.z, 0u, 0x1404), __byte_perm(q.z, 0u, 0x3424), __byte_perm(q.w, 0u, 0x1404),
+                              __byte_perm(q.w, 0u, 0x3424));
+            } else {
+              lo = make_uint4(bits(e4m3x2_to_half2((uint16_t)q.x)), bits(e4m3x2_to_half2((uint16_t)(q.x >> 16))),
+                              bits(e4m3x2_to_half2((uint16_t)q.y)), bits(e4m3x2_to_half2((uint16_t)(q.y >> 16))));
+              hi = make_uint4(bits(e4m3x2_to_half2((uint16_t)q.z)), bits(e4m3x2_to_half2((uint16_t)(q.z >> 16))),
+                              bits(e4m3x2_to_half2((uint16_t)q.w)), bits(e4m3x2_to_half2((uint16_t)(q.w >> 16))));
+            }
+            uint8_t* row = dv + (t >> 3) * C::GB + s8 * 1024 + r * 128;
+            *reinterpret_cast<uint4*>(row + ((2 * c8) ^ r) * 16) = lo;
+            *reinterpret_cast<uint4*>(row + ((2 * c8 + 1) ^ r) * 16) = hi;
           }
         }
       }
@@ -921,14 +978,14 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (!ok) break;
       }
       // keys that no row of the item sees, and pages that were not loaded: zeros, whatever they hold
-      const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (mt.flags[lane & (kTPages - 1)] & xs::kSkip));
+      const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (mt.flags[lane & (kTPages - 1)] & kSkip));
       if (edge || smask) {
         __syncwarp();
         for (int page = vi; page < kTPages; page += C::MK)
           for (int x = lane; x < kPage * (D / 8); x += 32) {
-            const int key = page * kPage + x / (D / 8), c8 = x % (D / 8);
+            const int key = page * kPage + x / (D / 8), cz = x % (D / 8);
             if (key < mt.z0 || key >= mt.z1 || ((smask >> page) & 1u))
-              *reinterpret_cast<uint4*>(sV + vs * C::IB + (key >> 3) * C::GB + (c8 >> 3) * 1024 + (key & 7) * 128 + (c8 & 7) * 16) =
+              *reinterpret_cast<uint4*>(sV + vs * C::IB + (key >> 3) * C::GB + (cz >> 3) * 1024 + (key & 7) * 128 + (cz & 7) * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
           }
       }
@@ -989,47 +1046,62 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const BlockMeta& mt = bars->meta[(u0 + blk) % NM];
         const int k0 = (ja + blk) * kTKeys;
         const int badp = mt.bad;
-        uint32_t a[4][32];
-        tc05::ld32(t_s, a[0]);
-        tc05::ld32(t_s + 32, a[1]);
-        tc05::ld32(t_s + 64, a[2]);
-        tc05::ld32(t_s + 96, a[3]);
-        tc05::wait_ld();
-        if (k0 + kTKeys - 1 > all_hi || k0 <= all_lo || badp) {
-          const int hi_c = pos - k0, lo_c = lo - k0;
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4)
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (32 * c4 + x > hi_c || 32 * c4 + x <= lo_c) a[c4][x] = __float_as_uint(-INFINITY);
-          if (badp) {
-            for (int pg = 0; pg < kTPages; ++pg)
-              if (((badp >> pg) & 1) && pg * kPage <= hi_c && pg * kPage + kPage - 1 > lo_c) bad = true;
-          }
+        const bool masked = k0 + kTKeys - 1 > all_hi || k0 <= all_lo || badp;
+        const int hi_c = pos - k0, lo_c = lo - k0;
+        if (badp) {
+          for (int pg = 0; pg < kTPages; ++pg)
+            if (((badp >> pg) & 1) && pg * kPage <= hi_c && pg * kPage + kPage - 1 > lo_c) bad = true;
         }
-        // the row's maximum, in log2 units
+        // The row's maximum, in log2 units. NH 1: the row stays in registers. NH 2: half of it at a time, read
+        // again for the weights (and written back where masked), for half the code: the loops of a CTA's
+        // roles share one instruction cache, and where the makers' loop is the long one (mixed pages)
+        // or each softmax warp runs alone (ALT) that counts for more than the second read. Measured,
+        // NH 1 / 2: mixed chunks under a window 150 / 144 us, 48 x 5 tokens over mixed pages 166 / 161 us,
+        // 4,096 tokens behind 16K of E4M3 884 / 916 us.
+        constexpr int NH = ALT || VM == kXMixed ? 2 : 1, NC = 4 / NH;
+        uint32_t a[NC][32];
         float mx = -INFINITY;
+#pragma unroll 1
+        for (int hf = 0; hf < NH; ++hf) {
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          float m8[4];
+          for (int c4 = 0; c4 < NC; ++c4) tc05::ld32(t_s + 32 * (NC * hf + c4), a[c4]);
+          tc05::wait_ld();
+          if (masked) {
+            const int hc = hi_c - 32 * NC * hf, lc = lo_c - 32 * NC * hf;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t* y = a[c4] + 8 * q;
-            m8[q] = fmaxf(max3(max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2])),
-                               __uint_as_float(y[3]), __uint_as_float(y[4])),
-                          max3(__uint_as_float(y[5]), __uint_as_float(y[6]), __uint_as_float(y[7])));
+            for (int c4 = 0; c4 < NC; ++c4)
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (32 * c4 + x > hc || 32 * c4 + x <= lc) a[c4][x] = __float_as_uint(-INFINITY);
+            if (NH > 1) {
+#pragma unroll
+              for (int c4 = 0; c4 < NC; ++c4) tc05::st32(t_s + 32 * (NC * hf + c4), a[c4]);
+              tc05::wait_st();
+            }
           }
-          if (PS) {
-            mx = max3(mx, fmaf(fmaxf(m8[0], m8[1]), qs, mt.lsc[2 * c4]), fmaf(fmaxf(m8[2], m8[3]), qs, mt.lsc[2 * c4 + 1]));
-          } else {
-            mx = max3(mx, max3(m8[0], m8[1], m8[2]), m8[3]);
+#pragma unroll
+          for (int c4 = 0; c4 < NC; ++c4) {
+            float m8[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t* y = a[c4] + 8 * q;
+              m8[q] = fmaxf(max3(max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2])),
+                                 __uint_as_float(y[3]), __uint_as_float(y[4])),
+                            max3(__uint_as_float(y[5]), __uint_as_float(y[6]), __uint_as_float(y[7])));
+            }
+            if (PS) {
+              const float* lsc = mt.lsc + 2 * (NC * hf + c4);
+              mx = max3(mx, fmaf(fmaxf(m8[0], m8[1]), qs, lsc[0]), fmaf(fmaxf(m8[2], m8[3]), qs, lsc[1]));
+            } else {
+              mx = max3(mx, max3(m8[0], m8[1], m8[2]), m8[3]);
+            }
           }
         }
         if (!PS) mx *= qs;
         const float m_new = fmaxf(m_ref, mx);
         const bool need = m_new > m_ref + 8.f;
         if (__any_sync(0xffffffffu, need)) {
-          const float alpha = need ? xs::ex2(m_ref - m_new) : 1.f;
+          const float alpha = need ? ex2(m_ref - m_new) : 1.f;
           if (jj > 0) {
 #pragma unroll 1
             for (int x = 0; x < D / 16; ++x) {
@@ -1046,24 +1118,33 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         // a row that has seen no key yet keeps m = -inf: its weights are 2^-inf = 0
         const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+        // (P's columns 16 c .. of chunk c lie over S columns that have been read by then)
+#pragma unroll 1
+        for (int hf = 0; hf < NH; ++hf) {
+          if (NH > 1) {
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-#pragma unroll
-          for (int pg = 0; pg < 2; ++pg) {
-            const float add = PS ? nm + mt.lsc[2 * c4 + pg] : nm;
-            float la[2] = {0.f, 0.f}, lb[2] = {0.f, 0.f};
-#pragma unroll
-            for (int x = 8 * pg; x < 8 * pg + 8; ++x) {
-              float a0, a1;
-              ffma2(a0, a1, __uint_as_float(a[c4][2 * x]), __uint_as_float(a[c4][2 * x + 1]), qs, add);
-              const float p0 = xs::ex2(a0), p1 = xs::ex2(a1);
-              fadd2(la[x & 1], lb[x & 1], p0, p1);
-              a[c4][x] = pack2(p0, p1);
-            }
-            fadd2(la[0], lb[0], la[1], lb[1]);
-            l = PS ? fmaf(la[0] + lb[0], mt.ivs[2 * c4 + pg], l) : l + (la[0] + lb[0]);
+            for (int c4 = 0; c4 < NC; ++c4) tc05::ld32(t_s + 32 * (NC * hf + c4), a[c4]);
+            tc05::wait_ld();
           }
-          tst16(t_s + 16 * c4, &a[c4][0]);
+#pragma unroll
+          for (int c4 = 0; c4 < NC; ++c4) {
+#pragma unroll
+            for (int pg = 0; pg < 2; ++pg) {
+              const float add = PS ? nm + mt.lsc[2 * (NC * hf + c4) + pg] : nm;
+              float la[2] = {0.f, 0.f}, lb[2] = {0.f, 0.f};
+#pragma unroll
+              for (int x = 8 * pg; x < 8 * pg + 8; ++x) {
+                float a0, a1;
+                ffma2(a0, a1, __uint_as_float(a[c4][2 * x]), __uint_as_float(a[c4][2 * x + 1]), qs, add);
+                const float p0 = ex2(a0), p1 = ex2(a1);
+                fadd2(la[x & 1], lb[x & 1], p0, p1);
+                a[c4][x] = pack2(p0, p1);
+              }
+              fadd2(la[0], lb[0], la[1], lb[1]);
+              l = PS ? fmaf(la[0] + lb[0], mt.ivs[2 * (NC * hf + c4) + pg], l) : l + (la[0] + lb[0]);
+            }
+            tst16(t_s + 16 * (NC * hf + c4), &a[c4][0]);
+          }
         }
         tc05::wait_st();
         tc05::fence_before_sync();
@@ -1095,7 +1176,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         const float2 other = xch[1 - t][r];
         bad = bad || other.y < 0.f;
         const float M = fmaxf(m_ref, other.x);
-        float w0 = l > 0.f ? xs::ex2(m_ref - M) : 0.f, w1 = other.y > 0.f ? xs::ex2(other.x - M) : 0.f;
+        float w0 = l > 0.f ? ex2(m_ref - M) : 0.f, w1 = other.y > 0.f ? ex2(other.x - M) : 0.f;
         const float L = fmaf(l, w0, fmaxf(other.y, 0.f) * w1);
         if (t == 1) {                                  // w0 weighs stream 0
           const float x = w0;
