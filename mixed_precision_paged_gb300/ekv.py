@@ -114,19 +114,28 @@ def _ptr(x):
     """Device/host address of a tensor or array, an int address, or None -> NULL."""
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
     if hasattr(x, "data_ptr"):
         return x.data_ptr()
+    if isinstance(x, int):
+        return x
     if isinstance(x, np.ndarray):
         return x.ctypes.data
     raise TypeError(f"cannot take the address of {type(x)}")
 
 
+_torch = None
+
+
 def _stream(stream):
+    """The handle of `stream`; None: the current stream of the current device, asked for without
+    building a stream object (0.2 us instead of 2.9 us of every call)."""
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _torch
+        if _torch is None:
+            import torch
+            torch.cuda.current_stream()                  # initialises CUDA
+            _torch = torch
+        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
