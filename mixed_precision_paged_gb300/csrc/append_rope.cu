@@ -18,7 +18,9 @@
 namespace ekv {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeRows = 4;      // head rows a lane has in flight (2 x 16 B each)
+// Head rows a lane has in flight, 2 x 16 B each. 65,536 tokens of 48 rows: 4 rows 260 us, 6 rows 247 us, 8 rows
+// (fewer warps fit) 333 us.
+constexpr int kRopeRows = 6;
 
 // 8 pairs (lo[j], hi[j]) turned by (c[j], s[j]).
 __device__ __forceinline__ void rotate8(uint4& lo, uint4& hi, const float (&c)[8], const float (&s)[8]) {
@@ -64,7 +66,7 @@ __device__ __forceinline__ uint2 e4m3_encode8(const uint4& x, float s) {
 
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads)
-rope_append_kernel(const RopeAppendParams p, int parts) {
+rope_append_kernel(const RopeAppendParams p, int parts, int part_rows) {
   constexpr int UN = D / 16;                       // units of a head
   constexpr int SLOTS = 32 / UN;                   // head rows a warp works on at a time
   const CacheView& c = p.c;
@@ -85,12 +87,13 @@ rope_append_kernel(const RopeAppendParams p, int parts) {
     int b = -1, t = 0, page = -1, mode = 0;
     bool ok = false, page_ok = false;
     float cs[8], sn[8];
-    for (int x0 = part * SLOTS * kRopeRows; x0 < rows; x0 += parts * SLOTS * kRopeRows) {
+    const int x1 = min(rows, (part + 1) * part_rows);
+    for (int x0 = part * part_rows; x0 < x1; x0 += SLOTS * kRopeRows) {
       uint4 a0[kRopeRows], a1[kRopeRows];
 #pragma unroll
       for (int r = 0; r < kRopeRows; ++r) {
         const int x = x0 + r * SLOTS + slot;
-        if (x >= rows) continue;
+        if (x >= x1) continue;
         const bool is_v = x >= nq + c.Hkv;
         const __half* src = x < nq ? p.q + (size_t)i * p.q_stride + x * D
                             : !is_v ? p.k_new + (size_t)i * p.k_stride + (x - nq) * D
@@ -130,7 +133,7 @@ rope_append_kernel(const RopeAppendParams p, int parts) {
 #pragma unroll
       for (int r = 0; r < kRopeRows; ++r) {
         const int x = x0 + r * SLOTS + slot;
-        if (x < nq + c.Hkv) {                      // q or k: turned
+        if (x < x1 && x < nq + c.Hkv) {            // q or k: turned
           if (rot) {
             if (split) {
               rotate8(a0[r], a1[r], cs, sn);
@@ -148,7 +151,7 @@ rope_append_kernel(const RopeAppendParams p, int parts) {
         }
         // v: in the form of its page. The block of a microscaled row is two units, in two lanes.
         uint32_t mx2 = 0;
-        const bool is_v = x >= nq + c.Hkv && x < rows;
+        const bool is_v = x >= nq + c.Hkv && x < x1;
         if (is_v)
           mx2 = __vmaxu2(__vmaxu2(__vmaxu2(a0[r].x & 0x7fff7fffu, a0[r].y & 0x7fff7fffu),
                                   __vmaxu2(a0[r].z & 0x7fff7fffu, a0[r].w & 0x7fff7fffu)),
@@ -192,16 +195,19 @@ cudaError_t launch_rope_append(const RopeAppendParams& p, int num_sms, cudaStrea
   if (p.c.total_q <= 0 || p.c.batch <= 0) return cudaSuccess;
   const int slots = 512 / p.c.D;
   const int rows = (p.q ? p.c.Hq : 0) + 2 * p.c.Hkv;
-  const int chunks = (rows + slots * kRopeRows - 1) / (slots * kRopeRows);
-  // a warp per token, or per chunk of its heads while that leaves the GPU's warps idle
-  const long long room = (long long)num_sms * 16;
-  const int parts = p.c.total_q * (long long)chunks <= room ? chunks : 1;
+  // A warp takes a part of a token's rows: what its lanes hold in flight at once; or, while that leaves warps
+  // idle (16 a processor), two rows a lane (32 tokens: 8.3 -> 6.3 us). The parts of a token are of
+  // one size, so that the grid ends together.
+  const int fit = (rows + slots * kRopeRows - 1) / (slots * kRopeRows), fine = (rows + 2 * slots - 1) / (2 * slots);
+  const int want = p.c.total_q * (long long)fine <= (long long)num_sms * 16 ? fine : fit;
+  const int part_rows = (rows + want * slots - 1) / (want * slots) * slots;
+  const int parts = (rows + part_rows - 1) / part_rows;
   const long long warps = (long long)p.c.total_q * parts;
-  const long long most = (long long)num_sms * 12;      // blocks: resident ones, and no more
+  const long long most = (long long)num_sms * 8;
   long long grid = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (grid > most) grid = most;
-  if (p.c.D == 128) rope_append_kernel<128><<<(int)grid, kRopeThreads, 0, st>>>(p, parts);
-  else rope_append_kernel<64><<<(int)grid, kRopeThreads, 0, st>>>(p, parts);
+  if (p.c.D == 128) rope_append_kernel<128><<<(int)grid, kRopeThreads, 0, st>>>(p, parts, part_rows);
+  else rope_append_kernel<64><<<(int)grid, kRopeThreads, 0, st>>>(p, parts, part_rows);
   return cudaGetLastError();
 }
 
