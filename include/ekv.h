@@ -110,7 +110,8 @@ typedef struct {
 } ekv_config;
 
 /* Create a context on the current device: allocates the split-K partials, the plan
- * buffer and the sticky error word once (cudaMalloc). Returns EKV_ERR_UNSUPPORTED for
+ * buffer, the partial rows of ekv_extend_attention (2 * #SMs * 256 * (D + 2) floats) and the
+ * sticky error word once (cudaMalloc). Returns EKV_ERR_UNSUPPORTED for
  * shapes outside the supported set. *ctx is NULL on failure. */
 ekv_status ekv_create(ekv_ctx** ctx, const ekv_config* cfg);
 
@@ -374,11 +375,15 @@ ekv_status ekv_append_kv_rope(ekv_ctx* ctx, const void* q, const void* k_new, co
  *   out[i][h_q] = sum_k softmax_k(sm_scale * q[i][h_q] . K_k) V_k,
  *   lse[i][h_q] = log sum_k exp(sm_scale * q[i][h_q] . K_k)
  * over the keys max(0, t - window + 1) <= k <= t of sequence b (window 0: all k <= t). Pages
- * may hold values in any of the four forms. Keys outside that range are not used, whatever
- * their rows hold (NaN included).
+ * may hold values in any of the four forms. A key that no query of the sequence sees is not used,
+ * whatever its rows hold (NaN included), and pages of which none is seen are not read (their table
+ * entries may be stale). The values of a key that only some of them see must be finite: NaN or
+ * infinity times the weight 0 of a query that does not see it is NaN, as in ekv_prefill_attention.
+ * Other NaNs (of queries, keys, values) reach the queries that meet them and no others.
  *  q, out       fp16 [total_q][H_q][D], contiguous, 16-byte aligned; must not overlap.
  *  seq_lens, cu_q, total_q  as for ekv_append_kv_rope; rows >= cu_q[batch] are left as they are.
- *  max_q        host int, at least every n_b: chooses the kernel. A longer sequence is
+ *  max_q        host int, at least every n_b: chooses the kernel (small ones stream the cache
+ *               with least delay, large ones share a block among 256 rows). A longer sequence is
  *               reported (EKV_DETAIL_SEQ_LEN), as is one that the writer would report: its out
  *               is zeroed and its lse -inf.
  *  window       keys a query sees, its own among them; 0: no window.
@@ -386,7 +391,8 @@ ekv_status ekv_append_kv_rope(ekv_ctx* ctx, const void* q, const void* k_new, co
  * A page that fails its check (id, mode byte > 3, scale) zeroes out and sets lse = -inf for the
  * queries that see one of its keys (of one KV head for a bad per-(page, head) scale). Returns
  * EKV_ERR_CAPACITY when batch > cfg.max_batch, EKV_ERR_UNSUPPORTED when block_table_stride > 131072
- * or a pool has 2^31 or more head rows. Other arguments as for ekv_paged_decode; sums are fp32, the weights enter the product with V rounded to fp16. */
+ * or a pool has 2^31 or more head rows. Other arguments as
+ * for ekv_paged_decode. Sums are fp32; the weights enter the product with V rounded to fp16. */
 ekv_status ekv_extend_attention(ekv_ctx* ctx, const void* q, const void* k_pages, const void* v_pages,
                                 long long v_page_stride_bytes, int num_pages, const float* v_scales,
                                 int scale_mode, const uint8_t* page_mode, int uniform_mode,

@@ -21,12 +21,16 @@
 //     a second kernel joins them. Long causal chunks so balance to a block, and one short chunk
 //     behind a long prefix still uses every SM.
 // Roles: warp 0 checks the pages and loads Q and K; warp 1 issues the MMAs; warp 3 loads FP16 value
-// pages (warp 2 owns tensor memory); warps 4-7 and 8-11 are the softmax of tile 0 and
-// 1, a thread per row; the other warps load
-// and expand the other pages. The
-// registers are split to match (setmaxnreg): 80, 176, 176 and 80 a thread, 512 = 4 x the 128 of launch. Tensor memory of tile t: S and P at 256 t, O at 256 t + 128. The order of
-// the MMAs and the lazily moved maximum are those of the prefill (prefill_tc05.cu). Every wait is
-// bounded; a timeout is reported and every role winds down.
+// pages; warps 4-7 and 8-11 are the softmax of tile 0 and 1, a thread per row; the others (makers)
+// load and expand the other pages (warp 2 also owns tensor memory). The registers are split to match
+// (setmaxnreg): 80, 176, 176 and 80 a thread, 512 = 4 x the 128 of launch. Tensor memory of tile t: S
+// and P at 256 t, O at 256 t + 128. The order of the MMAs and the lazily moved maximum are those of the
+// prefill (prefill_tc05.cu).
+// The instruction cache is a resource here: sixteen warps run seven different loops, and once these no
+// longer fitted it (a second copy of the makers' loop, deeper unrolling) every role slowed down two- to
+// threefold, with the GPC's instruction cache at 86% of its request rate. So a role's loop stands once, the
+// makers are driven by block descriptions instead of walking the plan, and unrolling is chosen by measurement.
+// Every wait is bounded; a timeout is reported and every role winds down.
 #pragma once
 
 #include "extend.cuh"
@@ -110,7 +114,7 @@ struct XTBars {
   float2 xch[2][ALT ? kAltRows : 1];
   BlockMeta meta[C::NM];
   long long red[kT5Threads / 32], rest[kT5Threads / 32];
-  int st_b, st_i, st_j;               // where this CTA's range begins
+  int st_b, st_i, st_j;                     // where this CTA's range begins
   uint32_t tmem_base;
   int abort;
 };
@@ -160,40 +164,14 @@ __device__ __forceinline__ void zero_rows(const ExtendParams& e, const Seq& s) {
     for (long long i = threadIdx.x; i < n; i += blockDim.x) e.lse[(long long)r0 * c.Hq + i] = -INFINITY;
 }
 
-// try_wait with a suspend-time hint: the warp sleeps in hardware until the phase ends instead of
-// polling. A dozen warps of a CTA wait at any time, and their polls cost the others' shared-memory
-// accesses: without the hint a 32 x 8K decode step took 197 us instead of XXX us.
-__device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (sleep_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (sleep_wait(bar, parity)) return true;
-    if (*abort || globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
-  }
-}
+// A warp's wait for a phase, bounded, that also gives up once another role has: false then. One compact loop:
+// it stands at every wait of every role (see the instruction cache below).
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
-}
-// For the MMA and softmax warps, whose wake-up is on the critical path: without the hint.
-__device__ __forceinline__ bool wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort) {
   bool ok = mbar_try_wait(bar, parity);
   if (!ok) {
     const uint64_t t0 = globaltimer_ns();
-    for (uint32_t i = 1;; ++i) {
-      if ((ok = mbar_try_wait(bar, parity))) break;
-      if ((i & 63u) == 0 && (*abort || globaltimer_ns() - t0 > kWaitTimeoutNs)) break;
-    }
+    while (!(ok = mbar_try_wait(bar, parity)))
+      if (*abort || globaltimer_ns() - t0 > kWaitTimeoutNs) break;
   }
   return __all_sync(0xffffffffu, ok);
 }
@@ -206,9 +184,6 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
   }
-}
-__device__ __forceinline__ void expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -410,8 +385,10 @@ __device__ __forceinline__ Walk unpack_walk(const ExtendParams& e, int v) {
 }  // namespace xt
 
 // -------------------------------------------------------------------- the kernel
-// PS: E4M3 scales differ by page (and head), or pages differ in form. ALT: every sequence's rows fit
-// one tile; its key blocks alternate between the two softmax groups ("streams").
+// PS: E4M3 scales differ by page (and head), or pages differ in form. ALT: every sequence's rows are at most
+// kAltRows; its key blocks alternate between the two softmax groups ("streams"), whose results are joined
+// at the end of a segment: with one tile in use, a block's chain (S, softmax, P V: ~3,300 cycles) would bound
+// the stream at two thirds of HBM rate; two chains in turn leave it to the loads.
 template <int D, int VM, bool PS, bool ALT>
 __global__ void __launch_bounds__(kT5Threads, 1)
 extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -423,7 +400,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   constexpr int NK = C::NK, NV = C::NV, NR = C::NR, NM = C::NM, NB = C::NB;
   extern __shared__ __align__(1024) uint8_t sm_1k[];   // (no room to align by hand)
   uint8_t* sQ = sm_1k;                                  // [2][NB][128 rows][128 B]
-  uint8_t* sK = sQ + C::NQ * C::QB;                        // [NK][16 groups][NB][8 rows][128 B]
+  uint8_t* sK = sQ + C::NQ * C::QB;                    // [NK][16 groups][NB][8 rows][128 B]
   uint8_t* sV = sK + NK * C::IB;
   uint8_t* sR = sV + NV * C::IB;                       // [NR][8 pages][16 * D B]
   Bars* bars = reinterpret_cast<Bars*>(sR + NR * C::RB);
@@ -455,7 +432,11 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     for (int s = 0; s < NK; ++s) mbar_init(&bars->k_full[s], 1), mbar_init(&bars->k_empty[s], 1);
     for (int s = 0; s < NR; ++s)
       for (int x = 0; x < C::MK; ++x) mbar_init(&bars->raw_full[s][x], x + C::MK < kTPages ? 2 : 1);
-    for (int s = 0; s < NV; ++s) mbar_init(&bars->v_full[s], C::MK + (kDirect ? 1 : 0)), mbar_init(&bars->v_empty[s], 1), mbar_init(&bars->v_dir[s], 1);
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(&bars->v_full[s], C::MK + (kDirect ? 1 : 0));
+      mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->v_dir[s], 1);
+    }
     for (int s = 0; s < NM; ++s) mbar_init(&bars->meta_full[s], 1);
     mbar_init(&bars->mma_final, 1);
     bars->abort = 0;
@@ -572,705 +553,715 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   const int q_slab = (ALT ? 32 * nw : kTRows) * 128, q_buf = NB * q_slab;
   const int h_rows = TT * e.G;
 
-
   // (each register split stands at the head of its roles' code)
   if (warp < 4 || warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (warp == 0) {
-    // ------------------------------------------- producer: page checks, Q, K
-    // Pages are looked up in batches of four blocks, a page per lane: a batch's ids are fetched two
-    // batches ahead and its modes and scales one ahead, across segments. A block's description is
-    // posted kMetaAhead blocks before its keys are loaded, for the makers, whose loads take as long.
-    int u = 0, k = 0;                                  // blocks described, blocks whose keys were loaded
-    uint32_t ql[2] = {0u, 0u}, qseg = 0;
-    ExtTcSplit split;
-    split.n = 0;
-    struct Batch {
-      int b, j0, nb, lo, hi, qtok, tiles;              // keys [lo, hi); qtok < 0: not a segment's first batch
-    };
-    Segment sg;
-    sg.ja = sg.jb = 0;
-    auto next_batch = [&](Batch& x) {
-      x.qtok = -1;
-      x.tiles = 0;
-      x.nb = 0;
-      if (sg.ja >= sg.jb) {
-        if (!walk_next<ALT>(e, w, sg)) return;
-        x.qtok = sg.q0 + C::NQ * sg.i * TT;
-        x.tiles = (sg.nt[0] > 0 ? 1 : 0) | (sg.nt[1] > 0 ? 2 : 0);
-        if (sg.ja == sg.jlo && sg.jb < sg.jhi) {       // the item goes on in later CTAs
-          split.n = 1 + (int)((sg.jhi - sg.jb + per - 1) / per);
-          split.first = sg.slot;
-          split.b = sg.b;
-          split.h = h;
-          split.i = sg.i;
-        }
-      }
-      x.b = sg.b;
-      x.j0 = sg.ja;
-      x.nb = min(32 / kTPages, sg.jb - sg.ja);
-      x.lo = sg.lo;
-      x.hi = sg.hi;
-      sg.ja += x.nb;
-    };
-    auto in_batch = [&](const Batch& x) {
-      const int k0 = x.j0 * kTKeys + lane * kPage;
-      return lane < x.nb * kTPages && k0 + kPage > x.lo && k0 < x.hi;
-    };
-    auto ids = [&](const Batch& x) {
-      return in_batch(x) ? __ldg(c.block_table + (size_t)x.b * c.bt_stride + x.j0 * kTPages + lane) : 0;
-    };
-    auto lookup = [&](const Batch& x, int id, int& mode, float& vs) {
-      mode = VM == kXFP16 ? EKV_MODE_TARGET_FP16 : VM == kXE4M3 ? EKV_MODE_COMPACT_E4M3 : VM == kXMicro ? EKV_MODE_MICRO_FP4 : c.uniform_mode;
-      vs = 0.f;
-      if (!in_batch(x) || id < 0 || id >= c.num_pages) return;
-      if (VM == kXMixed && c.page_mode) mode = (int)__ldg(c.page_mode + id);
-      if ((VM == kXE4M3 || VM == kXMixed) && c.v_scales)
-        vs = __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)id * c.Hkv + h));
-    };
-    bool ok = true;
-    // the queries (first block of a segment) and keys of block k
-    auto load_k = [&]() {
-      const BlockMeta& mt = bars->meta[k % NM];
-      if (mt.qtok >= 0) {
-        const int tiles = ALT ? 1 << (qseg % nqb) : mt.tiles;
-        ++qseg;
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (!((tiles >> t) & 1)) continue;
-          if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
-          if (!ok) return;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(h_rows * D * 2));
-            for (int s = 0; s < NB; ++s)
-              tma_load_5d(sQ + t * q_buf + s * q_slab, &tq, 0, 0, s, h, mt.qtok + (ALT ? 0 : t * TT), &bars->q_full[t]);
-          }
-          ++ql[t];
-        }
-      }
-      const int ks = k % NK;
-      if (k >= NK) ok = wait_warp(&bars->k_empty[ks], (uint32_t)(k / NK - 1) & 1u, abort);
-      if (!ok) return;
-      const bool load = lane < kTPages && !(mt.flags[lane & (kTPages - 1)] & kSkip);
-      const int n = __popc(__ballot_sync(0xffffffffu, load));
-      if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[ks], (uint32_t)n * (kPage * D * 2));
-      __syncwarp();
-      if (load)
-        tma_load_5d(sK + ks * C::IB + lane * (2 * C::GB), &tk, 0, 0, 0, 0, mt.page[lane] * kPage * c.Hkv + h, &bars->k_full[ks]);
-      ++k;
-    };
-    Batch b0, b1, b2;
-    next_batch(b0);
-    next_batch(b1);
-    next_batch(b2);
-    int id0 = ids(b0), id1 = ids(b1), mode0, mode1;
-    float vs0, vs1;
-    lookup(b0, id0, mode0, vs0);
-    while (ok && b0.nb > 0) {
-      // this batch's pages
-      int flags = kSkip, detail = EKV_DETAIL_NONE;
-      float vs = 1.f;
-      if (in_batch(b0)) {
-        flags = mode0 == EKV_MODE_COMPACT_E4M3 ? kE4 : mode0 == EKV_MODE_BASE ? kBs : mode0 == EKV_MODE_MICRO_FP4 ? kMx : 0;
-        if (id0 < 0 || id0 >= c.num_pages) detail = EKV_DETAIL_PAGE_ID;
-        else if (mode0 > EKV_MODE_MICRO_FP4) detail = EKV_DETAIL_PAGE_MODE;
-        else if ((flags & kE4) && !scale_ok(vs0)) detail = EKV_DETAIL_SCALE;
-        else if (flags & kE4) vs = vs0;
-        if (detail) {
-          report_error(c.err, EKV_ERR_DEVICE_CHECK, detail, b0.b);
-          flags = kSkip;
-        }
-      }
-      const float lsc = log2f(vs), ivs = 1.f / vs;
-      const uint32_t bad = __ballot_sync(0xffffffffu, detail != EKV_DETAIL_NONE);
-      lookup(b1, id1, mode1, vs1);                     // the next batch's, and the ids after
-      const int id2 = ids(b2);
-      for (int i = 0; i < b0.nb && ok; ++i, ++u) {
-        BlockMeta& mt = bars->meta[u % NM];
-        const int pg = lane & (kTPages - 1);
-        if (lane / kTPages == i) {
-          mt.page[pg] = id0;
-          mt.flags[pg] = (uint8_t)flags;
-          mt.lsc[pg] = lsc;
-          mt.ivs[pg] = ivs;
-          if (pg == 0) {
-            mt.bad = (int)((bad >> (i * kTPages)) & 0xffu);
-            mt.qtok = i == 0 ? b0.qtok : -1;
-            mt.tiles = (uint8_t)b0.tiles;
-            mt.last = i + 1 == b0.nb && b1.nb == 0;
-            mt.z0 = (uint8_t)max(0, b0.lo - (b0.j0 + i) * kTKeys);
-            mt.z1 = (uint8_t)min(kTKeys, b0.hi - (b0.j0 + i) * kTKeys);
+    if (warp == 0) {
+      // ------------------------------------------- producer: page checks, Q, K
+      // Pages are looked up in batches of four blocks, a page per lane: a batch's ids are fetched two
+      // batches ahead and its modes and scales one ahead, across segments. A block's description is
+      // posted kMetaAhead blocks before its keys are loaded, for the makers, whose loads take as long.
+      int u = 0, k = 0;                                  // blocks described, blocks whose keys were loaded
+      uint32_t ql[2] = {0u, 0u}, qseg = 0;
+      ExtTcSplit split;
+      split.n = 0;
+      struct Batch {
+        int b, j0, nb, lo, hi, qtok, tiles;              // keys [lo, hi); qtok < 0: not a segment's first batch
+      };
+      Segment sg;
+      sg.ja = sg.jb = 0;
+      auto next_batch = [&](Batch& x) {
+        x.qtok = -1;
+        x.tiles = 0;
+        x.nb = 0;
+        if (sg.ja >= sg.jb) {
+          if (!walk_next<ALT>(e, w, sg)) return;
+          x.qtok = sg.q0 + C::NQ * sg.i * TT;
+          x.tiles = (sg.nt[0] > 0 ? 1 : 0) | (sg.nt[1] > 0 ? 2 : 0);
+          if (sg.ja == sg.jlo && sg.jb < sg.jhi) {       // the item goes on in later CTAs
+            split.n = 1 + (int)((sg.jhi - sg.jb + per - 1) / per);
+            split.first = sg.slot;
+            split.b = sg.b;
+            split.h = h;
+            split.i = sg.i;
           }
         }
+        x.b = sg.b;
+        x.j0 = sg.ja;
+        x.nb = min(32 / kTPages, sg.jb - sg.ja);
+        x.lo = sg.lo;
+        x.hi = sg.hi;
+        sg.ja += x.nb;
+      };
+      auto in_batch = [&](const Batch& x) {
+        const int k0 = x.j0 * kTKeys + lane * kPage;
+        return lane < x.nb * kTPages && k0 + kPage > x.lo && k0 < x.hi;
+      };
+      auto ids = [&](const Batch& x) {
+        return in_batch(x) ? __ldg(c.block_table + (size_t)x.b * c.bt_stride + x.j0 * kTPages + lane) : 0;
+      };
+      auto lookup = [&](const Batch& x, int id, int& mode, float& vs) {
+        mode = VM == kXFP16 ? EKV_MODE_TARGET_FP16 : VM == kXE4M3 ? EKV_MODE_COMPACT_E4M3
+               : VM == kXMicro ? EKV_MODE_MICRO_FP4 : c.uniform_mode;
+        vs = 0.f;
+        if (!in_batch(x) || id < 0 || id >= c.num_pages) return;
+        if (VM == kXMixed && c.page_mode) mode = (int)__ldg(c.page_mode + id);
+        if ((VM == kXE4M3 || VM == kXMixed) && c.v_scales)
+          vs = __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)id * c.Hkv + h));
+      };
+      bool ok = true;
+      // the queries (first block of a segment) and keys of block k
+      auto load_k = [&]() {
+        const BlockMeta& mt = bars->meta[k % NM];
+        if (mt.qtok >= 0) {
+          const int tiles = ALT ? 1 << (qseg % nqb) : mt.tiles;
+          ++qseg;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (!((tiles >> t) & 1)) continue;
+            if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
+            if (!ok) return;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(h_rows * D * 2));
+              for (int s = 0; s < NB; ++s)
+                tma_load_5d(sQ + t * q_buf + s * q_slab, &tq, 0, 0, s, h, mt.qtok + (ALT ? 0 : t * TT), &bars->q_full[t]);
+            }
+            ++ql[t];
+          }
+        }
+        const int ks = k % NK;
+        if (k >= NK) ok = wait_warp(&bars->k_empty[ks], (uint32_t)(k / NK - 1) & 1u, abort);
+        if (!ok) return;
+        const bool load = lane < kTPages && !(mt.flags[lane & (kTPages - 1)] & kSkip);
+        const int n = __popc(__ballot_sync(0xffffffffu, load));
+        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[ks], (uint32_t)n * (kPage * D * 2));
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->meta_full[u % NM]);
-        if (u >= kMetaAhead) load_k();
-      }
-      b0 = b1;
-      id0 = id1;
-      mode0 = mode1;
-      vs0 = vs1;
-      b1 = b2;
-      id1 = id2;
+        if (load)
+          tma_load_5d(sK + ks * C::IB + lane * (2 * C::GB), &tk, 0, 0, 0, 0, mt.page[lane] * kPage * c.Hkv + h,
+                      &bars->k_full[ks]);
+        ++k;
+      };
+      Batch b0, b1, b2;
+      next_batch(b0);
+      next_batch(b1);
       next_batch(b2);
-    }
-    while (ok && k < u) load_k();
-    if (!ok && lane == 0) give_up(c.err, abort);
-    if (lane == 0) p.split[blockIdx.x] = split;
-    // the copies still in flight land before the CTA can exit
-    for (int v = max(0, k - NK); v < k; ++v) drain(&bars->k_full[v % NK], (v / NK) & 1);
-    for (int t = 0; t < 2; ++t)
-      if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
-  } else if (kDirect && warp == 3) {
-    // ------------------------------------------------ loads of FP16 value pages
-    int u = 0;
-    bool ok = any;
-    const bool run = ok;
-    for (bool last = false; ok && !last; ++u) {
-      const int vs = u % NV;
-      ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
-      if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
-      if (!ok) break;
-      const BlockMeta& mt = bars->meta[u % NM];
-      last = mt.last;
-      const int flags = lane < kTPages ? mt.flags[lane] : kSkip;
-      const int page = lane < kTPages ? mt.page[lane] : 0;
-      // a stage with rows to zero is announced on a barrier of its own; they are zeroed once it has landed
-      const bool edge = mt.z0 > 0 || mt.z1 < kTKeys;
-      const uint32_t dmask = __ballot_sync(0xffffffffu, flags == 0);
-      uint64_t* bar = edge ? &bars->v_dir[vs] : &bars->v_full[vs];
-      if (lane == 0) {
-        if (edge) mbar_arrive(&bars->v_full[vs]);
-        if (!edge || dmask) mbar_arrive_expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
-      }
-      __syncwarp();
-      if (flags == 0) tma_load_5d(sV + vs * C::IB + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + h * p.v16_head, bar);
-    }
-    if (!ok && run && lane == 0) give_up(c.err, abort);
-    if (run)
-      for (int v = max(0, u - NV); v < u; ++v) drain(&bars->v_full[v % NV], (uint32_t)(v / NV) & 1u);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------- MMA issuer
-    constexpr uint32_t idS = tc05::idesc_f16_f32(kTRows, kTKeys, false);
-    constexpr uint32_t idO = tc05::idesc_f16_f32(kTRows, D, true);
-    constexpr uint32_t HIQ = tc05::sdesc_hi(1024), HIB = tc05::sdesc_hi(C::GB);
-    const uint32_t q_lo = tc05::sdesc_lo(smem_u32(sQ), 16);
-    const uint32_t k_lo = tc05::sdesc_lo(smem_u32(sK), 16);
-    const uint32_t v_lo = tc05::sdesc_lo(smem_u32(sV), 1024);     // the next 64 columns lie 1024 B on
-    int ks = 0, vst = 0, qbuf = 0;                     // qbuf (ALT): the segment's query buffer
-    uint32_t kph = 0, vph = 0;
-    uint32_t qc[2] = {0u, 0u}, pc[2] = {0u, 0u}, oc[2] = {0u, 0u};
-    auto issue_s = [&](int t) {                        // S_t = Q_t K^T from stage ks
-      const uint32_t qa = q_lo + (ALT ? qbuf : t) * (q_buf >> 4), ka = k_lo + ks * (C::IB >> 4);
-      const uint32_t d = tbase + t * 256;
-      if (tc05::elect_one()) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc05::mma_ss(d, tc05::sdesc_join(qa + (((k >> 2) * q_slab + (k & 3) * 32) >> 4), HIQ),
-                       tc05::sdesc_join(ka + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), HIB), idS, k > 0);
-        tc05::commit(&bars->s_full[t]);
-      }
-      __syncwarp();
-    };
-    auto commit_one = [&](uint64_t* bar) {
-      if (tc05::elect_one()) tc05::commit(bar);
-      __syncwarp();
-    };
-    bool ok = true;
-    Segment sg;
-    while (ok && walk_next<ALT>(e, w, sg)) {
-      const int n = sg.jb - sg.ja;
-      if (ALT) {
-        // block j belongs to stream j mod 2: O_t += P_t V_j, then S_t of block j + 2 over P_t
-        auto issue_next = [&](int j) {                 // S of block j
-          ok = wait_spin(&bars->k_full[ks], kph, abort);
-          if (!ok) return;
-          tc05::fence_after_sync();
-          issue_s(j & 1);
-          commit_one(&bars->k_empty[ks]);
-          if (++ks == NK) ks = 0, kph ^= 1u;
-          if (j == n - 1) commit_one(&bars->q_empty[qbuf]);
-        };
-        ok = wait_spin(&bars->q_full[qbuf], qc[qbuf] & 1u, abort);
-        ++qc[qbuf];
-        for (int j = 0; j < min(n, 2) && ok; ++j) issue_next(j);
-        for (int j = 0; ok && j < n; ++j) {
-          const int t = j & 1;
-          ok = wait_spin(&bars->v_full[vst], vph, abort);
-          if (ok) ok = wait_spin(&bars->p_full[t], pc[t] & 1u, abort);
-          ++pc[t];
-          // the last segment's O is read out by both streams together
-          if (ok && j == 0 && oc[0] > 0) ok = wait_spin(&bars->o_free[0], (oc[0] - 1u) & 1u, abort);
-          if (!ok) break;
-          tc05::fence_after_sync();
-          const uint32_t va = v_lo + vst * (C::IB >> 4), pa = tbase + t * 256, od = tbase + t * 256 + 128;
-          if (tc05::elect_one()) {
-#pragma unroll
-            for (int k = 0; k < kTKeys / 16; ++k)
-              tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2 * C::GB >> 4), HIB), idO, j > 1 || k > 0);
-            if (j + 2 >= n) tc05::commit(&bars->pv_done[t]);
+      int id0 = ids(b0), id1 = ids(b1), mode0, mode1;
+      float vs0, vs1;
+      lookup(b0, id0, mode0, vs0);
+      while (ok && b0.nb > 0) {
+        // this batch's pages
+        int flags = kSkip, detail = EKV_DETAIL_NONE;
+        float vs = 1.f;
+        if (in_batch(b0)) {
+          flags = mode0 == EKV_MODE_COMPACT_E4M3 ? kE4 : mode0 == EKV_MODE_BASE ? kBs
+                  : mode0 == EKV_MODE_MICRO_FP4 ? kMx : 0;
+          if (id0 < 0 || id0 >= c.num_pages) detail = EKV_DETAIL_PAGE_ID;
+          else if (mode0 > EKV_MODE_MICRO_FP4) detail = EKV_DETAIL_PAGE_MODE;
+          else if ((flags & kE4) && !scale_ok(vs0)) detail = EKV_DETAIL_SCALE;
+          else if (flags & kE4) vs = vs0;
+          if (detail) {
+            report_error(c.err, EKV_ERR_DEVICE_CHECK, detail, b0.b);
+            flags = kSkip;
+          }
+        }
+        const float lsc = log2f(vs), ivs = 1.f / vs;
+        const uint32_t bad = __ballot_sync(0xffffffffu, detail != EKV_DETAIL_NONE);
+        lookup(b1, id1, mode1, vs1);                     // the next batch's, and the ids after
+        const int id2 = ids(b2);
+        for (int i = 0; i < b0.nb && ok; ++i, ++u) {
+          BlockMeta& mt = bars->meta[u % NM];
+          const int pg = lane & (kTPages - 1);
+          if (lane / kTPages == i) {
+            mt.page[pg] = id0;
+            mt.flags[pg] = (uint8_t)flags;
+            mt.lsc[pg] = lsc;
+            mt.ivs[pg] = ivs;
+            if (pg == 0) {
+              mt.bad = (int)((bad >> (i * kTPages)) & 0xffu);
+              mt.qtok = i == 0 ? b0.qtok : -1;
+              mt.tiles = (uint8_t)b0.tiles;
+              mt.last = i + 1 == b0.nb && b1.nb == 0;
+              mt.z0 = (uint8_t)max(0, b0.lo - (b0.j0 + i) * kTKeys);
+              mt.z1 = (uint8_t)min(kTKeys, b0.hi - (b0.j0 + i) * kTKeys);
+            }
           }
           __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->meta_full[u % NM]);
+          if (u >= kMetaAhead) load_k();
+        }
+        b0 = b1;
+        id0 = id1;
+        mode0 = mode1;
+        vs0 = vs1;
+        b1 = b2;
+        id1 = id2;
+        next_batch(b2);
+      }
+      while (ok && k < u) load_k();
+      if (!ok && lane == 0) give_up(c.err, abort);
+      if (lane == 0) p.split[blockIdx.x] = split;
+      // the copies still in flight land before the CTA can exit
+      for (int v = max(0, k - NK); v < k; ++v) drain(&bars->k_full[v % NK], (v / NK) & 1);
+      for (int t = 0; t < 2; ++t)
+        if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
+    } else if (kDirect && warp == 3) {
+      // ------------------------------------------------ loads of FP16 value pages
+      int u = 0;
+      uint32_t dir_used = 0, dir_ph = 0;                 // bit s: v_dir[s] has had a phase; parity of its next
+      bool ok = any;
+      const bool run = ok;
+      for (bool last = false; ok && !last; ++u) {
+        const int vs = u % NV;
+        ok = wait_warp(&bars->meta_full[u % NM], (uint32_t)(u / NM) & 1u, abort);
+        if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
+        if (!ok) break;
+        const BlockMeta& mt = bars->meta[u % NM];
+        last = mt.last;
+        const int flags = lane < kTPages ? mt.flags[lane] : kSkip;
+        const int page = lane < kTPages ? mt.page[lane] : 0;
+        // a stage with rows to zero is announced on a barrier of its own; they are zeroed once it has landed
+        const bool edge = mt.z0 > 0 || mt.z1 < kTKeys;
+        const uint32_t dmask = __ballot_sync(0xffffffffu, flags == 0);
+        uint64_t* bar = edge ? &bars->v_dir[vs] : &bars->v_full[vs];
+        if (lane == 0) {
+          if (edge) mbar_arrive(&bars->v_full[vs]);
+          if (!edge || dmask) mbar_arrive_expect_tx(bar, (uint32_t)__popc(dmask) * (kPage * D * 2));
+        }
+        if (edge && dmask) dir_used |= 1u << vs, dir_ph ^= 1u << vs;
+        __syncwarp();
+        if (flags == 0)
+          tma_load_5d(sV + vs * C::IB + lane * (2 * C::GB), &tv16, 0, 0, 0, 0, page * p.v16_mul + h * p.v16_head, bar);
+      }
+      if (!ok && run && lane == 0) give_up(c.err, abort);
+      if (run)
+        for (int v = max(0, u - NV); v < u; ++v) {
+          const int s = v % NV;
+          if ((dir_used >> s) & 1u) drain(&bars->v_dir[s], ((dir_ph >> s) & 1u) ^ 1u);
+          drain(&bars->v_full[s], (uint32_t)(v / NV) & 1u);
+        }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------- MMA issuer
+      constexpr uint32_t idS = tc05::idesc_f16_f32(kTRows, kTKeys, false);
+      constexpr uint32_t idO = tc05::idesc_f16_f32(kTRows, D, true);
+      constexpr uint32_t HIQ = tc05::sdesc_hi(1024), HIB = tc05::sdesc_hi(C::GB);
+      const uint32_t q_lo = tc05::sdesc_lo(smem_u32(sQ), 16);
+      const uint32_t k_lo = tc05::sdesc_lo(smem_u32(sK), 16);
+      const uint32_t v_lo = tc05::sdesc_lo(smem_u32(sV), 1024);     // the next 64 columns lie 1024 B on
+      int ks = 0, vst = 0, qbuf = 0;                     // qbuf (ALT): the segment's query buffer
+      uint32_t kph = 0, vph = 0;
+      uint32_t qc[2] = {0u, 0u}, pc[2] = {0u, 0u}, oc[2] = {0u, 0u};
+      auto issue_s = [&](int t) {                        // S_t = Q_t K^T from stage ks
+        const uint32_t qa = q_lo + (ALT ? qbuf : t) * (q_buf >> 4), ka = k_lo + ks * (C::IB >> 4);
+        const uint32_t d = tbase + t * 256;
+        if (tc05::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc05::mma_ss(d, tc05::sdesc_join(qa + (((k >> 2) * q_slab + (k & 3) * 32) >> 4), HIQ),
+                         tc05::sdesc_join(ka + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), HIB), idS, k > 0);
+          tc05::commit(&bars->s_full[t]);
+        }
+        __syncwarp();
+      };
+      auto commit_one = [&](uint64_t* bar) {
+        if (tc05::elect_one()) tc05::commit(bar);
+        __syncwarp();
+      };
+      bool ok = true;
+      Segment sg;
+      while (ok && walk_next<ALT>(e, w, sg)) {
+        const int n = sg.jb - sg.ja;
+        if (ALT) {
+          // block j belongs to stream j mod 2: O_t += P_t V_j, then S_t of block j + 2 over P_t
+          auto issue_next = [&](int j) {                 // S of block j
+            ok = wait_warp(&bars->k_full[ks], kph, abort);
+            if (!ok) return;
+            tc05::fence_after_sync();
+            issue_s(j & 1);
+            commit_one(&bars->k_empty[ks]);
+            if (++ks == NK) ks = 0, kph ^= 1u;
+            if (j == n - 1) commit_one(&bars->q_empty[qbuf]);
+          };
+          ok = wait_warp(&bars->q_full[qbuf], qc[qbuf] & 1u, abort);
+          ++qc[qbuf];
+          for (int j = 0; j < min(n, 2) && ok; ++j) issue_next(j);
+          for (int j = 0; ok && j < n; ++j) {
+            const int t = j & 1;
+            ok = wait_warp(&bars->v_full[vst], vph, abort);
+            if (ok) ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
+            ++pc[t];
+            // the last segment's O is read out by both streams together
+            if (ok && j == 0 && oc[0] > 0) ok = wait_warp(&bars->o_free[0], (oc[0] - 1u) & 1u, abort);
+            if (!ok) break;
+            tc05::fence_after_sync();
+            const uint32_t va = v_lo + vst * (C::IB >> 4), pa = tbase + t * 256, od = tbase + t * 256 + 128;
+            if (tc05::elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kTKeys / 16; ++k)
+                tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2 * C::GB >> 4), HIB), idO, j > 1 || k > 0);
+              if (j + 2 >= n) tc05::commit(&bars->pv_done[t]);
+            }
+            __syncwarp();
+            commit_one(&bars->v_empty[vst]);
+            if (++vst == NV) vst = 0, vph ^= 1u;
+            if (j + 2 < n) issue_next(j + 2);
+          }
+          ++oc[0];
+          if (++qbuf == nqb) qbuf = 0;
+          continue;
+        }
+        ok = wait_warp(&bars->k_full[ks], kph, abort);
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (sg.nt[t] == 0) continue;
+          ok = wait_warp(&bars->q_full[t], qc[t] & 1u, abort);
+          ++qc[t];
+          if (!ok) break;
+          tc05::fence_after_sync();
+          issue_s(t);
+          if (sg.nt[t] == 1) commit_one(&bars->q_empty[t]);
+        }
+        if (!ok) break;
+        commit_one(&bars->k_empty[ks]);
+        if (++ks == NK) ks = 0, kph ^= 1u;
+        for (int j = 0; ok && j < n; ++j) {
+          ok = wait_warp(&bars->v_full[vst], vph, abort);
+          if (!ok) break;
+          tc05::fence_after_sync();
+          const uint32_t va = v_lo + vst * (C::IB >> 4);
+          bool k_ready = false;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (j >= sg.nt[t]) continue;
+            ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
+            ++pc[t];
+            if (ok && j == 0 && oc[t] > 0) ok = wait_warp(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
+            if (!ok) break;
+            tc05::fence_after_sync();
+            const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
+            if (tc05::elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kTKeys / 16; ++k)
+                tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2 * C::GB >> 4), HIB), idO, j > 0 || k > 0);
+              if (j + 1 == sg.nt[t]) tc05::commit(&bars->pv_done[t]);
+            }
+            __syncwarp();
+            if (j + 1 < sg.nt[t]) {                      // the next S overwrites P, behind its product
+              ok = k_ready || wait_warp(&bars->k_full[ks], kph, abort);
+              if (!ok) break;
+              k_ready = true;
+              tc05::fence_after_sync();
+              issue_s(t);
+              if (j + 2 == sg.nt[t]) commit_one(&bars->q_empty[t]);
+            }
+          }
+          if (!ok) break;
           commit_one(&bars->v_empty[vst]);
           if (++vst == NV) vst = 0, vph ^= 1u;
-          if (j + 2 < n) issue_next(j + 2);
+          if (j + 1 < n) {
+            commit_one(&bars->k_empty[ks]);
+            if (++ks == NK) ks = 0, kph ^= 1u;
+          }
         }
-        ++oc[0];
-        if (++qbuf == nqb) qbuf = 0;
-        continue;
+        for (int t = 0; t < 2; ++t)
+          if (sg.nt[t] > 0) ++oc[t];
       }
-      ok = wait_spin(&bars->k_full[ks], kph, abort);
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (sg.nt[t] == 0) continue;
-        ok = wait_spin(&bars->q_full[t], qc[t] & 1u, abort);
-        ++qc[t];
-        if (!ok) break;
-        tc05::fence_after_sync();
-        issue_s(t);
-        if (sg.nt[t] == 1) commit_one(&bars->q_empty[t]);
-      }
-      if (!ok) break;
-      commit_one(&bars->k_empty[ks]);
-      if (++ks == NK) ks = 0, kph ^= 1u;
-      for (int j = 0; ok && j < n; ++j) {
-        ok = wait_spin(&bars->v_full[vst], vph, abort);
-        if (!ok) break;
-        tc05::fence_after_sync();
-        const uint32_t va = v_lo + vst * (C::IB >> 4);
-        bool k_ready = false;
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (j >= sg.nt[t]) continue;
-          ok = wait_spin(&bars->p_full[t], pc[t] & 1u, abort);
-          ++pc[t];
-          if (ok && j == 0 && oc[t] > 0) ok = wait_spin(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
-          if (!ok) break;
-          tc05::fence_after_sync();
-          const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
-          if (tc05::elect_one()) {
-#pragma unroll
-            for (int k = 0; k < kTKeys / 16; ++k)
-              tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2 * C::GB >> 4), HIB), idO, j > 0 || k > 0);
-            if (j + 1 == sg.nt[t]) tc05::commit(&bars->pv_done[t]);
+      if (!ok && lane == 0) give_up(c.err, abort);
+      commit_one(&bars->mma_final);
+      if (lane == 0) drain(&bars->mma_final, 0);
+    } else if (C::MK == 6 || warp != 12) {
+      // ---------------------------- the V stages: pages vi, vi + MK of every block
+      // (index: C::MK 6: warps 2, 3, 12-15; 5: 13, 2, 3, 14, 15; 4: 13, 14, 15, 2)
+      const int vi = C::MK == 6 ? (warp < 4 ? warp - 2 : warp - 10)
+                     : C::MK == 5 ? (warp == 13 ? 0 : warp < 4 ? warp - 1 : warp - 11)
+                                  : (warp < 4 ? 3 : warp - 13);
+      int issued = 0;
+      uint32_t dir_ph = 0;                               // bit s: parity of v_dir[s]'s next phase
+      bool ok = any, more = any;                         // more: blocks left to issue
+      const bool run = ok;
+      const int pg = min(vi + (lane & 1) * C::MK, kTPages - 1);   // lane 0's and lane 1's page
+      const bool two = vi + C::MK < kTPages;
+      // this warp's raw pages of the next block that has none in flight: a ring of its own
+      auto issue = [&]() {
+        ok = wait_warp(&bars->meta_full[issued % NM], (uint32_t)(issued / NM) & 1u, abort);
+        if (!ok) return;
+        const BlockMeta& mt = bars->meta[issued % NM];
+        more = !mt.last;
+        if (kRaw) {
+          const int rs = issued % NR;
+          uint64_t* bar = &bars->raw_full[rs][vi];
+          // lane 0's page and, where there is one, lane 1's: an arrival and its bytes each
+          if (lane < (two ? 2 : 1)) {
+            const int flags = mt.flags[pg];
+            uint8_t* dst = sR + rs * C::RB + pg * (kPage * D);
+            const bool mx = VM == kXMicro ? !(flags & kSkip) : VM == kXMixed && (flags & kMx);
+            const bool by = flags & (kE4 | kBs);
+            mbar_arrive_expect_tx(bar, mx ? micro_head_bytes(D) : by ? kPage * D : 0);
+            if (mx)
+              bulk_load(dst, c.v_pages + (size_t)mt.page[pg] * c.v_page_stride + h * micro_head_bytes(D),
+                      micro_head_bytes(D), bar);
+            else if (by)
+              tma_load_4d(dst, &tv8, 0, h, 0, mt.page[pg], bar);
           }
           __syncwarp();
-          if (j + 1 < sg.nt[t]) {                      // the next S overwrites P, behind its product
-            ok = k_ready || wait_spin(&bars->k_full[ks], kph, abort);
-            if (!ok) break;
-            k_ready = true;
-            tc05::fence_after_sync();
-            issue_s(t);
-            if (j + 2 == sg.nt[t]) commit_one(&bars->q_empty[t]);
-          }
         }
+        ++issued;
+      };
+      // A lane's 16 E4M3 codes of a row become the 16-byte chunks 2 c and 2 c + 1, its 32 microscaled ones chunks
+      // 4 c .. 4 c + 3. The lanes are dealt over chunks, rows and slabs such that the eight that store at a
+      // time meet eight chunk places (chunk ^ row): rows r, r ^ 1 with four c each, or four rows with two.
+      const int c8 = lane & 3, s8 = D == 128 ? (lane >> 3) & 1 : 0;
+      const int t8 = D == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2;
+      const int c4 = lane & 1, t4 = D == 128 ? ((lane >> 1) & 3) | ((lane >> 4) << 2) : lane >> 1;
+      for (int u = 0; ok && (more || u < issued); ++u) {
+        while (ok && more && issued < u + (kRaw ? NR : 1)) issue();
+        const int vs = u % NV, rs = u % NR;
+        if (ok && kRaw) ok = wait_warp(&bars->raw_full[rs][vi], (uint32_t)(u / NR) & 1u, abort);
+        if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
         if (!ok) break;
-        commit_one(&bars->v_empty[vst]);
-        if (++vst == NV) vst = 0, vph ^= 1u;
-        if (j + 1 < n) {
-          commit_one(&bars->k_empty[ks]);
-          if (++ks == NK) ks = 0, kph ^= 1u;
-        }
-      }
-      for (int t = 0; t < 2; ++t)
-        if (sg.nt[t] > 0) ++oc[t];
-    }
-    if (!ok && lane == 0) give_up(c.err, abort);
-    commit_one(&bars->mma_final);
-    if (lane == 0) drain(&bars->mma_final, 0);
-  } else if (C::MK == 6 || warp != 12) {
-    // ---------------------------- the V stages: pages vi, vi + MK of every block
-    // (index: C::MK 6: warps 2, 3, 12-15; 5: 13, 2, 3, 14, 15; 4: 13, 14, 15, 2)
-    const int vi = C::MK == 6 ? (warp < 4 ? warp - 2 : warp - 10)
-                   : C::MK == 5 ? (warp == 13 ? 0 : warp < 4 ? warp - 1 : warp - 11)
-                                : (warp < 4 ? 3 : warp - 13);
-    int issued = 0;
-    uint32_t dir_ph = 0;                               // bit s: parity of v_dir[s]'s next phase
-    bool ok = any, more = any;                 // more: blocks left to issue
-    const bool run = ok;
-    const int pg = min(vi + (lane & 1) * C::MK, kTPages - 1);   // lane 0's and lane 1's page
-    const bool two = vi + C::MK < kTPages;
-    // this warp's raw pages of the next block that has none in flight: a ring of its own
-    auto issue = [&]() {
-      ok = wait_warp(&bars->meta_full[issued % NM], (uint32_t)(issued / NM) & 1u, abort);
-      if (!ok) return;
-      const BlockMeta& mt = bars->meta[issued % NM];
-      more = !mt.last;
-      if (kRaw) {
-        const int rs = issued % NR;
-        uint64_t* bar = &bars->raw_full[rs][vi];
-        // lane 0's page and, where there is one, lane 1's: an arrival and its bytes each
-        if (lane < (two ? 2 : 1)) {
-          const int flags = mt.flags[pg];
-          uint8_t* dst = sR + rs * C::RB + pg * (kPage * D);
-          const bool mx = VM == kXMicro ? !(flags & kSkip) : VM == kXMixed && (flags & kMx);
-          const bool by = flags & (kE4 | kBs);
-          mbar_arrive_expect_tx(bar, mx ? micro_head_bytes(D) : by ? kPage * D : 0);
-          if (mx)
-            bulk_load(dst, c.v_pages + (size_t)mt.page[pg] * c.v_page_stride + h * micro_head_bytes(D), micro_head_bytes(D), bar);
-          else if (by)
-            tma_load_4d(dst, &tv8, 0, h, 0, mt.page[pg], bar);
-        }
-        __syncwarp();
-      }
-      ++issued;
-    };
-    // A lane's 16 E4M3 codes of a row become the 16-byte chunks 2 c and 2 c + 1, its 32 microscaled ones chunks
-    // 4 c .. 4 c + 3. The lanes are dealt over chunks, rows and slabs such that the eight that store at a
-    // time meet eight chunk places (chunk ^ row): rows r, r ^ 1 with four c each, or four rows with two.
-    const int c8 = lane & 3, s8 = D == 128 ? (lane >> 3) & 1 : 0;
-    const int t8 = D == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2;
-    const int c4 = lane & 1, t4 = D == 128 ? ((lane >> 1) & 3) | ((lane >> 4) << 2) : lane >> 1;
-    for (int u = 0; ok && (more || u < issued); ++u) {
-      while (ok && more && issued < u + (kRaw ? NR : 1)) issue();
-      const int vs = u % NV, rs = u % NR;
-      if (ok && kRaw) ok = wait_warp(&bars->raw_full[rs][vi], (uint32_t)(u / NR) & 1u, abort);
-      if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
-      if (!ok) break;
-      const BlockMeta& mt = bars->meta[u % NM];
-      const bool edge = mt.z0 > 0 || mt.z1 < kTKeys;
+        const BlockMeta& mt = bars->meta[u % NM];
+        const bool edge = mt.z0 > 0 || mt.z1 < kTKeys;
 #pragma unroll 1
-      for (int page = vi; page < kTPages; page += C::MK) {
-        const int fl = mt.flags[page];
-        uint8_t* dv = sV + vs * C::IB + page * (2 * C::GB);
-        const uint8_t* src = sR + rs * C::RB + page * (kPage * D);
-        if (VM == kXMicro ? !(fl & kSkip) : VM == kXMixed && (fl & kMx)) {
+        for (int page = vi; page < kTPages; page += C::MK) {
+          const int fl = mt.flags[page];
+          uint8_t* dv = sV + vs * C::IB + page * (2 * C::GB);
+          const uint8_t* src = sR + rs * C::RB + page * (kPage * D);
+          if (VM == kXMicro ? !(fl & kSkip) : VM == kXMixed && (fl & kMx)) {
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x) {
-            const int t = t4 + x * (1024 / D), r = t & 7, q = 2 * s8 + c4;
-            const uint4 codes = *reinterpret_cast<const uint4*>(src + t * (D / 2) + q * 16);
-            uint32_t sb = src[micro_scale_off(D) + t * (D / kMicroBlock) + q];
-            if (!micro_scale_ok(sb)) {
-              if (page * kPage + t >= mt.z0 && page * kPage + t < mt.z1)
-                report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SCALE, -1);
-              sb = 0;
+            for (int x = 0; x < D / 64; ++x) {
+              const int t = t4 + x * (1024 / D), r = t & 7, q = 2 * s8 + c4;
+              const uint4 codes = *reinterpret_cast<const uint4*>(src + t * (D / 2) + q * 16);
+              uint32_t sb = src[micro_scale_off(D) + t * (D / kMicroBlock) + q];
+              if (!micro_scale_ok(sb)) {
+                if (page * kPage + t >= mt.z0 && page * kPage + t < mt.z1)
+                  report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SCALE, -1);
+                sb = 0;
+              }
+              const __half2 s2 = micro_scale_h2(sb);
+              uint8_t* row = dv + (t >> 3) * C::GB + s8 * 1024 + r * 128;
+              *reinterpret_cast<uint4*>(row + ((4 * c4) ^ r) * 16) = micro_decode8(codes.x, s2);
+              *reinterpret_cast<uint4*>(row + ((4 * c4 + 1) ^ r) * 16) = micro_decode8(codes.y, s2);
+              *reinterpret_cast<uint4*>(row + ((4 * c4 + 2) ^ r) * 16) = micro_decode8(codes.z, s2);
+              *reinterpret_cast<uint4*>(row + ((4 * c4 + 3) ^ r) * 16) = micro_decode8(codes.w, s2);
             }
-            const __half2 s2 = micro_scale_h2(sb);
-            uint8_t* row = dv + (t >> 3) * C::GB + s8 * 1024 + r * 128;
-            *reinterpret_cast<uint4*>(row + ((4 * c4) ^ r) * 16) = micro_decode8(codes.x, s2);
-            *reinterpret_cast<uint4*>(row + ((4 * c4 + 1) ^ r) * 16) = micro_decode8(codes.y, s2);
-            *reinterpret_cast<uint4*>(row + ((4 * c4 + 2) ^ r) * 16) = micro_decode8(codes.z, s2);
-            *reinterpret_cast<uint4*>(row + ((4 * c4 + 3) ^ r) * 16) = micro_decode8(codes.w, s2);
-          }
-        } else if (kRaw && (fl & (kE4 | kBs))) {
+          } else if (kRaw && (fl & (kE4 | kBs))) {
 #pragma unroll (VM == kXMixed ? 2 : D / 32)
-          for (int x = 0; x < D / 32; ++x) {
-            const int t = t8 + x * (512 / D), r = t & 7, ch = 4 * s8 + c8;
-            uint4 lo, hi;
-            const uint4 q = *reinterpret_cast<const uint4*>(src + (D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16)));
-            if (VM == kXMixed && (fl & kBs)) {
-              lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
-                              __byte_perm(q.y, 0u, 0x3424));
-              hi = make_uint4(__byte_perm(q.z, 0u, 0x1404), __byte_perm(q.z, 0u, 0x3424), __byte_perm(q.w, 0u, 0x1404),
-                              __byte_perm(q.w, 0u, 0x3424));
-            } else {
-              lo = make_uint4(bits(e4m3x2_to_half2((uint16_t)q.x)), bits(e4m3x2_to_half2((uint16_t)(q.x >> 16))),
-                              bits(e4m3x2_to_half2((uint16_t)q.y)), bits(e4m3x2_to_half2((uint16_t)(q.y >> 16))));
-              hi = make_uint4(bits(e4m3x2_to_half2((uint16_t)q.z)), bits(e4m3x2_to_half2((uint16_t)(q.z >> 16))),
-                              bits(e4m3x2_to_half2((uint16_t)q.w)), bits(e4m3x2_to_half2((uint16_t)(q.w >> 16))));
+            for (int x = 0; x < D / 32; ++x) {
+              const int t = t8 + x * (512 / D), r = t & 7, ch = 4 * s8 + c8;
+              uint4 lo, hi;
+              const uint4 q = *reinterpret_cast<const uint4*>(src + (D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16)));
+              if (VM == kXMixed && (fl & kBs)) {
+                lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
+                                __byte_perm(q.y, 0u, 0x3424));
+                hi = make_uint4(__byte_perm(q.z, 0u, 0x1404), __byte_perm(q.z, 0u, 0x3424), __byte_perm(q.w, 0u, 0x1404),
+                                __byte_perm(q.w, 0u, 0x3424));
+              } else {
+                lo = make_uint4(bits(e4m3x2_to_half2((uint16_t)q.x)), bits(e4m3x2_to_half2((uint16_t)(q.x >> 16))),
+                                bits(e4m3x2_to_half2((uint16_t)q.y)), bits(e4m3x2_to_half2((uint16_t)(q.y >> 16))));
+                hi = make_uint4(bits(e4m3x2_to_half2((uint16_t)q.z)), bits(e4m3x2_to_half2((uint16_t)(q.z >> 16))),
+                                bits(e4m3x2_to_half2((uint16_t)q.w)), bits(e4m3x2_to_half2((uint16_t)(q.w >> 16))));
+              }
+              uint8_t* row = dv + (t >> 3) * C::GB + s8 * 1024 + r * 128;
+              *reinterpret_cast<uint4*>(row + ((2 * c8) ^ r) * 16) = lo;
+              *reinterpret_cast<uint4*>(row + ((2 * c8 + 1) ^ r) * 16) = hi;
             }
-            uint8_t* row = dv + (t >> 3) * C::GB + s8 * 1024 + r * 128;
-            *reinterpret_cast<uint4*>(row + ((2 * c8) ^ r) * 16) = lo;
-            *reinterpret_cast<uint4*>(row + ((2 * c8 + 1) ^ r) * 16) = hi;
           }
         }
-      }
-      if (kDirect && edge && __any_sync(0xffffffffu, lane < kTPages && mt.flags[lane & (kTPages - 1)] == 0)) {
-        ok = wait_warp(&bars->v_dir[vs], (dir_ph >> vs) & 1u, abort);
-        dir_ph ^= 1u << vs;
-        if (!ok) break;
-      }
-      // keys that no row of the item sees, and pages that were not loaded: zeros, whatever they hold
-      const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (mt.flags[lane & (kTPages - 1)] & kSkip));
-      if (edge || smask) {
+        if (kDirect && edge && __any_sync(0xffffffffu, lane < kTPages && mt.flags[lane & (kTPages - 1)] == 0)) {
+          ok = wait_warp(&bars->v_dir[vs], (dir_ph >> vs) & 1u, abort);
+          dir_ph ^= 1u << vs;
+          if (!ok) break;
+        }
+        // keys that no row of the item sees, and pages that were not loaded: zeros, whatever they hold
+        const uint32_t smask = __ballot_sync(0xffffffffu, lane < kTPages && (mt.flags[lane & (kTPages - 1)] & kSkip));
+        if (edge || smask) {
+          __syncwarp();
+          for (int page = vi; page < kTPages; page += C::MK)
+            for (int x = lane; x < kPage * (D / 8); x += 32) {
+              const int key = page * kPage + x / (D / 8), cz = x % (D / 8);
+              if (key < mt.z0 || key >= mt.z1 || ((smask >> page) & 1u))
+                *reinterpret_cast<uint4*>(sV + vs * C::IB + (key >> 3) * C::GB + (cz >> 3) * 1024 + (key & 7) * 128 + (cz & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        fence_async();                                   // written for the MMAs; the raw bytes read for their refill
         __syncwarp();
-        for (int page = vi; page < kTPages; page += C::MK)
-          for (int x = lane; x < kPage * (D / 8); x += 32) {
-            const int key = page * kPage + x / (D / 8), cz = x % (D / 8);
-            if (key < mt.z0 || key >= mt.z1 || ((smask >> page) & 1u))
-              *reinterpret_cast<uint4*>(sV + vs * C::IB + (key >> 3) * C::GB + (cz >> 3) * 1024 + (key & 7) * 128 + (cz & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          }
+        if (lane == 0) mbar_arrive(&bars->v_full[vs]);
       }
-      fence_async();                                   // written for the MMAs; the raw bytes read for their refill
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->v_full[vs]);
+      if (!ok && run && lane == 0) give_up(c.err, abort);
+      if (kRaw)
+        for (int v = max(0, issued - NR); v < issued; ++v) drain(&bars->raw_full[v % NR][vi], (uint32_t)(v / NR) & 1u);
     }
-    if (!ok && run && lane == 0) give_up(c.err, abort);
-    if (kRaw)
-      for (int v = max(0, issued - NR); v < issued; ++v) drain(&bars->raw_full[v % NR][vi], (uint32_t)(v / NR) & 1u);
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     if (!ALT || (warp & 3) < nw) {                     // (the others have no rows)
-    // ------------------------------------------------------- softmax, tile t
-    const int t = (warp - 4) >> 2, r = threadIdx.x - 128 - t * kTRows;
-    const uint32_t lanebase = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const float qs = e.qscale;
-    const float osc = p.scale_ptr ? __ldg(p.scale_ptr) : 1.f;   // one E4M3 scale for every code
-    const uint32_t t_s = tbase + t * 256 + lanebase, t_o = tbase + t * 256 + 128 + lanebase;
-    uint32_t sc = 0, pvc = 0, seg = 0;                 // phases: s_full, pv_done; segments
-    int u = 0;
-    bool ok = true;
-    const int tok_t = r / e.G;                         // this thread's token within the tile
-    int walk = pack_walk(w);
-    while (ok) {
-      // what the rows need of the segment; orow < 0: a row past the sequence
-      int nmine, u0 = u, ja, pos, lo, all_lo, all_hi, slot;
-      long long orow;
-      {
-        Segment sg;
-        Walk v = unpack_walk(e, walk);
-        if (!walk_next<ALT>(e, v, sg)) break;
-        walk = pack_walk(v);
-        nmine = sg.nt[t];
-        u += sg.jb - sg.ja;
-        ja = sg.ja;
-        const int first = (ALT ? sg.i : 2 * sg.i + t) * TT;   // the tile's first token
-        const int tok = first + tok_t;
-        pos = sg.t0 + tok;
-        lo = max(pos - e.window, -1);                  // the row sees keys lo + 1 .. pos
-        // keys that every valid row sees: from the last row's window start to the first row's own
-        all_lo = sg.t0 + min(first + TT, sg.n) - 1 - e.window;
-        all_hi = sg.t0 + first;
-        slot = sg.whole ? -1 : sg.slot;
-        orow = tok_t < TT && tok < sg.n ? (long long)(sg.q0 + tok) * c.Hq + h * e.G + r % e.G : -1;
-      }
-      const bool valid = orow >= 0, whole = slot < 0;
-      float m_ref = -INFINITY, l = 0.f;
-      bool bad = false;
-      for (int jj = 0; jj < nmine; ++jj) {
-        const int blk = ALT ? 2 * jj + t : jj;         // block of the segment
-        ok = wait_spin(&bars->s_full[t], sc & 1u, abort);
-        ++sc;
-        if (ok) ok = wait_spin(&bars->meta_full[(u0 + blk) % NM], (uint32_t)((u0 + blk) / NM) & 1u, abort);
-        if (!ok) break;
-        tc05::fence_after_sync();
-        const BlockMeta& mt = bars->meta[(u0 + blk) % NM];
-        const int k0 = (ja + blk) * kTKeys;
-        const int badp = mt.bad;
-        const bool masked = k0 + kTKeys - 1 > all_hi || k0 <= all_lo || badp;
-        const int hi_c = pos - k0, lo_c = lo - k0;
-        if (badp) {
-          for (int pg = 0; pg < kTPages; ++pg)
-            if (((badp >> pg) & 1) && pg * kPage <= hi_c && pg * kPage + kPage - 1 > lo_c) bad = true;
+      // ------------------------------------------------------- softmax, tile t
+      const int t = (warp - 4) >> 2, r = threadIdx.x - 128 - t * kTRows;
+      const uint32_t lanebase = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const float qs = e.qscale;
+      const float osc = p.scale_ptr ? __ldg(p.scale_ptr) : 1.f;   // one E4M3 scale for every code
+      const uint32_t t_s = tbase + t * 256 + lanebase, t_o = tbase + t * 256 + 128 + lanebase;
+      uint32_t sc = 0, pvc = 0, seg = 0;                 // phases: s_full, pv_done; segments
+      int u = 0;
+      bool ok = true;
+      const int tok_t = r / e.G;                         // this thread's token within the tile
+      int walk = pack_walk(w);
+      while (ok) {
+        // what the rows need of the segment; orow < 0: a row past the sequence
+        int nmine, u0 = u, ja, pos, lo, all_lo, all_hi, slot;
+        long long orow;
+        {
+          Segment sg;
+          Walk v = unpack_walk(e, walk);
+          if (!walk_next<ALT>(e, v, sg)) break;
+          walk = pack_walk(v);
+          nmine = sg.nt[t];
+          u += sg.jb - sg.ja;
+          ja = sg.ja;
+          const int first = (ALT ? sg.i : 2 * sg.i + t) * TT;   // the tile's first token
+          const int tok = first + tok_t;
+          pos = sg.t0 + tok;
+          lo = max(pos - e.window, -1);                  // the row sees keys lo + 1 .. pos
+          // keys that every valid row sees: from the last row's window start to the first row's own
+          all_lo = sg.t0 + min(first + TT, sg.n) - 1 - e.window;
+          all_hi = sg.t0 + first;
+          slot = sg.whole ? -1 : sg.slot;
+          orow = tok_t < TT && tok < sg.n ? (long long)(sg.q0 + tok) * c.Hq + h * e.G + r % e.G : -1;
         }
-        // The row's maximum, in log2 units. NH 1: the row stays in registers. NH 2: half of it at a time, read
-        // again for the weights (and written back where masked), for half the code: the loops of a CTA's
-        // roles share one instruction cache, and where the makers' loop is the long one (mixed pages)
-        // or each softmax warp runs alone (ALT) that counts for more than the second read. Measured,
-        // NH 1 / 2: mixed chunks under a window 150 / 144 us, 48 x 5 tokens over mixed pages 166 / 161 us,
-        // 4,096 tokens behind 16K of E4M3 884 / 916 us.
-        constexpr int NH = ALT || VM == kXMixed ? 2 : 1, NC = 4 / NH;
-        uint32_t a[NC][32];
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int hf = 0; hf < NH; ++hf) {
-#pragma unroll
-          for (int c4 = 0; c4 < NC; ++c4) tc05::ld32(t_s + 32 * (NC * hf + c4), a[c4]);
-          tc05::wait_ld();
-          if (masked) {
-            const int hc = hi_c - 32 * NC * hf, lc = lo_c - 32 * NC * hf;
-#pragma unroll
-            for (int c4 = 0; c4 < NC; ++c4)
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (32 * c4 + x > hc || 32 * c4 + x <= lc) a[c4][x] = __float_as_uint(-INFINITY);
-            if (NH > 1) {
-#pragma unroll
-              for (int c4 = 0; c4 < NC; ++c4) tc05::st32(t_s + 32 * (NC * hf + c4), a[c4]);
-              tc05::wait_st();
-            }
+        const bool valid = orow >= 0, whole = slot < 0;
+        float m_ref = -INFINITY, l = 0.f;
+        bool bad = false;
+        for (int jj = 0; jj < nmine; ++jj) {
+          const int blk = ALT ? 2 * jj + t : jj;         // block of the segment
+          ok = wait_warp(&bars->s_full[t], sc & 1u, abort);
+          ++sc;
+          if (ok) ok = wait_warp(&bars->meta_full[(u0 + blk) % NM], (uint32_t)((u0 + blk) / NM) & 1u, abort);
+          if (!ok) break;
+          tc05::fence_after_sync();
+          const BlockMeta& mt = bars->meta[(u0 + blk) % NM];
+          const int k0 = (ja + blk) * kTKeys;
+          const int badp = mt.bad;
+          const bool masked = k0 + kTKeys - 1 > all_hi || k0 <= all_lo || badp;
+          const int hi_c = pos - k0, lo_c = lo - k0;
+          if (badp) {
+            for (int pg = 0; pg < kTPages; ++pg)
+              if (((badp >> pg) & 1) && pg * kPage <= hi_c && pg * kPage + kPage - 1 > lo_c) bad = true;
           }
-#pragma unroll
-          for (int c4 = 0; c4 < NC; ++c4) {
-            float m8[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t* y = a[c4] + 8 * q;
-              m8[q] = fmaxf(max3(max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2])),
-                                 __uint_as_float(y[3]), __uint_as_float(y[4])),
-                            max3(__uint_as_float(y[5]), __uint_as_float(y[6]), __uint_as_float(y[7])));
-            }
-            if (PS) {
-              const float* lsc = mt.lsc + 2 * (NC * hf + c4);
-              mx = max3(mx, fmaf(fmaxf(m8[0], m8[1]), qs, lsc[0]), fmaf(fmaxf(m8[2], m8[3]), qs, lsc[1]));
-            } else {
-              mx = max3(mx, max3(m8[0], m8[1], m8[2]), m8[3]);
-            }
-          }
-        }
-        if (!PS) mx *= qs;
-        const float m_new = fmaxf(m_ref, mx);
-        const bool need = m_new > m_ref + 8.f;
-        if (__any_sync(0xffffffffu, need)) {
-          const float alpha = need ? ex2(m_ref - m_new) : 1.f;
-          if (jj > 0) {
+          // The row's maximum, in log2 units. NH 1: the row stays in registers. NH 2: half of it at a time, read
+          // again for the weights (and written back where masked), for half the code: the loops of a CTA's
+          // roles share one instruction cache, and where the makers' loop is the long one (mixed pages)
+          // or each softmax warp runs alone (ALT) that counts for more than the second read. Measured,
+          // NH 1 / 2: mixed chunks under a window 150 / 144 us, 48 x 5 tokens over mixed pages 166 / 161 us,
+          // 4,096 tokens behind 16K of E4M3 884 / 916 us.
+          constexpr int NH = ALT || VM == kXMixed ? 2 : 1, NC = 4 / NH;
+          uint32_t a[NC][32];
+          float mx = -INFINITY;
 #pragma unroll 1
-            for (int x = 0; x < D / 16; ++x) {
-              uint32_t o[16];
-              tld16(t_o + 16 * x, o);
-              tc05::wait_ld();
-#pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
-              tst16(t_o + 16 * x, o);
-            }
-          }
-          l *= alpha;
-          if (need) m_ref = m_new;
-        }
-        // a row that has seen no key yet keeps m = -inf: its weights are 2^-inf = 0
-        const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
-        // (P's columns 16 c .. of chunk c lie over S columns that have been read by then)
-#pragma unroll 1
-        for (int hf = 0; hf < NH; ++hf) {
-          if (NH > 1) {
+          for (int hf = 0; hf < NH; ++hf) {
 #pragma unroll
             for (int c4 = 0; c4 < NC; ++c4) tc05::ld32(t_s + 32 * (NC * hf + c4), a[c4]);
             tc05::wait_ld();
-          }
+            if (masked) {
+              const int hc = hi_c - 32 * NC * hf, lc = lo_c - 32 * NC * hf;
 #pragma unroll
-          for (int c4 = 0; c4 < NC; ++c4) {
+              for (int c4 = 0; c4 < NC; ++c4)
 #pragma unroll
-            for (int pg = 0; pg < 2; ++pg) {
-              const float add = PS ? nm + mt.lsc[2 * (NC * hf + c4) + pg] : nm;
-              float la[2] = {0.f, 0.f}, lb[2] = {0.f, 0.f};
+                for (int x = 0; x < 32; ++x)
+                  if (32 * c4 + x > hc || 32 * c4 + x <= lc) a[c4][x] = __float_as_uint(-INFINITY);
+              if (NH > 1) {
 #pragma unroll
-              for (int x = 8 * pg; x < 8 * pg + 8; ++x) {
-                float a0, a1;
-                ffma2(a0, a1, __uint_as_float(a[c4][2 * x]), __uint_as_float(a[c4][2 * x + 1]), qs, add);
-                const float p0 = ex2(a0), p1 = ex2(a1);
-                fadd2(la[x & 1], lb[x & 1], p0, p1);
-                a[c4][x] = pack2(p0, p1);
+                for (int c4 = 0; c4 < NC; ++c4) tc05::st32(t_s + 32 * (NC * hf + c4), a[c4]);
+                tc05::wait_st();
               }
-              fadd2(la[0], lb[0], la[1], lb[1]);
-              l = PS ? fmaf(la[0] + lb[0], mt.ivs[2 * (NC * hf + c4) + pg], l) : l + (la[0] + lb[0]);
             }
-            tst16(t_s + 16 * (NC * hf + c4), &a[c4][0]);
+#pragma unroll
+            for (int c4 = 0; c4 < NC; ++c4) {
+              float m8[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t* y = a[c4] + 8 * q;
+                m8[q] = fmaxf(max3(max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2])),
+                                   __uint_as_float(y[3]), __uint_as_float(y[4])),
+                              max3(__uint_as_float(y[5]), __uint_as_float(y[6]), __uint_as_float(y[7])));
+              }
+              if (PS) {
+                const float* lsc = mt.lsc + 2 * (NC * hf + c4);
+                mx = max3(mx, fmaf(fmaxf(m8[0], m8[1]), qs, lsc[0]), fmaf(fmaxf(m8[2], m8[3]), qs, lsc[1]));
+              } else {
+                mx = max3(mx, max3(m8[0], m8[1], m8[2]), m8[3]);
+              }
+            }
           }
+          if (!PS) mx *= qs;
+          const float m_new = fmaxf(m_ref, mx);
+          const bool need = m_new > m_ref + 8.f;
+          if (__any_sync(0xffffffffu, need)) {
+            const float alpha = need ? ex2(m_ref - m_new) : 1.f;
+            if (jj > 0) {
+#pragma unroll 1
+              for (int x = 0; x < D / 16; ++x) {
+                uint32_t o[16];
+                tld16(t_o + 16 * x, o);
+                tc05::wait_ld();
+#pragma unroll
+                for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
+                tst16(t_o + 16 * x, o);
+              }
+            }
+            l *= alpha;
+            if (need) m_ref = m_new;
+          }
+          // a row that has seen no key yet keeps m = -inf: its weights are 2^-inf = 0
+          const float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+          // (P's columns 16 c .. of chunk c lie over S columns that have been read by then)
+#pragma unroll 1
+          for (int hf = 0; hf < NH; ++hf) {
+            if (NH > 1) {
+#pragma unroll
+              for (int c4 = 0; c4 < NC; ++c4) tc05::ld32(t_s + 32 * (NC * hf + c4), a[c4]);
+              tc05::wait_ld();
+            }
+#pragma unroll
+            for (int c4 = 0; c4 < NC; ++c4) {
+#pragma unroll
+              for (int pg = 0; pg < 2; ++pg) {
+                const float add = PS ? nm + mt.lsc[2 * (NC * hf + c4) + pg] : nm;
+                float la[2] = {0.f, 0.f}, lb[2] = {0.f, 0.f};
+#pragma unroll
+                for (int x = 8 * pg; x < 8 * pg + 8; ++x) {
+                  float a0, a1;
+                  ffma2(a0, a1, __uint_as_float(a[c4][2 * x]), __uint_as_float(a[c4][2 * x + 1]), qs, add);
+                  const float p0 = ex2(a0), p1 = ex2(a1);
+                  fadd2(la[x & 1], lb[x & 1], p0, p1);
+                  a[c4][x] = pack2(p0, p1);
+                }
+                fadd2(la[0], lb[0], la[1], lb[1]);
+                l = PS ? fmaf(la[0] + lb[0], mt.ivs[2 * (NC * hf + c4) + pg], l) : l + (la[0] + lb[0]);
+              }
+              tst16(t_s + 16 * (NC * hf + c4), &a[c4][0]);
+            }
+          }
+          tc05::wait_st();
+          tc05::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[t]);
         }
-        tc05::wait_st();
-        tc05::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[t]);
-      }
-      if (!ok) break;
-      const size_t prow = (size_t)max(slot, 0) * (2 * kTRows) + (ALT ? 0 : t) * kTRows + r;
-      if (ALT) {
-        // join the streams: each posts (m, l) and reads the other's, and takes half of the columns of
-        // both O, which lie in its own tensor-memory lanes
-        if (nmine > 0) {
-          ok = wait_spin(&bars->pv_done[t], pvc & 1u, abort);
-          ++pvc;
-          if (!ok) break;
-        }
-        // the other stream has read what the last segment posted (it arrived here afterwards)
-        if (seg > 0) ok = wait_spin(&bars->o_free[0], (seg - 1u) & 1u, abort);
         if (!ok) break;
-        float2 (&xch)[2][ALT ? kAltRows : 1] = bars->xch;
-        xch[t][r] = make_float2(m_ref, bad ? kBadRecord : l);
-        tc05::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->x_full[t]);
-        ok = wait_spin(&bars->x_full[1 - t], seg & 1u, abort);
-        ++seg;
+        const size_t prow = (size_t)max(slot, 0) * (2 * kTRows) + (ALT ? 0 : t) * kTRows + r;
+        if (ALT) {
+          // join the streams: each posts (m, l) and reads the other's, and takes half of the columns of
+          // both O, which lie in its own tensor-memory lanes
+          if (nmine > 0) {
+            ok = wait_warp(&bars->pv_done[t], pvc & 1u, abort);
+            ++pvc;
+            if (!ok) break;
+          }
+          // the other stream has read what the last segment posted (it arrived here afterwards)
+          if (seg > 0) ok = wait_warp(&bars->o_free[0], (seg - 1u) & 1u, abort);
+          if (!ok) break;
+          float2 (&xch)[2][ALT ? kAltRows : 1] = bars->xch;
+          xch[t][r] = make_float2(m_ref, bad ? kBadRecord : l);
+          tc05::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->x_full[t]);
+          ok = wait_warp(&bars->x_full[1 - t], seg & 1u, abort);
+          ++seg;
+          if (!ok) break;
+          tc05::fence_after_sync();
+          const float2 other = xch[1 - t][r];
+          bad = bad || other.y < 0.f;
+          const float M = fmaxf(m_ref, other.x);
+          float w0 = l != 0.f ? ex2(m_ref - M) : 0.f, w1 = other.y != 0.f ? ex2(other.x - M) : 0.f;
+          const float L = fmaf(l, w0, other.y * w1);     // (of no use where bad)
+          if (t == 1) {                                  // w0 weighs stream 0
+            const float x = w0;
+            w0 = w1;
+            w1 = x;
+          }
+          const bool none = bad || L == 0.f;             // (a NaN goes on to the output)
+          const float inv = none ? 0.f : osc / L;
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) {
+            const int col = t * (D / 2) + 32 * x;
+            uint32_t o0[32], o1[32];
+            tc05::ld32(tbase + 128 + lanebase + col, o0);
+            tc05::ld32(tbase + 384 + lanebase + col, o1);
+            tc05::wait_ld();
+            if (x == D / 64 - 1) {
+              tc05::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->o_free[0]);
+            }
+#pragma unroll
+            for (int y = 0; y < 32; ++y) {               // (a stream without blocks left no O: weight 0)
+              const float a0 = w0 > 0.f ? __uint_as_float(o0[y]) * w0 : 0.f;
+              o0[y] = __float_as_uint(w1 > 0.f ? fmaf(__uint_as_float(o1[y]), w1, a0) : a0);
+            }
+            if (valid && whole) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                uint4 q;
+                q.x = pack2(__uint_as_float(o0[8 * y + 0]) * inv, __uint_as_float(o0[8 * y + 1]) * inv);
+                q.y = pack2(__uint_as_float(o0[8 * y + 2]) * inv, __uint_as_float(o0[8 * y + 3]) * inv);
+                q.z = pack2(__uint_as_float(o0[8 * y + 4]) * inv, __uint_as_float(o0[8 * y + 5]) * inv);
+                q.w = pack2(__uint_as_float(o0[8 * y + 6]) * inv, __uint_as_float(o0[8 * y + 7]) * inv);
+                if (none) q = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(e.out + orow * D + col + 8 * y) = q;
+              }
+            } else if (valid) {
+#pragma unroll
+              for (int y = 0; y < 8; ++y)
+                *reinterpret_cast<uint4*>(p.part_acc + prow * D + col + 4 * y) =
+                    make_uint4(o0[4 * y], o0[4 * y + 1], o0[4 * y + 2], o0[4 * y + 3]);
+            }
+          }
+          if (valid && t == 0) {
+            if (!whole) p.part_ml[prow] = make_float2(M, bad ? kBadRecord : L);
+            else if (e.lse) e.lse[orow] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+          }
+          continue;
+        }
+        if (nmine == 0) {
+          if (!whole && valid) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
+          continue;
+        }
+        ok = wait_warp(&bars->pv_done[t], pvc & 1u, abort);
+        ++pvc;
         if (!ok) break;
         tc05::fence_after_sync();
-        const float2 other = xch[1 - t][r];
-        bad = bad || other.y < 0.f;
-        const float M = fmaxf(m_ref, other.x);
-        float w0 = l > 0.f ? ex2(m_ref - M) : 0.f, w1 = other.y > 0.f ? ex2(other.x - M) : 0.f;
-        const float L = fmaf(l, w0, fmaxf(other.y, 0.f) * w1);
-        if (t == 1) {                                  // w0 weighs stream 0
-          const float x = w0;
-          w0 = w1;
-          w1 = x;
-        }
-        const bool none = bad || !(L > 0.f);
-        const float inv = none ? 0.f : osc / L;
+        const bool none = bad || l == 0.f;               // (a NaN goes on to the output)
+        const float inv = none ? 0.f : osc / l;
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          const int col = t * (D / 2) + 32 * x;
-          uint32_t o0[32], o1[32];
-          tc05::ld32(tbase + 128 + lanebase + col, o0);
-          tc05::ld32(tbase + 384 + lanebase + col, o1);
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t o[32];
+          tc05::ld32(t_o + 32 * x, o);
           tc05::wait_ld();
-          if (x == D / 64 - 1) {
+          if (x == D / 32 - 1) {                         // O is read out: the next item may overwrite it
             tc05::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->o_free[0]);
-          }
-#pragma unroll
-          for (int y = 0; y < 32; ++y) {               // (a stream without blocks left no O: weight 0)
-            const float a0 = w0 > 0.f ? __uint_as_float(o0[y]) * w0 : 0.f;
-            o0[y] = __float_as_uint(w1 > 0.f ? fmaf(__uint_as_float(o1[y]), w1, a0) : a0);
+            if (lane == 0) mbar_arrive(&bars->o_free[t]);
           }
           if (valid && whole) {
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               uint4 q;
-              q.x = pack2(__uint_as_float(o0[8 * y + 0]) * inv, __uint_as_float(o0[8 * y + 1]) * inv);
-              q.y = pack2(__uint_as_float(o0[8 * y + 2]) * inv, __uint_as_float(o0[8 * y + 3]) * inv);
-              q.z = pack2(__uint_as_float(o0[8 * y + 4]) * inv, __uint_as_float(o0[8 * y + 5]) * inv);
-              q.w = pack2(__uint_as_float(o0[8 * y + 6]) * inv, __uint_as_float(o0[8 * y + 7]) * inv);
+              q.x = pack2(__uint_as_float(o[8 * y + 0]) * inv, __uint_as_float(o[8 * y + 1]) * inv);
+              q.y = pack2(__uint_as_float(o[8 * y + 2]) * inv, __uint_as_float(o[8 * y + 3]) * inv);
+              q.z = pack2(__uint_as_float(o[8 * y + 4]) * inv, __uint_as_float(o[8 * y + 5]) * inv);
+              q.w = pack2(__uint_as_float(o[8 * y + 6]) * inv, __uint_as_float(o[8 * y + 7]) * inv);
               if (none) q = make_uint4(0u, 0u, 0u, 0u);
-              *reinterpret_cast<uint4*>(e.out + orow * D + col + 8 * y) = q;
+              *reinterpret_cast<uint4*>(e.out + orow * D + 32 * x + 8 * y) = q;
             }
           } else if (valid) {
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-              *reinterpret_cast<uint4*>(p.part_acc + prow * D + col + 4 * y) =
-                  make_uint4(o0[4 * y], o0[4 * y + 1], o0[4 * y + 2], o0[4 * y + 3]);
+              *reinterpret_cast<uint4*>(p.part_acc + prow * D + 32 * x + 4 * y) =
+                  make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
           }
         }
-        if (valid && t == 0) {
-          if (!whole) p.part_ml[prow] = make_float2(M, bad ? kBadRecord : L);
-          else if (e.lse) e.lse[orow] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-        }
-        continue;
-      }
-      if (nmine == 0) {
-        if (!whole && valid) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
-        continue;
-      }
-      ok = wait_spin(&bars->pv_done[t], pvc & 1u, abort);
-      ++pvc;
-      if (!ok) break;
-      tc05::fence_after_sync();
-      const bool none = bad || !(l > 0.f);
-      const float inv = none ? 0.f : osc / l;
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x) {
-        uint32_t o[32];
-        tc05::ld32(t_o + 32 * x, o);
-        tc05::wait_ld();
-        if (x == D / 32 - 1) {                         // O is read out: the next item may overwrite it
-          tc05::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->o_free[t]);
-        }
-        if (valid && whole) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            uint4 q;
-            q.x = pack2(__uint_as_float(o[8 * y + 0]) * inv, __uint_as_float(o[8 * y + 1]) * inv);
-            q.y = pack2(__uint_as_float(o[8 * y + 2]) * inv, __uint_as_float(o[8 * y + 3]) * inv);
-            q.z = pack2(__uint_as_float(o[8 * y + 4]) * inv, __uint_as_float(o[8 * y + 5]) * inv);
-            q.w = pack2(__uint_as_float(o[8 * y + 6]) * inv, __uint_as_float(o[8 * y + 7]) * inv);
-            if (none) q = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(e.out + orow * D + 32 * x + 8 * y) = q;
-          }
-        } else if (valid) {
-#pragma unroll
-          for (int y = 0; y < 8; ++y)
-            *reinterpret_cast<uint4*>(p.part_acc + prow * D + 32 * x + 4 * y) =
-                make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        if (valid) {
+          if (!whole) p.part_ml[prow] = make_float2(m_ref, bad ? kBadRecord : l);
+          else if (e.lse) e.lse[orow] = none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
         }
       }
-      if (valid) {
-        if (!whole) p.part_ml[prow] = make_float2(m_ref, bad ? kBadRecord : l);
-        else if (e.lse) e.lse[orow] = none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
-      }
+      if (!ok && lane == 0) give_up(c.err, abort);
     }
-    if (!ok && lane == 0) give_up(c.err, abort);
-  }
   }
   tc05::fence_before_sync();
   __syncthreads();
@@ -1304,7 +1295,7 @@ extend_join_kernel(const ExtTcParams p) {
   for (int i = 0; i < s.n; ++i) {
     const float2 ml = p.part_ml[at(i)];
     bad |= ml.y < 0.f;
-    if (ml.y > 0.f) M = fmaxf(M, ml.x);
+    if (ml.y != 0.f) M = fmaxf(M, ml.x);
   }
 #pragma unroll
   for (int y = 0; y < C; ++y) acc[y] = 0.f;
@@ -1315,7 +1306,7 @@ extend_join_kernel(const ExtTcParams p) {
     float4 v[C / 4];
 #pragma unroll
     for (int y = 0; y < C / 4; ++y) v[y] = src[y];
-    if (!(ml.y > 0.f)) continue;                       // (a record without keys holds no sums)
+    if (ml.y == 0.f) continue;                       // (a record without keys holds no sums)
     const float w = exp2f(ml.x - M);
     L = fmaf(w, ml.y, L);
 #pragma unroll
@@ -1327,7 +1318,7 @@ extend_join_kernel(const ExtTcParams p) {
     }
   }
   const size_t o = (size_t)(q0 + tok) * e.c.Hq + s.h * e.G + r % e.G;
-  const bool none = bad || !(L > 0.f);
+  const bool none = bad || L == 0.f;
   const float inv = none ? 0.f : (p.scale_ptr ? __ldg(p.scale_ptr) : 1.f) / L;
 #pragma unroll
   for (int y = 0; y < C; y += 8) {

@@ -331,3 +331,78 @@ def test_one_token_agrees_with_the_decode(ekv_lib, torch_cuda):
     out2, lse2 = run_extend(ekv_lib, ctx, d, d.q, cu, 1)
     assert ctx.error() == (0, 0)
     check(case, cu_of([1] * 4), case.q, out2, lse2)
+
+
+@pytest.mark.parametrize("most", [1, 30])
+def test_batches_of_more_sequences_than_threads(ekv_lib, torch_cuda, most):
+    """The plan reads sequences in passes of one per thread; empty ones among them."""
+    rng = np.random.default_rng(30 + most)
+    lens = rng.integers(1, 200, 1300)
+    new = [int(min(n, rng.integers(0, most + 1))) for n in lens]
+    run_and_check(ekv_lib, torch_cuda, lens, new, 4, 2, 64, "e4m3", 0, seed=31, max_q=most,
+                  rows=set(rng.integers(0, sum(new), 300).tolist()) | {0, sum(new) - 1})
+
+
+@pytest.mark.parametrize("length,n", [(300, 1), (300, 50), (9000, 2), (9000, 40)])
+def test_nan_goes_to_the_queries_that_meet_it(ekv_lib, torch_cuda, length, n):
+    """A NaN query or visible NaN key gives NaN, as the formula does; the other queries keep their bits."""
+    torch = torch_cuda
+    case = make_case([length], 8, 2, 128, "e4m3", 0, 32)
+    d, cu = to_device(case), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    q = torch.randn((n, 8, 128), dtype=torch.float16, device="cuda")
+    ctx = ekv_lib.Context(8, 2, 128, 1)
+    out, lse = run_extend(ekv_lib, ctx, d, q, cu, n)
+    q2 = q.clone()
+    q2[n // 2, 5, 77] = float("nan")
+    out2, lse2 = run_extend(ekv_lib, ctx, d, q2, cu, n)
+    hit = torch.zeros((n, 8), dtype=torch.bool, device="cuda")
+    hit[n // 2, 5] = True
+    assert torch.isnan(out2[hit]).all() and torch.isnan(lse2[hit]).all()
+    assert torch.equal(out2[~hit], out[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+    t = length - 1 - n // 3                              # a key that the last third of the queries see
+    d.k_pages[int(case.block_table[0, t // 16]), t % 16, 1, 3] = float("nan")
+    out3, lse3 = run_extend(ekv_lib, ctx, d, q, cu, n)
+    hit[:] = False
+    hit[n - 1 - n // 3:, 4:] = True
+    assert torch.isnan(out3[hit]).all() and torch.isnan(lse3[hit]).all()
+    assert torch.equal(out3[~hit], out[~hit]) and torch.equal(lse3[~hit], lse[~hit])
+    assert ctx.error() == (0, 0)
+
+
+@pytest.mark.parametrize("n", [1, 70])
+def test_stale_table_entries_outside_the_window(ekv_lib, torch_cuda, n):
+    torch = torch_cuda
+    case = make_case([900, 33], 8, 2, 64, "all", 1, 33)
+    cu = cu_of([n, min(n, 33)])
+    q = np.random.default_rng(34).standard_normal((int(cu[-1]), 8, 64)).astype(np.float16)
+    d = to_device(case)
+    seen = 900 - n - 100 + 1                             # first key that a query of sequence 0 sees
+    d.block_table[0, :seen // 16] = torch.tensor(2 ** 31 - 1, dtype=torch.int32)
+    d.block_table[1, 3:] = -5
+    ctx = ekv_lib.Context(8, 2, 64, 2)
+    out, lse = run_extend(ekv_lib, ctx, d, torch.from_numpy(q).cuda(), torch.from_numpy(cu).cuda(), n, window=100)
+    assert ctx.error() == (0, 0)
+    check(case, cu, q, out, lse, window=100)
+
+
+def test_two_contexts_at_once_and_again(ekv_lib, torch_cuda):
+    """Calls of two contexts that overlap on two streams, repeated: each keeps its bits."""
+    torch = torch_cuda
+    runs = []
+    for i, (lens, new) in enumerate((([5000, 300, 2000], [1, 2, 3]), ([3000, 700], [200, 90]))):
+        case = make_case(lens, 8, 2, 128, "all", 1, 40 + i)
+        cu = cu_of(new)
+        q = torch.randn((int(cu[-1]), 8, 128), dtype=torch.float16, device="cuda")
+        ctx, d, dcu = ekv_lib.Context(8, 2, 128, 3), to_device(case), torch.from_numpy(cu).cuda()
+        runs.append((ctx, d, q, dcu, max(new), torch.cuda.Stream(), run_extend(ekv_lib, ctx, d, q, dcu, max(new))))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for ctx, d, q, dcu, mq, s, _ref in runs:
+            with torch.cuda.stream(s):
+                got.append((run_extend(ekv_lib, ctx, d, q, dcu, mq, stream=s.cuda_stream), _ref))
+    torch.cuda.synchronize()
+    for (out, lse), ref in got:
+        assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    for r in runs:
+        assert r[0].error() == (0, 0)
