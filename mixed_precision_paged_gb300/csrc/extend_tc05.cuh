@@ -84,6 +84,7 @@ struct XT {
   // Block descriptions. One is written once the K stage NK + kMetaAhead + 1 blocks back is free, so
   // once that block's S is issued, which is behind the product of the block before (ALT: two before).
   static constexpr int NM = D == 128 ? 8 : 12;
+  static constexpr int NS = 8;                         // segment descriptions (see the producer)
   static_assert(NM >= NK + kMetaAhead + (ALT ? 3 : 2), "a description is read until its block's weights are handed over");
 };
 
@@ -99,6 +100,15 @@ struct BlockMeta {
   uint8_t z0, z1;                           // keys of the block that some row of the item sees: [z0, z1)
 };
 
+struct SegMeta {                            // a segment: the blocks of one item in one CTA's range
+  int n;                                    // blocks; 0: no segment follows
+  int nt[2];                                // of them, those that each tile takes part in, from the first on
+  int ja;                                   // first block, of the sequence
+  int q0, ntok, t0;                         // the sequence: first row of q, new tokens, position of the first
+  int i;                                    // the item
+  int slot;                                 // of the partial rows; -1: the whole item
+};
+
 template <int D, int VM, bool ALT>
 struct XTBars {
   using C = XT<D, VM, ALT>;
@@ -108,13 +118,15 @@ struct XTBars {
   uint64_t v_full[C::NV], v_empty[C::NV];
   uint64_t v_dir[C::NV];                    // FP16 pages of a stage whose edge rows are zeroed after they land
   uint64_t meta_full[C::NM];
+  uint64_t seg_full[C::NS], seg_empty[C::NS];
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t mma_final;
   uint64_t x_full[2];                       // ALT: a stream's (m, l) of the segment posted
   float2 xch[2][ALT ? kAltRows : 1];
   BlockMeta meta[C::NM];
-  long long red[kT5Threads / 32], rest[kT5Threads / 32];
-  int st_b, st_i, st_j;                     // where this CTA's range begins
+  SegMeta seg[C::NS];
+  long long red[kT5Threads / 32];
+  int st_b, st_off;                         // where this CTA's range begins: sequence, blocks into it
   uint32_t tmem_base;
   int abort;
 };
@@ -284,7 +296,7 @@ __device__ __forceinline__ Items items_of(const ExtendParams& e, const Seq& s) {
   return it;
 }
 
-// A walk over this CTA's segments; every role makes the same one.
+// The producer's walk over the CTA's segments.
 struct Walk {
   int b, i, j;              // next: sequence, item, block (j may lie kItemCost before the item's first)
   int budget;               // blocks left in the CTA's range
@@ -352,36 +364,6 @@ __device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segmen
   return false;
 }
 
-// A walk in one register, a field per lane: for the softmax warps, whose registers hold their rows.
-__device__ __forceinline__ int pack_walk(const Walk& w) {
-  const int lane = threadIdx.x & 31;
-  int v = w.b;
-  v = lane == 1 ? w.i : v;
-  v = lane == 2 ? w.j : v;
-  v = lane == 3 ? w.budget : v;
-  v = lane == 4 ? w.index : v;
-  v = lane == 5 ? w.q0 : v;
-  v = lane == 6 ? w.it.n : v;
-  v = lane == 7 ? w.it.t0 : v;
-  v = lane == 8 ? w.it.np : v;
-  return lane == 9 ? w.it.step : v;
-}
-__device__ __forceinline__ Walk unpack_walk(const ExtendParams& e, int v) {
-  Walk w;
-  w.b = __shfl_sync(0xffffffffu, v, 0);
-  w.i = __shfl_sync(0xffffffffu, v, 1);
-  w.j = __shfl_sync(0xffffffffu, v, 2);
-  w.budget = __shfl_sync(0xffffffffu, v, 3);
-  w.index = __shfl_sync(0xffffffffu, v, 4);
-  w.q0 = __shfl_sync(0xffffffffu, v, 5);
-  w.it.n = __shfl_sync(0xffffffffu, v, 6);
-  w.it.t0 = __shfl_sync(0xffffffffu, v, 7);
-  w.it.np = __shfl_sync(0xffffffffu, v, 8);
-  w.it.step = __shfl_sync(0xffffffffu, v, 9);
-  w.it.window = e.window;
-  return w;
-}
-
 }  // namespace xt
 
 // -------------------------------------------------------------------- the kernel
@@ -438,9 +420,9 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       mbar_init(&bars->v_dir[s], 1);
     }
     for (int s = 0; s < NM; ++s) mbar_init(&bars->meta_full[s], 1);
+    for (int s = 0; s < C::NS; ++s) mbar_init(&bars->seg_full[s], 1), mbar_init(&bars->seg_empty[s], 1 + 2 * nw);
     mbar_init(&bars->mma_final, 1);
     bars->abort = 0;
-    bars->st_b = -1;
     fence_barrier_init();
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tk);
@@ -449,8 +431,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   }
   if (warp == 2) tc05::tmem_alloc(&bars->tmem_base, 512);
 
-  // ---- plan: the blocks of all items, in equal ranges (see the top). The costs of the first kT5Threads
-  // sequences are kept: a batch no larger is read once and planned with one barrier.
+  // ---- plan: the blocks of all items, in equal ranges (see the top), kT5Threads sequences at a time
   const int tid = threadIdx.x;
   bool fails = false;
   auto cost = [&](int b) -> long long {
@@ -471,82 +452,62 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     }
     return x;
   };
-  long long mine = cost(tid), incl = warp_incl(mine), total = 0;
-  for (int b = tid + kT5Threads; b < c.batch; b += kT5Threads) total += cost(b);
-  if (c.batch > kT5Threads) total = __shfl_sync(0xffffffffu, warp_incl(total), 31);
-  if (lane == 31) {
-    bars->red[warp] = incl;
-    bars->rest[warp] = total;
-  }
-  tc05::fence_before_sync();
-  const int any_fails = __syncthreads_or(fails);
-  tc05::fence_after_sync();
-  total = 0;
-  for (int w = 0; w < kT5Threads / 32; ++w) total += bars->red[w] + bars->rest[w];
-  if (any_fails && blockIdx.x == 0) {                  // reported and zeroed once
-    for (int b = 0; b < c.batch; ++b) {
-      Seq s;
-      if (!load_seq(e, b, s) || seq_ok(e, s)) continue;
-      if (tid == 0) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SEQ_LEN, b);
-      zero_rows(e, s);
-    }
-  }
   // CTA x works on KV head x mod H_kv and range x / H_kv: the heads of a page are read at about the
   // same time
-  const int ranges = (int)gridDim.x / c.Hkv, h = (int)blockIdx.x % c.Hkv;
-  long long per = (total + ranges - 1) / ranges;
-  if (per < 2) per = 2;
-  const long long start = (int)blockIdx.x / c.Hkv < ranges ? per * ((int)blockIdx.x / c.Hkv) : total;
-  const int budget0 = (int)max(0ll, min(per, total - start));
-  // the sequence, item and block of position `start`
-  long long carry = 0;
-  for (int b0 = 0; budget0 > 0; b0 += kT5Threads) {
-    if (b0 > 0) {
+  const int ranges = (int)gridDim.x / c.Hkv, h = (int)blockIdx.x % c.Hkv, chunks = (c.batch + kT5Threads - 1) / kT5Threads;
+  long long mine = 0, incl = 0, total = 0, carry = 0, per = 0, start = 0;
+  int budget0 = 0;
+  // the total, and then the sequence of position `start`; one chunk's costs serve both
+#pragma unroll 1
+  for (int x = 0; x < 2 * chunks; ++x) {
+    const int b0 = (x < chunks ? x : x - chunks) * kT5Threads;
+    if (x == 0 || chunks > 1) {
       mine = cost(b0 + tid);
       incl = warp_incl(mine);
-      __syncthreads();                                 // the last use of red is behind
+      if (x > 0) __syncthreads();                        // the last use of red is behind
       if (lane == 31) bars->red[warp] = incl;
-      __syncthreads();
+      tc05::fence_before_sync();
+      const int any_fails = __syncthreads_or(fails && x < chunks);
+      tc05::fence_after_sync();
+      if (any_fails && blockIdx.x == 0) {                // reported and zeroed once
+        for (int b = b0; b < min(b0 + kT5Threads, c.batch); ++b) {
+          Seq s;
+          if (!load_seq(e, b, s) || seq_ok(e, s)) continue;
+          if (tid == 0) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SEQ_LEN, b);
+          zero_rows(e, s);
+        }
+        fails = false;
+      }
     }
     long long before = carry;
+#pragma unroll 1
     for (int w = 0; w < kT5Threads / 32; ++w) {
       const long long v = bars->red[w];
       if (w < warp) before += v;
       carry += v;
     }
+    if (x < chunks) {
+      if (x == chunks - 1) {
+        total = carry;
+        carry = 0;
+        per = (total + ranges - 1) / ranges;
+        if (per < 2) per = 2;
+        start = (int)blockIdx.x / c.Hkv < ranges ? per * ((int)blockIdx.x / c.Hkv) : total;
+        budget0 = (int)max(0ll, min(per, total - start));
+        if (budget0 == 0) break;
+      }
+      continue;
+    }
     const long long at = start - (before + incl - mine);
     if (mine > 0 && at >= 0 && at < mine) {
-      Seq s;
-      load_seq(e, b0 + tid, s);
-      const Items it = items_of<ALT>(e, s);
-      const int off = (int)at;
-      int lo = 0, hi = it.np - 1;                      // the last item that begins at or before `off`
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (it.before<ALT>(mid) <= off) lo = mid;
-        else hi = mid - 1;
-      }
       bars->st_b = b0 + tid;
-      bars->st_i = lo;
-      bars->st_j = it.jlo(lo) - kItemCost + off - it.before<ALT>(lo);
+      bars->st_off = (int)at;
     }
-    if (carry > start || b0 + kT5Threads >= c.batch) break;
+    if (carry > start) break;
   }
   __syncthreads();
-  Walk w;
-  w.b = bars->st_b;
-  w.i = bars->st_i;
-  w.j = bars->st_j;
-  w.budget = w.b < 0 ? 0 : budget0;
-  w.index = 0;
-  bool any = false;                                    // a block in the range
-  if (w.budget > 0) {
-    Seq sq;
-    load_seq(e, w.b, sq);
-    w.q0 = sq.q0;
-    w.it = items_of<ALT>(e, sq);
-    any = w.j + w.budget > w.it.jlo(w.i);
-  }
+  // (two units of a range hold a block, as does its last one: a range that is not empty has blocks)
+  const bool any = budget0 > 0;
   const uint32_t tbase = bars->tmem_base;
   const int TT = e.tile_tokens;                        // tokens of a tile
   const int nqb = ALT ? 2 / nw : 2;                    // query buffers: tiles, or (ALT, few rows) segments in turn
@@ -561,8 +522,36 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       // Pages are looked up in batches of four blocks, a page per lane: a batch's ids are fetched two
       // batches ahead and its modes and scales one ahead, across segments. A block's description is
       // posted kMetaAhead blocks before its keys are loaded, for the makers, whose loads take as long.
+      // Its walk is the only one: what the MMA and softmax warps need of a segment is posted in a ring of NS
+      // descriptions (a walk of every role's own cost each item 10,000 cycles of cold code). Up to
+      // four segments may be posted whose keys are not loaded yet, and a description is free once its
+      // readers are through with the segment before: eight always leave the producer its way.
       int u = 0, k = 0;                                  // blocks described, blocks whose keys were loaded
-      uint32_t ql[2] = {0u, 0u}, qseg = 0;
+      uint32_t ql[2] = {0u, 0u}, qseg = 0, nseg = 0;
+      bool ok = true, ended = false;
+      Walk w;
+      w.b = 0;
+      w.index = 0;
+      w.budget = budget0;
+      if (any) {
+        w.b = bars->st_b;
+        Seq sq;
+        load_seq(e, w.b, sq);
+        w.q0 = sq.q0;
+        w.it = items_of<ALT>(e, sq);
+        const int off = bars->st_off;
+        int lo = 0, n = w.it.np, before = 0;             // the item: the last that begins at or before `off`
+        while (n > 1) {                                  // among n from lo on; 32 are looked at together
+          const int step = (n + 31) / 32, at = lo + lane * step;
+          const int x = lane * step < n ? w.it.before<ALT>(at) : INT_MAX;
+          const int last = __popc(__ballot_sync(0xffffffffu, x <= off)) - 1;
+          before = __shfl_sync(0xffffffffu, x, last);
+          n = min(step, n - last * step);
+          lo += last * step;
+        }
+        w.i = lo;
+        w.j = w.it.jlo(lo) - kItemCost + off - before;
+      }
       ExtTcSplit split;
       split.n = 0;
       struct Batch {
@@ -575,7 +564,26 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         x.tiles = 0;
         x.nb = 0;
         if (sg.ja >= sg.jb) {
-          if (!walk_next<ALT>(e, w, sg)) return;
+          if (ended) return;
+          ended = !walk_next<ALT>(e, w, sg);
+          if (nseg >= C::NS) ok = wait_warp(&bars->seg_empty[nseg % C::NS], (nseg / C::NS - 1u) & 1u, abort);
+          if (!ok) return;
+          if (lane == 0) {
+            SegMeta& sm = bars->seg[nseg % C::NS];
+            sm.n = ended ? 0 : sg.jb - sg.ja;
+            sm.nt[0] = sg.nt[0];
+            sm.nt[1] = sg.nt[1];
+            sm.ja = sg.ja;
+            sm.q0 = sg.q0;
+            sm.ntok = sg.n;
+            sm.t0 = sg.t0;
+            sm.i = sg.i;
+            sm.slot = sg.whole ? -1 : sg.slot;
+            mbar_arrive(&bars->seg_full[nseg % C::NS]);
+          }
+          __syncwarp();
+          ++nseg;
+          if (ended) return;
           x.qtok = sg.q0 + C::NQ * sg.i * TT;
           x.tiles = (sg.nt[0] > 0 ? 1 : 0) | (sg.nt[1] > 0 ? 2 : 0);
           if (sg.ja == sg.jlo && sg.jb < sg.jhi) {       // the item goes on in later CTAs
@@ -609,7 +617,6 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if ((VM == kXE4M3 || VM == kXMixed) && c.v_scales)
           vs = __ldg(c.v_scales + (c.scale_mode == EKV_SCALE_PER_TENSOR ? 0 : (size_t)id * c.Hkv + h));
       };
-      bool ok = true;
       // the queries (first block of a segment) and keys of block k
       auto load_k = [&]() {
         const BlockMeta& mt = bars->meta[k % NM];
@@ -641,13 +648,21 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         ++k;
       };
       Batch b0, b1, b2;
-      next_batch(b0);
-      next_batch(b1);
-      next_batch(b2);
-      int id0 = ids(b0), id1 = ids(b1), mode0, mode1;
-      float vs0, vs1;
-      lookup(b0, id0, mode0, vs0);
-      while (ok && b0.nb > 0) {
+      int id0 = 0, id1 = 0, id2 = 0, mode0 = 0, mode1 = 0;
+      float vs0 = 0.f, vs1 = 0.f;
+      b1.nb = b2.nb = 0;
+#pragma unroll 1
+      for (int round = 0; ok; ++round) {
+        b0 = b1;
+        id0 = id1;
+        mode0 = mode1;
+        vs0 = vs1;
+        b1 = b2;
+        id1 = id2;
+        next_batch(b2);                                  // two batches ahead
+        id2 = ids(b2);
+        lookup(b1, id1, mode1, vs1);
+        if (round < 2) continue;
         // this batch's pages
         int flags = kSkip, detail = EKV_DETAIL_NONE;
         float vs = 1.f;
@@ -665,41 +680,38 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         const float lsc = log2f(vs), ivs = 1.f / vs;
         const uint32_t bad = __ballot_sync(0xffffffffu, detail != EKV_DETAIL_NONE);
-        lookup(b1, id1, mode1, vs1);                     // the next batch's, and the ids after
-        const int id2 = ids(b2);
-        for (int i = 0; i < b0.nb && ok; ++i, ++u) {
-          BlockMeta& mt = bars->meta[u % NM];
-          const int pg = lane & (kTPages - 1);
-          if (lane / kTPages == i) {
-            mt.page[pg] = id0;
-            mt.flags[pg] = (uint8_t)flags;
-            mt.lsc[pg] = lsc;
-            mt.ivs[pg] = ivs;
-            if (pg == 0) {
-              mt.bad = (int)((bad >> (i * kTPages)) & 0xffu);
-              mt.qtok = i == 0 ? b0.qtok : -1;
-              mt.tiles = (uint8_t)b0.tiles;
-              mt.last = i + 1 == b0.nb && b1.nb == 0;
-              mt.z0 = (uint8_t)max(0, b0.lo - (b0.j0 + i) * kTKeys);
-              mt.z1 = (uint8_t)min(kTKeys, b0.hi - (b0.j0 + i) * kTKeys);
+        const bool end = b0.nb == 0;                     // only the keys of the last blocks are left
+#pragma unroll 1
+        for (int i = 0; i < (end ? kMetaAhead : b0.nb) && ok; ++i) {
+          if (!end) {
+            BlockMeta& mt = bars->meta[u % NM];
+            const int pg = lane & (kTPages - 1);
+            if (lane / kTPages == i) {
+              mt.page[pg] = id0;
+              mt.flags[pg] = (uint8_t)flags;
+              mt.lsc[pg] = lsc;
+              mt.ivs[pg] = ivs;
+              if (pg == 0) {
+                mt.bad = (int)((bad >> (i * kTPages)) & 0xffu);
+                mt.qtok = i == 0 ? b0.qtok : -1;
+                mt.tiles = (uint8_t)b0.tiles;
+                mt.last = i + 1 == b0.nb && b1.nb == 0;
+                mt.z0 = (uint8_t)max(0, b0.lo - (b0.j0 + i) * kTKeys);
+                mt.z1 = (uint8_t)min(kTKeys, b0.hi - (b0.j0 + i) * kTKeys);
+              }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->meta_full[u % NM]);
+            ++u;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->meta_full[u % NM]);
-          if (u >= kMetaAhead) load_k();
+          if (end ? k < u : u > kMetaAhead) load_k();
         }
-        b0 = b1;
-        id0 = id1;
-        mode0 = mode1;
-        vs0 = vs1;
-        b1 = b2;
-        id1 = id2;
-        next_batch(b2);
+        if (end) break;
       }
-      while (ok && k < u) load_k();
       if (!ok && lane == 0) give_up(c.err, abort);
       if (lane == 0) p.split[blockIdx.x] = split;
       // the copies still in flight land before the CTA can exit
+#pragma unroll 1
       for (int v = max(0, k - NK); v < k; ++v) drain(&bars->k_full[v % NK], (v / NK) & 1);
       for (int t = 0; t < 2; ++t)
         if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
@@ -766,9 +778,14 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         __syncwarp();
       };
       bool ok = true;
-      Segment sg;
-      while (ok && walk_next<ALT>(e, w, sg)) {
-        const int n = sg.jb - sg.ja;
+      for (uint32_t seg = 0; ok; ++seg) {
+        ok = wait_warp(&bars->seg_full[seg % C::NS], (seg / C::NS) & 1u, abort);
+        if (!ok) break;
+        const SegMeta sg = bars->seg[seg % C::NS];
+        const int n = sg.n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->seg_empty[seg % C::NS]);
+        if (n == 0) break;
         if (ALT) {
           // block j belongs to stream j mod 2: O_t += P_t V_j, then S_t of block j + 2 over P_t
           auto issue_next = [&](int j) {                 // S of block j
@@ -829,9 +846,9 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           bool k_ready = false;
           for (int t = 0; t < 2 && ok; ++t) {
             if (j >= sg.nt[t]) continue;
-            ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
+            if (j == 0 && oc[t] > 0) ok = wait_warp(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
+            if (ok) ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
             ++pc[t];
-            if (ok && j == 0 && oc[t] > 0) ok = wait_warp(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
             if (!ok) break;
             tc05::fence_after_sync();
             const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
@@ -852,12 +869,13 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             }
           }
           if (!ok) break;
-          commit_one(&bars->v_empty[vst]);
-          if (++vst == NV) vst = 0, vph ^= 1u;
-          if (j + 1 < n) {
-            commit_one(&bars->k_empty[ks]);
-            if (++ks == NK) ks = 0, kph ^= 1u;
+          if (tc05::elect_one()) {
+            tc05::commit(&bars->v_empty[vst]);
+            if (j + 1 < n) tc05::commit(&bars->k_empty[ks]);
           }
+          __syncwarp();
+          if (++vst == NV) vst = 0, vph ^= 1u;
+          if (j + 1 < n && ++ks == NK) ks = 0, kph ^= 1u;
         }
         for (int t = 0; t < 2; ++t)
           if (sg.nt[t] > 0) ++oc[t];
@@ -986,7 +1004,8 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       }
       if (!ok && run && lane == 0) give_up(c.err, abort);
       if (kRaw)
-        for (int v = max(0, issued - NR); v < issued; ++v) drain(&bars->raw_full[v % NR][vi], (uint32_t)(v / NR) & 1u);
+  #pragma unroll 1
+      for (int v = max(0, issued - NR); v < issued; ++v) drain(&bars->raw_full[v % NR][vi], (uint32_t)(v / NR) & 1u);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
@@ -1001,37 +1020,41 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       int u = 0;
       bool ok = true;
       const int tok_t = r / e.G;                         // this thread's token within the tile
-      int walk = pack_walk(w);
       while (ok) {
         // what the rows need of the segment; orow < 0: a row past the sequence
         int nmine, u0 = u, ja, pos, lo, all_lo, all_hi, slot;
         long long orow;
+        const uint32_t rs = seg % C::NS;
+        ok = wait_warp(&bars->seg_full[rs], (seg / C::NS) & 1u, abort);
+        if (!ok) break;
         {
-          Segment sg;
-          Walk v = unpack_walk(e, walk);
-          if (!walk_next<ALT>(e, v, sg)) break;
-          walk = pack_walk(v);
+          const SegMeta& sg = bars->seg[rs];
+          const int n = sg.n;
           nmine = sg.nt[t];
-          u += sg.jb - sg.ja;
           ja = sg.ja;
           const int first = (ALT ? sg.i : 2 * sg.i + t) * TT;   // the tile's first token
           const int tok = first + tok_t;
           pos = sg.t0 + tok;
           lo = max(pos - e.window, -1);                  // the row sees keys lo + 1 .. pos
           // keys that every valid row sees: from the last row's window start to the first row's own
-          all_lo = sg.t0 + min(first + TT, sg.n) - 1 - e.window;
+          all_lo = sg.t0 + min(first + TT, sg.ntok) - 1 - e.window;
           all_hi = sg.t0 + first;
-          slot = sg.whole ? -1 : sg.slot;
-          orow = tok_t < TT && tok < sg.n ? (long long)(sg.q0 + tok) * c.Hq + h * e.G + r % e.G : -1;
+          slot = sg.slot;
+          orow = tok_t < TT && tok < sg.ntok ? (long long)(sg.q0 + tok) * c.Hq + h * e.G + r % e.G : -1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->seg_empty[rs]);
+          if (n == 0) break;
+          u += n;
+          ++seg;
         }
         const bool valid = orow >= 0, whole = slot < 0;
         float m_ref = -INFINITY, l = 0.f;
         bool bad = false;
         for (int jj = 0; jj < nmine; ++jj) {
           const int blk = ALT ? 2 * jj + t : jj;         // block of the segment
-          ok = wait_warp(&bars->s_full[t], sc & 1u, abort);
+          ok = wait_warp(&bars->meta_full[(u0 + blk) % NM], (uint32_t)((u0 + blk) / NM) & 1u, abort);
+          if (ok) ok = wait_warp(&bars->s_full[t], sc & 1u, abort);
           ++sc;
-          if (ok) ok = wait_warp(&bars->meta_full[(u0 + blk) % NM], (uint32_t)((u0 + blk) / NM) & 1u, abort);
           if (!ok) break;
           tc05::fence_after_sync();
           const BlockMeta& mt = bars->meta[(u0 + blk) % NM];
@@ -1153,15 +1176,14 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             if (!ok) break;
           }
           // the other stream has read what the last segment posted (it arrived here afterwards)
-          if (seg > 0) ok = wait_warp(&bars->o_free[0], (seg - 1u) & 1u, abort);
+          if (seg > 1) ok = wait_warp(&bars->o_free[0], seg & 1u, abort);
           if (!ok) break;
           float2 (&xch)[2][ALT ? kAltRows : 1] = bars->xch;
           xch[t][r] = make_float2(m_ref, bad ? kBadRecord : l);
           tc05::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->x_full[t]);
-          ok = wait_warp(&bars->x_full[1 - t], seg & 1u, abort);
-          ++seg;
+          ok = wait_warp(&bars->x_full[1 - t], (seg - 1u) & 1u, abort);
           if (!ok) break;
           tc05::fence_after_sync();
           const float2 other = xch[1 - t][r];
@@ -1176,7 +1198,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           }
           const bool none = bad || L == 0.f;             // (a NaN goes on to the output)
           const float inv = none ? 0.f : osc / L;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < D / 64; ++x) {
             const int col = t * (D / 2) + 32 * x;
             uint32_t o0[32], o1[32];
@@ -1227,7 +1249,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tc05::fence_after_sync();
         const bool none = bad || l == 0.f;               // (a NaN goes on to the output)
         const float inv = none ? 0.f : osc / l;
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < D / 32; ++x) {
           uint32_t o[32];
           tc05::ld32(t_o + 32 * x, o);
