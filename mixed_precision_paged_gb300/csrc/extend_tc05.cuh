@@ -81,6 +81,8 @@ struct XT {
   // maker warps: warps 2 and 13-15, warp 3 where no FP16 pages are to be loaded, and warp 12 where
   // its scheduler does not have all of the softmax (ALT)
   static constexpr int MK = VM == kXFP16 || VM == kXMixed ? 4 : ALT ? 5 : 6;
+  // five or four makers leave warp 12 to load the raw pages for all of them
+  static constexpr bool kLoader = VM != kXFP16 && MK < 6;
   // Block descriptions. One is written once the K stage NK + kMetaAhead + 1 blocks back is free, so
   // once that block's S is issued, which is behind the product of the block before (ALT: two before).
   static constexpr int NM = D == 128 ? 8 : 12;
@@ -114,7 +116,7 @@ struct XTBars {
   using C = XT<D, VM, ALT>;
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[C::NK], k_empty[C::NK];
-  uint64_t raw_full[C::NR][C::MK];
+  uint64_t raw_full[C::NR][C::MK], raw_empty[C::NR];   // (with a loader warp: raw_full[..][0])
   uint64_t v_full[C::NV], v_empty[C::NV];
   uint64_t v_dir[C::NV];                    // FP16 pages of a stage whose edge rows are zeroed after they land
   uint64_t meta_full[C::NM];
@@ -300,7 +302,7 @@ __device__ __forceinline__ Items items_of(const ExtendParams& e, const Seq& s) {
 struct Walk {
   int b, i, j;              // next: sequence, item, block (j may lie kItemCost before the item's first)
   int budget;               // blocks left in the CTA's range
-  int index;                // segments so far
+  int index, u;             // segments and blocks so far
   int q0;                   // the sequence's first row of q
   Items it;
 };
@@ -333,8 +335,8 @@ __device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segmen
     sg.jb = jb;
     sg.whole = sg.ja == sg.jlo && jb == sg.jhi;
     if (ALT) {                                       // one tile, its blocks in turn
-      sg.nt[0] = (jb - sg.ja + 1) / 2;
-      sg.nt[1] = (jb - sg.ja) / 2;
+      sg.nt[0] = (jb - sg.ja + 1 - (w.u & 1)) / 2;
+      sg.nt[1] = (jb - sg.ja + (w.u & 1)) / 2;
     } else {                                         // tile 0 ends with its own last token's block
       const int half = w.it.step / 2;
       const int e0 = (w.it.t0 + min(w.i * w.it.step + half, w.it.n) + kTKeys - 1) / kTKeys;
@@ -358,6 +360,7 @@ __device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segmen
     if (sg.ja < sg.jb) {
       sg.slot = 2 * (int)blockIdx.x + (w.index == 0 ? 0 : 1);
       ++w.index;
+      w.u += sg.jb - sg.ja;
       return true;
     }
   }
@@ -412,8 +415,10 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       mbar_init(&bars->x_full[t], nw);
     }
     for (int s = 0; s < NK; ++s) mbar_init(&bars->k_full[s], 1), mbar_init(&bars->k_empty[s], 1);
-    for (int s = 0; s < NR; ++s)
-      for (int x = 0; x < C::MK; ++x) mbar_init(&bars->raw_full[s][x], x + C::MK < kTPages ? 2 : 1);
+    for (int s = 0; s < NR; ++s) {
+      for (int x = 0; x < C::MK; ++x) mbar_init(&bars->raw_full[s][x], !C::kLoader && x + C::MK < kTPages ? 2 : 1);
+      mbar_init(&bars->raw_empty[s], C::MK);
+    }
     for (int s = 0; s < NV; ++s) {
       mbar_init(&bars->v_full[s], C::MK + (kDirect ? 1 : 0));
       mbar_init(&bars->v_empty[s], 1);
@@ -479,18 +484,14 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         fails = false;
       }
     }
-    long long before = carry;
-#pragma unroll 1
-    for (int w = 0; w < kT5Threads / 32; ++w) {
-      const long long v = bars->red[w];
-      if (w < warp) before += v;
-      carry += v;
-    }
+    const long long sums = warp_incl(lane < kT5Threads / 32 ? bars->red[lane] : 0);
+    const long long before = carry + (warp > 0 ? __shfl_sync(0xffffffffu, sums, warp - 1) : 0);
+    carry += __shfl_sync(0xffffffffu, sums, 31);
     if (x < chunks) {
       if (x == chunks - 1) {
         total = carry;
         carry = 0;
-        per = (total + ranges - 1) / ranges;
+        per = total <= INT_MAX ? ((uint32_t)total + ranges - 1u) / (uint32_t)ranges : (total + ranges - 1) / ranges;
         if (per < 2) per = 2;
         start = (int)blockIdx.x / c.Hkv < ranges ? per * ((int)blockIdx.x / c.Hkv) : total;
         budget0 = (int)max(0ll, min(per, total - start));
@@ -531,7 +532,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       bool ok = true, ended = false;
       Walk w;
       w.b = 0;
-      w.index = 0;
+      w.index = w.u = 0;
       w.budget = budget0;
       if (any) {
         w.b = bars->st_b;
@@ -778,7 +779,74 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         __syncwarp();
       };
       bool ok = true;
-      for (uint32_t seg = 0; ok; ++seg) {
+      if (ALT) {
+        // Block g of the range belongs to stream g mod 2: O_t += P_t V, and then S_t of block g + 2 over P_t, of the
+        // next segment too. js of ns: the segment of S; jp of np: that of the products; nq: lengths between.
+        int gs = 0, gp = 0, js = 0, ns = 0, jp = 0, np = 0, nq[3] = {0, 0, 0};
+        uint32_t segs = 0, segp = 0;
+        bool more = true;
+        while (ok) {
+          while (more && gs < gp + 2) {
+            if (js == ns) {
+              ok = wait_warp(&bars->seg_full[segs % C::NS], (segs / C::NS) & 1u, abort);
+              if (!ok) break;
+              ns = bars->seg[segs % C::NS].n;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->seg_empty[segs % C::NS]);
+              ++segs;
+              js = 0;
+              more = ns > 0;
+              if (!more) break;
+              if (nq[0] == 0) nq[0] = ns;
+              else if (nq[1] == 0) nq[1] = ns;
+              else nq[2] = ns;
+              ok = wait_warp(&bars->q_full[qbuf], qc[qbuf] & 1u, abort);
+              ++qc[qbuf];
+            }
+            if (ok) ok = wait_warp(&bars->k_full[ks], kph, abort);
+            if (!ok) break;
+            tc05::fence_after_sync();
+            issue_s(gs & 1);
+            commit_one(&bars->k_empty[ks]);
+            if (++ks == NK) ks = 0, kph ^= 1u;
+            ++gs;
+            if (++js == ns) {
+              commit_one(&bars->q_empty[qbuf]);
+              if (++qbuf == nqb) qbuf = 0;
+            }
+          }
+          if (!ok || gp == gs) break;
+          if (jp == np) {
+            np = nq[0];
+            nq[0] = nq[1];
+            nq[1] = nq[2];
+            nq[2] = 0;
+            jp = 0;
+            // the last segment's O is read out by both streams together
+            if (segp > 0) ok = wait_warp(&bars->o_free[0], (segp - 1u) & 1u, abort);
+            ++segp;
+          }
+          const int t = gp & 1;
+          if (ok) ok = wait_warp(&bars->v_full[vst], vph, abort);
+          if (ok) ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
+          ++pc[t];
+          if (!ok) break;
+          tc05::fence_after_sync();
+          const uint32_t va = v_lo + vst * (C::IB >> 4), pa = tbase + t * 256, od = tbase + t * 256 + 128;
+          if (tc05::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kTKeys / 16; ++k)
+              tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2 * C::GB >> 4), HIB), idO, jp > 1 || k > 0);
+            if (jp + 2 >= np) tc05::commit(&bars->pv_done[t]);
+            tc05::commit(&bars->v_empty[vst]);
+          }
+          __syncwarp();
+          if (++vst == NV) vst = 0, vph ^= 1u;
+          ++jp;
+          ++gp;
+        }
+      }
+      for (uint32_t seg = 0; !ALT && ok; ++seg) {
         ok = wait_warp(&bars->seg_full[seg % C::NS], (seg / C::NS) & 1u, abort);
         if (!ok) break;
         const SegMeta sg = bars->seg[seg % C::NS];
@@ -786,45 +854,6 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->seg_empty[seg % C::NS]);
         if (n == 0) break;
-        if (ALT) {
-          // block j belongs to stream j mod 2: O_t += P_t V_j, then S_t of block j + 2 over P_t
-          auto issue_next = [&](int j) {                 // S of block j
-            ok = wait_warp(&bars->k_full[ks], kph, abort);
-            if (!ok) return;
-            tc05::fence_after_sync();
-            issue_s(j & 1);
-            commit_one(&bars->k_empty[ks]);
-            if (++ks == NK) ks = 0, kph ^= 1u;
-            if (j == n - 1) commit_one(&bars->q_empty[qbuf]);
-          };
-          ok = wait_warp(&bars->q_full[qbuf], qc[qbuf] & 1u, abort);
-          ++qc[qbuf];
-          for (int j = 0; j < min(n, 2) && ok; ++j) issue_next(j);
-          for (int j = 0; ok && j < n; ++j) {
-            const int t = j & 1;
-            ok = wait_warp(&bars->v_full[vst], vph, abort);
-            if (ok) ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
-            ++pc[t];
-            // the last segment's O is read out by both streams together
-            if (ok && j == 0 && oc[0] > 0) ok = wait_warp(&bars->o_free[0], (oc[0] - 1u) & 1u, abort);
-            if (!ok) break;
-            tc05::fence_after_sync();
-            const uint32_t va = v_lo + vst * (C::IB >> 4), pa = tbase + t * 256, od = tbase + t * 256 + 128;
-            if (tc05::elect_one()) {
-#pragma unroll
-              for (int k = 0; k < kTKeys / 16; ++k)
-                tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2 * C::GB >> 4), HIB), idO, j > 1 || k > 0);
-              if (j + 2 >= n) tc05::commit(&bars->pv_done[t]);
-            }
-            __syncwarp();
-            commit_one(&bars->v_empty[vst]);
-            if (++vst == NV) vst = 0, vph ^= 1u;
-            if (j + 2 < n) issue_next(j + 2);
-          }
-          ++oc[0];
-          if (++qbuf == nqb) qbuf = 0;
-          continue;
-        }
         ok = wait_warp(&bars->k_full[ks], kph, abort);
         for (int t = 0; t < 2 && ok; ++t) {
           if (sg.nt[t] == 0) continue;
@@ -883,6 +912,34 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       if (!ok && lane == 0) give_up(c.err, abort);
       commit_one(&bars->mma_final);
       if (lane == 0) drain(&bars->mma_final, 0);
+    } else if (C::kLoader && warp == 12) {
+      // ------------------------------------- raw value pages: a page per lane, a block per stage
+      bool ok = any;
+      const bool run = ok;
+      int v = 0;
+      for (bool last = false; ok && !last; ++v) {
+        const int rs = v % NR;
+        ok = wait_warp(&bars->meta_full[v % NM], (uint32_t)(v / NM) & 1u, abort);
+        if (ok && v >= NR) ok = wait_warp(&bars->raw_empty[rs], (uint32_t)(v / NR - 1) & 1u, abort);
+        if (!ok) break;
+        const BlockMeta& mt = bars->meta[v % NM];
+        last = mt.last;
+        const int pg = lane & (kTPages - 1), flags = lane < kTPages ? mt.flags[pg] : kSkip;
+        const bool mx = VM == kXMicro ? !(flags & kSkip) : VM == kXMixed && (flags & kMx);
+        const bool by = flags & (kE4 | kBs);
+        const uint32_t bytes = __reduce_add_sync(0xffffffffu, mx ? micro_head_bytes(D) : by ? kPage * D : 0);
+        if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[rs][0], bytes);
+        __syncwarp();
+        uint8_t* dst = sR + rs * C::RB + pg * (kPage * D);
+        if (mx)
+          bulk_load(dst, c.v_pages + (size_t)mt.page[pg] * c.v_page_stride + h * micro_head_bytes(D), micro_head_bytes(D),
+                    &bars->raw_full[rs][0]);
+        else if (by)
+          tma_load_4d(dst, &tv8, 0, h, 0, mt.page[pg], &bars->raw_full[rs][0]);
+      }
+      if (!ok && run && lane == 0) give_up(c.err, abort);
+#pragma unroll 1
+      for (int x = max(0, v - NR); x < v; ++x) drain(&bars->raw_full[x % NR][0], (uint32_t)(x / NR) & 1u);
     } else if (C::MK == 6 || warp != 12) {
       // ---------------------------- the V stages: pages vi, vi + MK of every block
       // (index: C::MK 6: warps 2, 3, 12-15; 5: 13, 2, 3, 14, 15; 4: 13, 14, 15, 2)
@@ -928,12 +985,14 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       const int t8 = D == 128 ? ((lane >> 2) & 1) | ((lane >> 4) << 1) : lane >> 2;
       const int c4 = lane & 1, t4 = D == 128 ? ((lane >> 1) & 3) | ((lane >> 4) << 2) : lane >> 1;
       for (int u = 0; ok && (more || u < issued); ++u) {
-        while (ok && more && issued < u + (kRaw ? NR : 1)) issue();
+        if (!C::kLoader)
+          while (ok && more && issued < u + (kRaw ? NR : 1)) issue();
         const int vs = u % NV, rs = u % NR;
-        if (ok && kRaw) ok = wait_warp(&bars->raw_full[rs][vi], (uint32_t)(u / NR) & 1u, abort);
+        if (ok && kRaw) ok = wait_warp(&bars->raw_full[rs][C::kLoader ? 0 : vi], (uint32_t)(u / NR) & 1u, abort);
         if (ok && u >= NV) ok = wait_warp(&bars->v_empty[vs], (uint32_t)(u / NV - 1) & 1u, abort);
         if (!ok) break;
         const BlockMeta& mt = bars->meta[u % NM];
+        if (C::kLoader) more = !mt.last;
         const bool edge = mt.z0 > 0 || mt.z1 < kTKeys;
 #pragma unroll 1
         for (int page = vi; page < kTPages; page += C::MK) {
@@ -1000,11 +1059,12 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         }
         fence_async();                                   // written for the MMAs; the raw bytes read for their refill
         __syncwarp();
+        if (C::kLoader && lane == 0) mbar_arrive(&bars->raw_empty[rs]);
         if (lane == 0) mbar_arrive(&bars->v_full[vs]);
       }
       if (!ok && run && lane == 0) give_up(c.err, abort);
-      if (kRaw)
-  #pragma unroll 1
+      if (kRaw && !C::kLoader)
+#pragma unroll 1
       for (int v = max(0, issued - NR); v < issued; ++v) drain(&bars->raw_full[v % NR][vi], (uint32_t)(v / NR) & 1u);
     }
   } else {
@@ -1051,7 +1111,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         float m_ref = -INFINITY, l = 0.f;
         bool bad = false;
         for (int jj = 0; jj < nmine; ++jj) {
-          const int blk = ALT ? 2 * jj + t : jj;         // block of the segment
+          const int blk = ALT ? 2 * jj + (t ^ (u0 & 1)) : jj;   // block of the segment
           ok = wait_warp(&bars->meta_full[(u0 + blk) % NM], (uint32_t)((u0 + blk) / NM) & 1u, abort);
           if (ok) ok = wait_warp(&bars->s_full[t], sc & 1u, abort);
           ++sc;
