@@ -393,7 +393,6 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const ExtendParams& e = p.e;
   const CacheView& c = e.c;
-  griddep_launch_dependents();
   if (smem_u32(sm_1k) & 1023u) {                       // the swizzled layouts would not hold
     if (threadIdx.x == 0) {
       report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_TIMEOUT, -2);
@@ -1354,8 +1353,10 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
 }
 
 // Joins the items that crossed CTAs: block (x, y) takes rows 32 y .. 32 y + 31 of the item that
-// begins in CTA x and ends in a later one, eight threads a row with D / 8 columns each: first the
-// row's maxima and sums, then its records, every load independent of the others.
+// begins in CTA x and ends in a later one, eight threads a row with D / 8 columns each, in the order of its
+// blocks; the loads are independent of the running maximum. Its blocks are dispatched as the last CTAs of the
+// attention leave: dispatched at its start they took 2-4 us from it. (Joined by the last of an item's
+// CTAs instead, behind a ticket, chunks took 40 us longer: one CTA per item is too few loads in flight.)
 //   M = max m_i,  L = sum l_i 2^(m_i - M),  out = sum acc_i 2^(m_i - M) / L
 template <int D, bool ALT>
 __global__ void __launch_bounds__(256)
@@ -1365,7 +1366,7 @@ extend_join_kernel(const ExtTcParams p) {
   if (s.n == 0) return;
   const ExtendParams& e = p.e;
   constexpr int C = D / 8;
-  const int row = blockIdx.y * 32 + (threadIdx.x >> 3), c0 = (threadIdx.x & 7) * C;
+  const int row = blockIdx.y * 32 + (threadIdx.x >> 3), c0 = (threadIdx.x & 7) * 4;
   const int TT = e.tile_tokens, t = row / kTRows, r = row % kTRows;
   const int q0 = __ldg(e.c.cu_q + s.b), n = __ldg(e.c.cu_q + s.b + 1) - q0;
   const int tok = (ALT ? s.i : 2 * s.i + t) * TT + r / e.G;
@@ -1373,12 +1374,6 @@ extend_join_kernel(const ExtTcParams p) {
   auto at = [&](int i) { return (size_t)(i == 0 ? s.first : 2 * ((int)blockIdx.x + i * e.c.Hkv)) * (2 * kTRows) + row; };
   float M = -INFINITY, L = 0.f, acc[C];
   bool bad = false;
-#pragma unroll 4
-  for (int i = 0; i < s.n; ++i) {
-    const float2 ml = p.part_ml[at(i)];
-    bad |= ml.y < 0.f;
-    if (ml.y != 0.f) M = fmaxf(M, ml.x);
-  }
 #pragma unroll
   for (int y = 0; y < C; ++y) acc[y] = 0.f;
 #pragma unroll 2
@@ -1387,27 +1382,28 @@ extend_join_kernel(const ExtTcParams p) {
     const float4* src = reinterpret_cast<const float4*>(p.part_acc + at(i) * D + c0);
     float4 v[C / 4];
 #pragma unroll
-    for (int y = 0; y < C / 4; ++y) v[y] = src[y];
-    if (ml.y == 0.f) continue;                       // (a record without keys holds no sums)
-    const float w = exp2f(ml.x - M);
-    L = fmaf(w, ml.y, L);
+    for (int y = 0; y < C / 4; ++y) v[y] = src[8 * y];
+    bad |= ml.y < 0.f;
+    if (ml.y == 0.f) continue;                         // (a record without keys holds no sums)
+    const float m = fmaxf(M, ml.x), a = L == 0.f ? 0.f : exp2f(M - m), w = exp2f(ml.x - m);
+    M = m;
+    L = fmaf(L, a, ml.y * w);
 #pragma unroll
     for (int y = 0; y < C / 4; ++y) {
-      acc[4 * y] = fmaf(w, v[y].x, acc[4 * y]);
-      acc[4 * y + 1] = fmaf(w, v[y].y, acc[4 * y + 1]);
-      acc[4 * y + 2] = fmaf(w, v[y].z, acc[4 * y + 2]);
-      acc[4 * y + 3] = fmaf(w, v[y].w, acc[4 * y + 3]);
+      acc[4 * y] = fmaf(acc[4 * y], a, v[y].x * w);
+      acc[4 * y + 1] = fmaf(acc[4 * y + 1], a, v[y].y * w);
+      acc[4 * y + 2] = fmaf(acc[4 * y + 2], a, v[y].z * w);
+      acc[4 * y + 3] = fmaf(acc[4 * y + 3], a, v[y].w * w);
     }
   }
   const size_t o = (size_t)(q0 + tok) * e.c.Hq + s.h * e.G + r % e.G;
   const bool none = bad || L == 0.f;
   const float inv = none ? 0.f : (p.scale_ptr ? __ldg(p.scale_ptr) : 1.f) / L;
 #pragma unroll
-  for (int y = 0; y < C; y += 8) {
-    uint4 q = make_uint4(xt::pack2(acc[y] * inv, acc[y + 1] * inv), xt::pack2(acc[y + 2] * inv, acc[y + 3] * inv),
-                         xt::pack2(acc[y + 4] * inv, acc[y + 5] * inv), xt::pack2(acc[y + 6] * inv, acc[y + 7] * inv));
-    if (none) q = make_uint4(0u, 0u, 0u, 0u);
-    *reinterpret_cast<uint4*>(e.out + o * D + c0 + y) = q;
+  for (int y = 0; y < C / 4; ++y) {
+    uint2 q = make_uint2(xt::pack2(acc[4 * y] * inv, acc[4 * y + 1] * inv), xt::pack2(acc[4 * y + 2] * inv, acc[4 * y + 3] * inv));
+    if (none) q = make_uint2(0u, 0u);
+    *reinterpret_cast<uint2*>(e.out + o * D + c0 + 32 * y) = q;
   }
   if (c0 == 0 && e.lse) e.lse[o] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
