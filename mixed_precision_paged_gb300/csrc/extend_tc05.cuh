@@ -49,7 +49,6 @@ constexpr int kTPages = kTKeys / kPage;
 constexpr int kT5Threads = 512;
 constexpr int kAltRows = 64;                // rows of a sequence and KV head up to which blocks alternate
 constexpr int kMetaAhead = 2;               // blocks that page lookups are ahead of the K loads
-constexpr int kItemCost = 1;                // an item's start (query load, epilogue) in blocks
 
 struct ExtTcSplit {                         // an item that crosses CTAs, for the joining kernel
   int n;                                    // CTAs it spans; 0: none
@@ -262,6 +261,11 @@ __device__ __forceinline__ int floor_sum(int n, int m, int a, int b) {
   return (int)s;
 }
 
+// What an item's start and end (queries, first scores, epilogue) cost, in blocks. ALT, 1 / 2 / 3 / 4: 200 microscaled
+// sequences of 1-4 tokens 125 / 123 / 121 / 122 us; pairs, 1 / 2: chunks 229.4 / 229.6 us.
+template <bool ALT>
+constexpr int kItemCost = ALT ? 3 : 1;
+
 // The items of one sequence and KV head: pairs of tiles, `step` tokens each.
 struct Items {
   int n, t0, np;              // new tokens, position of the first, items
@@ -278,9 +282,9 @@ struct Items {
   template <bool ALT>
   __device__ __forceinline__ int before(int i) const {
     if (i <= 0) return 0;
-    if (ALT) return kItemCost + jhi(0) - jlo(0);      // (one item)
+    if (ALT) return kItemCost<ALT> + jhi(0) - jlo(0);      // (one item)
     const int full = i == np ? np - 1 : i;            // the last item may be short
-    int s = kItemCost * i + floor_sum(full, kTKeys, step, t0 + step + kTKeys - 1);
+    int s = kItemCost<ALT> * i + floor_sum(full, kTKeys, step, t0 + step + kTKeys - 1);
     if (i == np) s += jhi(np - 1);
     const int i0 = t0 >= window - 1 ? 0 : min(i, (window - 2 - t0) / step + 1);   // items whose window starts at key 0
     if (i > i0) s -= floor_sum(i - i0, kTKeys, step, t0 + i0 * step - window + 1);
@@ -355,7 +359,7 @@ __device__ __forceinline__ bool walk_next(const ExtendParams& e, Walk& w, Segmen
           w.it = items_of<ALT>(e, sq);
         }
       }
-      if (w.b < e.c.batch) w.j = w.it.jlo(w.i) - kItemCost;
+      if (w.b < e.c.batch) w.j = w.it.jlo(w.i) - kItemCost<ALT>;
     }
     if (sg.ja < sg.jb) {
       sg.slot = 2 * (int)blockIdx.x + (w.index == 0 ? 0 : 1);
@@ -491,7 +495,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         total = carry;
         carry = 0;
         per = total <= INT_MAX ? ((uint32_t)total + ranges - 1u) / (uint32_t)ranges : (total + ranges - 1) / ranges;
-        if (per < 2) per = 2;
+        if (per <= kItemCost<ALT>) per = kItemCost<ALT> + 1;
         start = (int)blockIdx.x / c.Hkv < ranges ? per * ((int)blockIdx.x / c.Hkv) : total;
         budget0 = (int)max(0ll, min(per, total - start));
         if (budget0 == 0) break;
@@ -506,7 +510,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     if (carry > start) break;
   }
   __syncthreads();
-  // (two units of a range hold a block, as does its last one: a range that is not empty has blocks)
+  // (kItemCost + 1 units hold a block, and the last unit of all is one: a range that is not empty has blocks)
   const bool any = budget0 > 0;
   const uint32_t tbase = bars->tmem_base;
   const int TT = e.tile_tokens;                        // tokens of a tile
@@ -550,7 +554,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           lo += last * step;
         }
         w.i = lo;
-        w.j = w.it.jlo(lo) - kItemCost + off - before;
+        w.j = w.it.jlo(lo) - kItemCost<ALT> + off - before;
       }
       ExtTcSplit split;
       split.n = 0;
@@ -1125,13 +1129,14 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             for (int pg = 0; pg < kTPages; ++pg)
               if (((badp >> pg) & 1) && pg * kPage <= hi_c && pg * kPage + kPage - 1 > lo_c) bad = true;
           }
-          // The row's maximum, in log2 units. NH 1: the row stays in registers. NH 2: half of it at a time, read
-          // again for the weights (and written back where masked), for half the code: the loops of a CTA's
-          // roles share one instruction cache, and where the makers' loop is the long one (mixed pages)
-          // or each softmax warp runs alone (ALT) that counts for more than the second read. Measured,
-          // NH 1 / 2: mixed chunks under a window 150 / 144 us, 48 x 5 tokens over mixed pages 166 / 161 us,
-          // 4,096 tokens behind 16K of E4M3 884 / 916 us.
-          constexpr int NH = ALT || VM == kXMixed ? 2 : 1, NC = 4 / NH;
+          // The row's maximum, in log2 units. NH 1: the row stays in registers. NH 4: a quarter of it at a time, read
+          // again for the weights (and written back where masked), for a quarter of the code: the loops of
+          // a CTA's roles share one instruction cache, and where the makers' loop is the long one (mixed
+          // pages) or each softmax warp runs alone (ALT) that counts for more than the second read.
+          // NH 1 / 2 / 4: a token behind 8K keys (32 sequences) 152 / 146 / 144 us, 48 x 5 tokens over mixed
+          // pages 166 / 151 / 147 us, mixed chunks under a window 146 / 136 / 135 us, 4,096 tokens behind 16K of E4M3
+          // 844 / 852 / 936 us.
+          constexpr int NH = ALT || VM == kXMixed ? 4 : 1, NC = 4 / NH;
           uint32_t a[NC][32];
           float mx = -INFINITY;
 #pragma unroll 1
@@ -1140,12 +1145,13 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             for (int c4 = 0; c4 < NC; ++c4) tc05::ld32(t_s + 32 * (NC * hf + c4), a[c4]);
             tc05::wait_ld();
             if (masked) {
-              const int hc = hi_c - 32 * NC * hf, lc = lo_c - 32 * NC * hf;
+              const int lc = lo_c - 32 * NC * hf;        // keys lc + 1 .. lc + seen of these
+              const uint32_t seen = (uint32_t)max(hi_c - lo_c, 0);
 #pragma unroll
               for (int c4 = 0; c4 < NC; ++c4)
 #pragma unroll
                 for (int x = 0; x < 32; ++x)
-                  if (32 * c4 + x > hc || 32 * c4 + x <= lc) a[c4][x] = __float_as_uint(-INFINITY);
+                  if ((uint32_t)(32 * c4 + x - lc - 1) >= seen) a[c4][x] = __float_as_uint(-INFINITY);
               if (NH > 1) {
 #pragma unroll
                 for (int c4 = 0; c4 < NC; ++c4) tc05::st32(t_s + 32 * (NC * hf + c4), a[c4]);
