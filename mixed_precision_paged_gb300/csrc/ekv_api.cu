@@ -22,7 +22,6 @@ cudaError_t launch_split_simt(const CUtensorMap& tk, const CUtensorMap& t8, cons
 cudaError_t launch_split_mma(const CUtensorMap& tk, const CUtensorMap& t8, const CUtensorMap& t16,
                              const DecodeParams& p, int D, int vmode, int grid, size_t smem, cudaStream_t st);
 
-
 cudaError_t launch_extend_tc05_64(const ExtTcMaps& m, const ExtTcParams& p, int vm, int grid, cudaStream_t st);
 cudaError_t launch_extend_tc05_128(const ExtTcMaps& m, const ExtTcParams& p, int vm, int grid, cudaStream_t st);
 
@@ -705,6 +704,7 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
   const long long rows = (long long)p.G * max_q;
   x.nw = rows <= kAltRows ? (int)((rows + 31) / 32) : 0;
   x.e.tile_tokens = (x.nw > 0 ? 32 * x.nw : kTRows) / p.G;
+  if (vm == kXE4M3 && scale_mode == EKV_SCALE_PER_TENSOR) x.scale_ptr = v_scales;
   // one coordinate for (page, head): in units that divide both the page stride and a head's row
   int unit = 2 * D;
   while (v_page_stride_bytes % unit) unit /= 2;
@@ -718,7 +718,8 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
   if ((vm == kXFP16 || vm == kXMixed) && !encode_group_map(&m.v16, v_pages, D, Hkv, places, unit)) return EKV_ERR_INVALID_ARG;
   if ((vm == kXE4M3 || vm == kXMixed) && !encode_e4m3_slice_map(&m.v8, v_pages, D, Hkv, num_pages, v_page_stride_bytes))
     return EKV_ERR_INVALID_ARG;
-  const cudaError_t e = D == 128 ? launch_extend_tc05_128(m, x, vm, c->split_ctas, st) : launch_extend_tc05_64(m, x, vm, c->split_ctas, st);
+  const cudaError_t e = D == 128 ? launch_extend_tc05_128(m, x, vm, c->split_ctas, st)
+                                 : launch_extend_tc05_64(m, x, vm, c->split_ctas, st);
   if (e != cudaSuccess) return EKV_ERR_CUDA;
   note_launch(st, kAfterReader);
   return EKV_OK;

@@ -462,7 +462,8 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   };
   // CTA x works on KV head x mod H_kv and range x / H_kv: the heads of a page are read at about the
   // same time
-  const int ranges = (int)gridDim.x / c.Hkv, h = (int)blockIdx.x % c.Hkv, chunks = (c.batch + kT5Threads - 1) / kT5Threads;
+  const int ranges = (int)gridDim.x / c.Hkv, h = (int)blockIdx.x % c.Hkv;
+  const int chunks = (c.batch + kT5Threads - 1) / kT5Threads;
   long long mine = 0, incl = 0, total = 0, carry = 0, per = 0, start = 0;
   int budget0 = 0;
   // the total, and then the sequence of position `start`; one chunk's costs serve both
@@ -1025,7 +1026,8 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             for (int x = 0; x < D / 32; ++x) {
               const int t = t8 + x * (512 / D), r = t & 7, ch = 4 * s8 + c8;
               uint4 lo, hi;
-              const uint4 q = *reinterpret_cast<const uint4*>(src + (D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16)));
+              const uint32_t at = D == 128 ? swz128(t * 128 + ch * 16) : swz64(t * 64 + ch * 16);
+              const uint4 q = *reinterpret_cast<const uint4*>(src + at);
               if (VM == kXMixed && (fl & kBs)) {
                 lo = make_uint4(__byte_perm(q.x, 0u, 0x1404), __byte_perm(q.x, 0u, 0x3424), __byte_perm(q.y, 0u, 0x1404),
                                 __byte_perm(q.y, 0u, 0x3424));
@@ -1056,8 +1058,8 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             for (int x = lane; x < kPage * (D / 8); x += 32) {
               const int key = page * kPage + x / (D / 8), cz = x % (D / 8);
               if (key < mt.z0 || key >= mt.z1 || ((smask >> page) & 1u))
-                *reinterpret_cast<uint4*>(sV + vs * C::IB + (key >> 3) * C::GB + (cz >> 3) * 1024 + (key & 7) * 128 + (cz & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(sV + vs * C::IB + (key >> 3) * C::GB + (cz >> 3) * 1024 + (key & 7) * 128 +
+                                          (cz & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
         }
         fence_async();                                   // written for the MMAs; the raw bytes read for their refill
@@ -1407,7 +1409,8 @@ extend_join_kernel(const ExtTcParams p) {
   const float inv = none ? 0.f : (p.scale_ptr ? __ldg(p.scale_ptr) : 1.f) / L;
 #pragma unroll
   for (int y = 0; y < C / 4; ++y) {
-    uint2 q = make_uint2(xt::pack2(acc[4 * y] * inv, acc[4 * y + 1] * inv), xt::pack2(acc[4 * y + 2] * inv, acc[4 * y + 3] * inv));
+    uint2 q = make_uint2(xt::pack2(acc[4 * y] * inv, acc[4 * y + 1] * inv),
+                         xt::pack2(acc[4 * y + 2] * inv, acc[4 * y + 3] * inv));
     if (none) q = make_uint2(0u, 0u);
     *reinterpret_cast<uint2*>(e.out + o * D + c0 + 32 * y) = q;
   }
