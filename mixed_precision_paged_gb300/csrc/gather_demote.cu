@@ -204,6 +204,7 @@ transition_kernel(const DemoteParams p, int n, int S) {
   __shared__ float s_scale[kMaxKvHeads];
   __shared__ float s_recip[kMaxKvHeads];
   __shared__ int s_nonfinite;
+  __shared__ int s_bad[2];                        // kToMicro: the same of the page at hand and the next, in turn
   // kToMicro: the page being put together and the one being written, in turn
   const int out_bytes = p.Hkv * micro_head_bytes(p.D);
   uint8_t* const out = ring + S * (2 * kPage * p.Hkv * p.D);
@@ -218,6 +219,8 @@ transition_kernel(const DemoteParams p, int n, int S) {
   // (8v / D) mod H_kv. A thread's vectors are tid + 256u, 2048u elements apart, a
   // multiple of H_kv * D (<= 1024): they all lie in the same head.
   const int head = ((tid * 8) / p.D) % p.Hkv;
+  // microscaled forms: token row of vector tid, rows between a thread's vectors, column in the head
+  const int row0 = (tid * 8) / (p.Hkv * p.D), row_step = 8 * kDemoteThreads / (p.Hkv * p.D), col = (tid * 8) % p.D;
   const int want = OP == kPromote ? EKV_MODE_BASE : OP == kFromMicro ? EKV_MODE_MICRO_FP4 : EKV_MODE_TARGET_FP16;
 
   // items k0 .. k0 + kChunk - 1 of this CTA: page id if valid and in the source mode,
@@ -273,7 +276,7 @@ transition_kernel(const DemoteParams p, int n, int S) {
     fence_barrier_init();
   }
   if (tid < kMaxKvHeads) s_amax[tid] = 0u;
-  if (tid == 0) s_nonfinite = 0;
+  if (tid == 0) s_nonfinite = s_bad[0] = s_bad[1] = 0;
   load_chunk(0);
   __syncthreads();
   if (tid == 0)
@@ -302,13 +305,12 @@ transition_kernel(const DemoteParams p, int n, int S) {
       } else if (OP == kFromMicro) {
         // vector v: 8 values of token row 8v / (H_kv D), from 4 code bytes and their scale
         const uint8_t* st = ring + sl * page_bytes + head * micro_head_bytes(p.D);
-        const int col = (tid * 8) % p.D;
         bool bad = false;
 #pragma unroll
         for (int u = 0; u < kMaxVec; ++u) {
           const int v = tid + u * kDemoteThreads;
           if (v < nvec) {
-            const int row = (v * 8) / (p.Hkv * p.D);
+            const int row = row0 + u * row_step;
             const uint32_t codes = *reinterpret_cast<const uint32_t*>(st + (row * p.D + col) / 2);
             const uint32_t sb = st[micro_scale_off(p.D) + (row * p.D + col) / kMicroBlock];
             const bool good = micro_scale_ok(sb);
@@ -332,8 +334,12 @@ transition_kernel(const DemoteParams p, int n, int S) {
           }
         }
         unsigned int mx = max(mx2 & 0xffffu, mx2 >> 16);
-        for (int off = 1; off < lanes_per_row; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        if ((lane % lanes_per_row) == 0 && tid < nvec) atomicMax(&s_amax[head], mx);
+        if (OP == kToMicro) {
+          if (mx >= 0x7c00u) s_bad[k & 1] = 1;
+        } else {
+          for (int off = 1; off < lanes_per_row; off <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+          if ((lane % lanes_per_row) == 0 && tid < nvec) atomicMax(&s_amax[head], mx);
+        }
       }
     }
     const int kn = k + S;                          // the item that refills this slot
@@ -368,7 +374,7 @@ transition_kernel(const DemoteParams p, int n, int S) {
       if (tid == 0) p.page_mode[page] = EKV_MODE_TARGET_FP16;
       continue;
     }
-    if (tid < p.Hkv) {
+    if (OP != kToMicro && tid < p.Hkv) {
       const unsigned int bits = s_amax[tid];
       s_amax[tid] = 0u;
       if (bits >= 0x7c00u) {
@@ -380,8 +386,8 @@ transition_kernel(const DemoteParams p, int n, int S) {
         s_recip[tid] = __frcp_rn(sc);
       }
     }
-    __syncthreads();
-    const bool skip = s_nonfinite != 0;
+    if (OP != kToMicro) __syncthreads();
+    const bool skip = (OP == kToMicro ? s_bad[k & 1] : s_nonfinite) != 0;
     if (!skip && OP == kToE4M3) {
       const float s = s_scale[head], rs = s_recip[head];
 #pragma unroll
@@ -418,13 +424,12 @@ transition_kernel(const DemoteParams p, int n, int S) {
     }
     if (!skip && OP == kToMicro) {
       uint8_t* slice = out + (k & 1) * out_bytes + head * micro_head_bytes(p.D);
-      const int col = (tid * 8) % p.D;
 #pragma unroll
       for (int u = 0; u < kMaxVec; ++u) {
         const int v = tid + u * kDemoteThreads;
         // nvec is a multiple of 128: whole warps leave here, so the shuffles see full warps
         if (v >= nvec) break;
-        const int row = (v * 8) / (p.Hkv * p.D);
+        const int row = row0 + u * row_step;
         uint32_t mx2 = __vmaxu2(__vmaxu2(buf[u].x & 0x7fff7fffu, buf[u].y & 0x7fff7fffu),
                                 __vmaxu2(buf[u].z & 0x7fff7fffu, buf[u].w & 0x7fff7fffu));
         mx2 = __vmaxu2(mx2, __shfl_xor_sync(0xffffffffu, mx2, 1));
@@ -443,7 +448,7 @@ transition_kernel(const DemoteParams p, int n, int S) {
     if (tid == 0) {
       if (skip) report_error(p.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_NONFINITE_PAGE, page);
       else p.page_mode[page] = OP == kToBase ? EKV_MODE_BASE : OP == kToMicro ? EKV_MODE_MICRO_FP4 : EKV_MODE_COMPACT_E4M3;
-      s_nonfinite = 0;
+      s_nonfinite = s_bad[k & 1] = 0;
     }
   }
   if (OP == kToMicro && tid == 0) bulk_store_wait();
