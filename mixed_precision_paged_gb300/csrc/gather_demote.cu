@@ -168,8 +168,9 @@ gather_kernel(const GatherParams p, const GatherRanges r) {
 //    bytes and the backing's low bytes.
 //  kToMicro (TARGET -> microscaled FP4): a thread's vector of 8 values and those of the 3
 //    lanes beside it are one block of 32; its largest magnitude is two shuffles away. The page's
-//    codes and scales are put together in shared memory and leave by one bulk copy (8,192 pages
-//    of 32 KiB: 74 us; written by 4-byte stores 79 us).
+//    codes and scales are put together in shared memory and leave by one bulk copy, 74 us for 8,192
+//    pages of 32 KiB where 4-byte stores took 79; without maxima per head (a flag serves) and without a
+//    division per vector 59 us, 5.8 TB/s (the way back, likewise, 70 -> 59 us).
 //  kFromMicro (microscaled FP4 -> TARGET): every code times its scale, an fp16 value.
 // Demotions skip (and report) a page holding NaN/inf and leave it TARGET.
 //
