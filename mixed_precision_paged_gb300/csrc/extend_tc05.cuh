@@ -10,8 +10,10 @@
 //     rows, and one tile's softmax runs while the other's products do.
 //   * blocks: 8 pages by one TMA box each, 8-token groups of [D / 64][8 rows][128 B] (128B swizzle),
 //     which serve as K-major B of S and, for V, as N-major B of the second product.
-//   * values: FP16 pages land in a V stage directly. E4M3, BASE and microscaled pages land raw, each
-//     maker warp's in a ring of its own, and are expanded into the V stage, exactly; E4M3 scales join the
+//   * values: FP16 pages land in a V stage directly. E4M3, BASE and microscaled pages land raw, in a ring
+//     that one warp fills for all makers or each maker for itself (loads and conversions of one warp
+//     wait for one another: 200 microscaled sequences 139 us, with the loader 129), and are expanded into
+//     the V stage, exactly; E4M3 scales join the
 //     exponent, p' = 2^(score + log2 scale - m) with the maximum m over the scaled scores, and the sum
 //     takes p' / scale: so codes enter the product exactly as they are, and p' is rounded to fp16
 //     once relative to the largest contribution, whatever the scales; one scale for all codes
@@ -21,8 +23,8 @@
 //     a second kernel joins them. Long causal chunks so balance to a block, and one short chunk
 //     behind a long prefix still uses every SM.
 // Roles: warp 0 checks the pages and loads Q and K; warp 1 issues the MMAs; warp 3 loads FP16 value
-// pages; warps 4-7 and 8-11 are the softmax of tile 0 and 1, a thread per row; the others (makers)
-// load and expand the other pages (warp 2 also owns tensor memory). The registers are split to match
+// pages; warps 4-7 and 8-11 are the softmax of tile 0 and 1, a thread per row; the others are makers,
+// which expand the other pages, or their loader (warp 2 also owns tensor memory). The registers are split to match
 // (setmaxnreg): 80, 176, 176 and 80 a thread, 512 = 4 x the 128 of launch. Tensor memory of tile t: S
 // and P at 256 t, O at 256 t + 128. The order of the MMAs and the lazily moved maximum are those of the
 // prefill (prefill_tc05.cu).
@@ -77,8 +79,8 @@ struct XT {
   static constexpr int NK = (VM == kXFP16 || ALT ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 4)) + (ALT && D == 64 ? 1 : 0);
   static constexpr int NV = (D == 128 ? 2 : 4) + (ALT && VM == kXFP16 ? 1 : 0);
   static constexpr int NR = (D == 128 ? 2 : 4) + (ALT ? 1 : 0);
-  // maker warps: warps 2 and 13-15, warp 3 where no FP16 pages are to be loaded, and warp 12 where
-  // its scheduler does not have all of the softmax (ALT)
+  // maker warps: warps 2 and 13-15, warp 3 too where there are no FP16 pages for it to load, and warp 12
+  // too where blocks are shared by two tiles and so last longer
   static constexpr int MK = VM == kXFP16 || VM == kXMixed ? 4 : ALT ? 5 : 6;
   // five or four makers leave warp 12 to load the raw pages for all of them
   static constexpr bool kLoader = VM != kXFP16 && MK < 6;
