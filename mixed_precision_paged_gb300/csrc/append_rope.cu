@@ -4,7 +4,8 @@
 // Per pair (u, w) of a head at angle a: (u cos a - w sin a, w cos a + u sin a), in fp32 from
 // the caller's table, rounded once to fp16. Pure streaming: every input value is read once and
 // every output written once (per token 2 B in and out of each query, key and FP16 value), plus
-// the table row, which all heads of a token share: the floor is those bytes at HBM rate.
+// the table row, which all heads of a token share: the floor is those bytes at HBM rate. 65,536 tokens of
+// 32 + 2 x 8 heads of 128, FP16 pages: 252 us, 6.4 TB/s. (Consecutive tokens a warp, which saves look-ups, 259 us.)
 //
 // One warp takes a token, or a share of its heads when tokens are few. A lane owns unit u of a
 // head, 16 values: with half-split pairs the 8-value vectors u and u + rope_dim / 16, so that
