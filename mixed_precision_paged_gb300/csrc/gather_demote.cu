@@ -206,7 +206,10 @@ transition_kernel(const DemoteParams p, int n, int S) {
   __shared__ float s_recip[kMaxKvHeads];
   __shared__ int s_nonfinite;
   __shared__ int s_bad[2];                        // kToMicro: the same of the page at hand and the next, in turn
-  // kToMicro: the page being put together and the one being written, in turn
+  // kToMicro: the page being put together and the one being written, in turn. The turn goes by the
+  // pages stored (`stored`, the same in all threads), not by items: an item that is skipped waits for no copy,
+  // so only the buffer that the last stored page did not use is known to have been read.
+  int stored = 0;
   const int out_bytes = p.Hkv * micro_head_bytes(p.D);
   uint8_t* const out = ring + S * (2 * kPage * p.Hkv * p.D);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -424,7 +427,7 @@ transition_kernel(const DemoteParams p, int n, int S) {
       }
     }
     if (!skip && OP == kToMicro) {
-      uint8_t* slice = out + (k & 1) * out_bytes + head * micro_head_bytes(p.D);
+      uint8_t* slice = out + (stored & 1) * out_bytes + head * micro_head_bytes(p.D);
 #pragma unroll
       for (int u = 0; u < kMaxVec; ++u) {
         const int v = tid + u * kDemoteThreads;
@@ -442,9 +445,12 @@ transition_kernel(const DemoteParams p, int n, int S) {
     }
     if (OP == kToMicro) fence_reads_before_refill();   // (orders the stores above before the bulk copy too)
     __syncthreads();                               // s_nonfinite and the scales are read
-    if (OP == kToMicro && tid == 0 && !skip) {
-      bulk_store(base, out + (k & 1) * out_bytes, (uint32_t)out_bytes);
-      bulk_store_wait_read<1>();                     // the one before has left the buffer that comes next
+    if (OP == kToMicro && !skip) {
+      if (tid == 0) {
+        bulk_store(base, out + (stored & 1) * out_bytes, (uint32_t)out_bytes);
+        bulk_store_wait_read<1>();                   // the one before has left the buffer that comes next
+      }
+      ++stored;
     }
     if (tid == 0) {
       if (skip) report_error(p.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_NONFINITE_PAGE, page);
