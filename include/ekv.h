@@ -351,8 +351,8 @@ ekv_status ekv_append_kv(ekv_ctx* ctx, const void* k_new, const void* v_new, voi
  *  rope_style       0: pairs (i, i + rope_dim / 2); 1: pairs (2i, 2i + 1).
  *  q_out            fp16 [total_q][H_q][D], contiguous; may be q itself when q is contiguous.
  *  seq_lens         int32 [batch]: tokens of each sequence with the new ones; cu_q int32 [batch + 1],
- *                   nondecreasing from 0; total_q: rows of q (host). Rows >= cu_q[batch] are neither
- *                   read nor written.
+ *                   nondecreasing from 0; total_q: at least cu_q[batch] (host). Rows from cu_q[batch]
+ *                   on are neither read nor written, and need not exist.
  * Device checks (reported; nothing is written): n_b < 0 or > seq_lens[b], seq_lens[b] >
  * block_table_stride * 16 (EKV_DETAIL_SEQ_LEN, the whole sequence); a page id outside the
  * pool, a mode byte > 3 (the token's K and V rows); a scale that is not positive finite

@@ -5,7 +5,7 @@
 // the caller's table, rounded once to fp16. Pure streaming: every input value is read once and
 // every output written once (per token 2 B in and out of each query, key and FP16 value), plus
 // the table row, which all heads of a token share: the floor is those bytes at HBM rate. 65,536 tokens of
-// 32 + 2 x 8 heads of 128, FP16 pages: 252 us, 6.4 TB/s. (Consecutive tokens a warp, which saves look-ups, 259 us.)
+// 32 + 2 x 8 heads of 128, FP16 pages: 253 us, 6.4 TB/s. (Consecutive tokens a warp, which saves look-ups, 259 us.)
 //
 // One warp takes a token, or a share of its heads when tokens are few. A lane owns unit u of a
 // head, 16 values: with half-split pairs the 8-value vectors u and u + rope_dim / 16, so that
@@ -82,7 +82,10 @@ rope_append_kernel(const RopeAppendParams p, int parts, int part_rows) {
   // below rope_dim / 8, and 2u of the first unit past them is rope_dim / 8
   const bool split = rot && p.rope_style == 0;
   const int v0 = split ? u : 2 * u, v1 = split ? u + p.rope_dim / 16 : 2 * u + 1;
-  const long long items = (long long)c.total_q * parts;
+  // Rows behind the last sequence are not touched: k_new and v_new may end there. (Known before the first row is
+  // loaded, which costs a look-up once, 1 us of 253.)
+  const int end = min(c.total_q, __ldg(c.cu_q + c.batch));
+  const long long items = (long long)end * parts;
   for (long long it = warp; it < items; it += warps) {
     const int i = (int)(it / parts), part = (int)(it % parts);
     int b = -1, t = 0, page = -1, mode = 0;
