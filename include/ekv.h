@@ -389,7 +389,10 @@ ekv_status ekv_append_kv_rope(ekv_ctx* ctx, const void* q, const void* k_new, co
  *  window       keys a query sees, its own among them; 0: no window.
  *  lse          fp32 [total_q][H_q], natural logarithm, or NULL.
  * A page that fails its check (id, mode byte > 3, scale) zeroes out and sets lse = -inf for the
- * queries that see one of its keys (of one KV head for a bad per-(page, head) scale). Returns
+ * queries that see one of its keys (of one KV head for a bad per-(page, head) scale).
+ * The one scale of a uniform E4M3 pool may be any positive finite one. Scales per (page, head), or beside
+ * pages of other forms, may be up to 2^40; a larger one fails its check (EKV_DETAIL_SCALE), and one below
+ * 2^-44 counts as 2^-44 (the page's values, below 2^-35, leave no trace in fp16). Returns
  * EKV_ERR_CAPACITY when batch > cfg.max_batch, EKV_ERR_UNSUPPORTED when block_table_stride > 131072
  * or a pool has 2^31 or more head rows. Other arguments as
  * for ekv_paged_decode. Sums are fp32; the weights enter the product with V rounded to fp16. */

@@ -53,6 +53,12 @@ constexpr int kTPages = kTKeys / kPage;
 constexpr int kT5Threads = 512;
 constexpr int kAltRows = 64;                // rows of a sequence and KV head up to which blocks alternate
 constexpr int kMetaAhead = 2;               // blocks that page lookups are ahead of the K loads
+// E4M3 scales where they differ by page, or beside pages of other forms: a page beyond kScaleMost fails its check (above
+// 2^25 no code but 0 stands for a value within fp16's range), and below kScaleLeast a scale counts as that (such values,
+// under 448 * 2^-44 < 2^-35, leave no trace in an fp16 output). So 1 / scale is finite, and a weight p' = 2^(score +
+// log2 scale - m) that ex2 flushes, below 2^-126, belongs to a key whose score is 2^42 below another's:
+// up to 2^-126 * 2^(40 + 44) of the sum, however the scales differ.
+constexpr float kScaleLeast = 1.f / (1ll << 44), kScaleMost = (float)(1ll << 40);
 
 struct ExtTcSplit {                         // an item that crosses CTAs, for the joining kernel
   int n;                                    // CTAs it spans; 0: none
@@ -680,8 +686,8 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                   : mode0 == EKV_MODE_MICRO_FP4 ? kMx : 0;
           if (id0 < 0 || id0 >= c.num_pages) detail = EKV_DETAIL_PAGE_ID;
           else if (mode0 > EKV_MODE_MICRO_FP4) detail = EKV_DETAIL_PAGE_MODE;
-          else if ((flags & kE4) && !scale_ok(vs0)) detail = EKV_DETAIL_SCALE;
-          else if (flags & kE4) vs = vs0;
+          else if ((flags & kE4) && !(scale_ok(vs0) && (!PS || vs0 <= kScaleMost))) detail = EKV_DETAIL_SCALE;
+          else if (flags & kE4) vs = fmaxf(vs0, kScaleLeast);
           if (detail) {
             report_error(c.err, EKV_ERR_DEVICE_CHECK, detail, b0.b);
             flags = kSkip;
