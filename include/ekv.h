@@ -395,7 +395,9 @@ ekv_status ekv_append_kv_rope(ekv_ctx* ctx, const void* q, const void* k_new, co
  * 2^-44 counts as 2^-44 (the page's values, below 2^-35, leave no trace in fp16). Returns
  * EKV_ERR_CAPACITY when batch > cfg.max_batch, EKV_ERR_UNSUPPORTED when block_table_stride > 131072
  * or a pool has 2^31 or more head rows. Other arguments as
- * for ekv_paged_decode. Sums are fp32; the weights enter the product with V rounded to fp16. */
+ * for ekv_paged_decode. Sums are fp32; the weights enter the product with V rounded to fp16 (times
+ * the page's scale where scales differ: a row's error is 2^-11 of each term, or 2^-32 of its largest
+ * weight times scale for the terms below 2^-21 of that). */
 ekv_status ekv_extend_attention(ekv_ctx* ctx, const void* q, const void* k_pages, const void* v_pages,
                                 long long v_page_stride_bytes, int num_pages, const float* v_scales,
                                 int scale_mode, const uint8_t* page_mode, int uniform_mode,

@@ -15,8 +15,8 @@
 //     wait for one another: 200 microscaled sequences 139 us, with the loader 129), and are expanded into
 //     the V stage, exactly; E4M3 scales join the exponent, p' = 2^(score + log2 scale - m) with the
 //     maximum m over the scaled scores, and the sum takes p' / scale: so codes enter the product exactly
-//     as they are, and p' is rounded to fp16 once relative to the largest contribution, whatever the
-//     scales; one scale for all codes scales the output instead. A microscaled value is code * 2^k, exact in fp16.
+//     as they are, and p' is rounded to fp16 once relative to the row's largest weight times scale;
+//     one scale for all codes scales the output instead. A microscaled value is code * 2^k, exact in fp16.
 //   * split: the blocks of all items form one stream, cut into equal ranges, one persistent CTA
 //     each; an item that crosses a border leaves partial rows (m, l, O) in at most two slots a CTA, and
 //     a second kernel joins them. Long causal chunks so balance to a block, and one short chunk
@@ -53,6 +53,11 @@ constexpr int kTPages = kTKeys / kPage;
 constexpr int kT5Threads = 512;
 constexpr int kAltRows = 64;                // rows of a sequence and KV head up to which blocks alternate
 constexpr int kMetaAhead = 2;               // blocks that page lookups are ahead of the K loads
+// The reference m of a row lies this far below its maximum (in log2), so weights are up to 2^7, and 2^15 before a
+// reference is moved (8 later): near the top of fp16's range, so that weights keep all their bits down to 2^-21 of the largest
+// weight times scale, and what is rounded below costs 2^-32 of it. With the maximum itself as the reference a page of
+// zeros (scale 1) took that precision from pages whose scale is small: values of 1e-4 came out 3% off.
+constexpr float kHeadroom = 7.f;
 // E4M3 scales where they differ by page, or beside pages of other forms: a page beyond kScaleMost fails its check (above
 // 2^25 no code but 0 stands for a value within fp16's range), and below kScaleLeast a scale counts as that (such values,
 // under 448 * 2^-44 < 2^-35, leave no trace in an fp16 output). So 1 / scale is finite, and a weight p' = 2^(score +
@@ -686,8 +691,8 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
                   : mode0 == EKV_MODE_MICRO_FP4 ? kMx : 0;
           if (id0 < 0 || id0 >= c.num_pages) detail = EKV_DETAIL_PAGE_ID;
           else if (mode0 > EKV_MODE_MICRO_FP4) detail = EKV_DETAIL_PAGE_MODE;
-          else if ((flags & kE4) && !(scale_ok(vs0) && (!PS || vs0 <= kScaleMost))) detail = EKV_DETAIL_SCALE;
-          else if (flags & kE4) vs = fmaxf(vs0, kScaleLeast);
+          else if ((flags & kE4) && !(PS ? vs0 > 0.f && vs0 <= kScaleMost : scale_ok(vs0))) detail = EKV_DETAIL_SCALE;
+          else if (PS && (flags & kE4)) vs = fmaxf(vs0, kScaleLeast);
           if (detail) {
             report_error(c.err, EKV_ERR_DEVICE_CHECK, detail, b0.b);
             flags = kSkip;
@@ -1188,7 +1193,7 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               }
             }
           }
-          if (!PS) mx *= qs;
+          mx = PS ? mx - kHeadroom : fmaf(mx, qs, -kHeadroom);
           const float m_new = fmaxf(m_ref, mx);
           const bool need = m_new > m_ref + 8.f;
           if (__any_sync(0xffffffffu, need)) {
