@@ -110,7 +110,7 @@ rope_append_kernel(const RopeAppendParams p, int parts, int part_rows) {
         if (b < c.batch) {
           const int q0 = __ldg(c.cu_q + b), q1 = __ldg(c.cu_q + b + 1), len = __ldg(c.seq_lens + b);
           t = len - (q1 - i);
-          ok = i >= q0 && q1 - q0 <= len && (long long)len <= (long long)c.bt_stride * kPage && (p.rope_dim == 0 || t < p.rope_len);
+          ok = q0 >= 0 && i >= q0 && q1 - q0 <= len && (long long)len <= (long long)c.bt_stride * kPage && (p.rope_dim == 0 || t < p.rope_len);
           if (!ok && lane == 0) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SEQ_LEN, b);
         }
         if (!ok) break;
