@@ -86,6 +86,9 @@ rope_append_kernel(const RopeAppendParams p, int parts, int part_rows) {
   // loaded, which costs a look-up once, 1 us of 253.)
   const int end = min(c.total_q, __ldg(c.cu_q + c.batch));
   const long long items = (long long)end * parts;
+  // a sequence of fewer than no new tokens has no row that would show it
+  for (int b = (int)blockIdx.x * kRopeThreads + (int)threadIdx.x; b < c.batch; b += (int)gridDim.x * kRopeThreads)
+    if (__ldg(c.cu_q + b + 1) < __ldg(c.cu_q + b)) report_error(c.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SEQ_LEN, b);
   for (long long it = warp; it < items; it += warps) {
     const int i = (int)(it / parts), part = (int)(it % parts);
     int b = -1, t = 0, page = -1, mode = 0;

@@ -41,3 +41,18 @@ def test_a_first_row_below_zero(ekv_lib, torch_cuda):
         err, rows, pages, _ = run(ekv_lib, torch_cuda, [0, low, 8], [40, 40 if low == -5 else 3], 8, 2)
         assert err == (ekv_lib.EKV_ERR_DEVICE_CHECK, ekv_lib.EKV_DETAIL_SEQ_LEN)
         assert not rows.any() and not pages
+
+
+@pytest.mark.parametrize("batch,at", [(3, 1), (3, 2), (300, 277), (2000, 1999)])
+def test_fewer_than_no_new_tokens(ekv_lib, torch_cuda, batch, at):
+    """No row belongs to such a sequence; the others are written."""
+    new = [1] * batch
+    new[at] = -1
+    cu = np.cumsum([0] + new).tolist()
+    err, rows, pages, table = run(ekv_lib, torch_cuda, cu, [40] * batch, batch, batch)
+    assert err == (ekv_lib.EKV_ERR_DEVICE_CHECK, ekv_lib.EKV_DETAIL_SEQ_LEN)
+    assert rows[:at - 1].all() and not rows[cu[-1]:].any()
+    assert int(table[at, 2]) not in pages and {int(p) for p in table[:at - 1, 2]} <= pages
+    new[at] = 0                                          # none at all is no error
+    err, rows, pages, _ = run(ekv_lib, torch_cuda, np.cumsum([0] + new).tolist(), [40] * batch, batch, batch)
+    assert err == (0, 0) and rows[:batch - 1].all() and len(pages) == batch - 1
