@@ -393,8 +393,9 @@ ekv_status ekv_append_kv_rope(ekv_ctx* ctx, const void* q, const void* k_new, co
  * The one scale of a uniform E4M3 pool may be any positive finite one. Scales per (page, head), or beside
  * pages of other forms, may be up to 2^40; a larger one fails its check (EKV_DETAIL_SCALE), and one below
  * 2^-44 counts as 2^-44 (the page's values, below 2^-35, leave no trace in fp16). Returns
- * EKV_ERR_CAPACITY when batch > cfg.max_batch, EKV_ERR_UNSUPPORTED when block_table_stride > 131072
- * or a pool has 2^31 or more head rows. Other arguments as
+ * EKV_ERR_CAPACITY when batch > cfg.max_batch, EKV_ERR_UNSUPPORTED when block_table_stride > 131072,
+ * when the K pool has 2^31 or more head rows, or when a V pool that may hold FP16 pages has as many units
+ * of the largest power of two of bytes that divides v_page_stride_bytes and 2 * D. Other arguments as
  * for ekv_paged_decode. Sums are fp32; the weights enter the product with V rounded to fp16 (times
  * the page's scale where scales differ: a row's error is 2^-11 of each term, or 2^-32 of its largest
  * weight times scale for the terms below 2^-21 of that). */

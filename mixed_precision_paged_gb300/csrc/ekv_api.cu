@@ -709,13 +709,14 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
   int unit = 2 * D;
   while (v_page_stride_bytes % unit) unit /= 2;
   const long long places = (long long)num_pages * (v_page_stride_bytes / unit);
-  if ((long long)num_pages * kPage * Hkv > 0x7fffffffLL || places > 0x7fffffffLL) return EKV_ERR_UNSUPPORTED;
+  const bool fp16_pages = vm == kXFP16 || vm == kXMixed;   // (the other forms' value pages need no such map)
+  if ((long long)num_pages * kPage * Hkv > 0x7fffffffLL || (fp16_pages && places > 0x7fffffffLL)) return EKV_ERR_UNSUPPORTED;
   x.v16_mul = (int)(v_page_stride_bytes / unit);
   x.v16_head = 2 * D / unit;
   if (!encode_query_map(&m.q, q, D, Hkv, p.G, total_q, x.e.tile_tokens) ||
       !encode_group_map(&m.k, k_pages, D, Hkv, (unsigned long long)num_pages * kPage * Hkv, 2 * D))
     return EKV_ERR_INVALID_ARG;
-  if ((vm == kXFP16 || vm == kXMixed) && !encode_group_map(&m.v16, v_pages, D, Hkv, places, unit)) return EKV_ERR_INVALID_ARG;
+  if (fp16_pages && !encode_group_map(&m.v16, v_pages, D, Hkv, places, unit)) return EKV_ERR_INVALID_ARG;
   if ((vm == kXE4M3 || vm == kXMixed) && !encode_e4m3_slice_map(&m.v8, v_pages, D, Hkv, num_pages, v_page_stride_bytes))
     return EKV_ERR_INVALID_ARG;
   const cudaError_t e = D == 128 ? launch_extend_tc05_128(m, x, vm, c->split_ctas, st)
