@@ -257,23 +257,22 @@ __device__ __forceinline__ void tld16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 
 // ------------------------------------------------------------------------ plan
-// sum over i < n of floor((a i + b) / m), n, a, b >= 0 (the Euclid-like reduction of the lattice
-// point count under a line; Graham, Knuth, Patashnik, Concrete Mathematics, Sec. 3.5).
-__device__ __forceinline__ int floor_sum(int n, int m, int a, int b) {
-  uint32_t s = 0, un = n, um = m, ua = a, ub = b;      // n <= 2^16, the sum < 2^31 (see the entry point's limit)
-  while (un > 0) {
-    s += un * (un - 1) / 2 * (ua / um) + un * (ub / um);
-    ua %= um;
-    ub %= um;
-    const uint32_t y = ua * un + ub;
-    if (y < um) break;
-    un = y / um;
-    ub = y % um;
-    const uint32_t t = um;
-    um = ua;
-    ua = t;
+// The sum of floor((a i + b) / m) over i < n, a and b >= 0. Multiples of m within a and b are summed at once. What
+// is left (a, b < m) counts the pairs (i, k >= 1) with k m <= a i + b: of all n K of them, K the last term's floor, without
+// those with i < ceil((k m - b) / a), which over k = 1 .. K are a sum of this kind with a and m exchanged.
+// In 32 bits that wrap, as the result is below 2^31 (n <= 2^16 items of up to 2^14 blocks, and K <= n).
+__device__ __forceinline__ int sum_of_floors(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  uint32_t total = 0, sign = 1;                        // sign: 1 or -1
+  while (n > 0) {
+    const uint32_t ra = a % m, rb = b % m, K = (ra * (n - 1) + rb) / m;
+    total += sign * (n * (n - 1) / 2 * (a / m) + n * (b / m) + n * K);
+    sign = 0u - sign;
+    n = K;                                             // ceil((k m - rb) / ra) = floor((m (k - 1) + m - rb + ra - 1) / ra)
+    a = m;
+    b = m - rb + ra - 1;
+    m = ra;
   }
-  return (int)s;
+  return (int)total;
 }
 
 // What an item's start and end (queries, first scores, epilogue) cost, in blocks. ALT, 1 / 2 / 3 / 4: 200 microscaled
@@ -299,10 +298,10 @@ struct Items {
     if (i <= 0) return 0;
     if (ALT) return kItemCost<ALT> + jhi(0) - jlo(0);      // (one item)
     const int full = i == np ? np - 1 : i;            // the last item may be short
-    int s = kItemCost<ALT> * i + floor_sum(full, kTKeys, step, t0 + step + kTKeys - 1);
+    int s = kItemCost<ALT> * i + sum_of_floors(full, kTKeys, step, t0 + step + kTKeys - 1);
     if (i == np) s += jhi(np - 1);
     const int i0 = t0 >= window - 1 ? 0 : min(i, (window - 2 - t0) / step + 1);   // items whose window starts at key 0
-    if (i > i0) s -= floor_sum(i - i0, kTKeys, step, t0 + i0 * step - window + 1);
+    if (i > i0) s -= sum_of_floors(i - i0, kTKeys, step, t0 + i0 * step - window + 1);
     return s;
   }
 };
