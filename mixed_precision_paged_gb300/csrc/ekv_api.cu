@@ -120,7 +120,7 @@ int last_kernel(cudaStream_t st) {
 }
 
 #ifdef EKV_TEST_WAIT_TIMEOUT
-// test build only: decode calls left that run their first ring wait out
+// test build only: calls left (decode, transitions) that run a ring wait out
 int g_inject_timeout_calls = 0;
 #endif
 
@@ -481,6 +481,10 @@ ekv_status transition(ekv_ctx* c, int op, void* v_pages, long long v_page_stride
   p.Hkv = Hkv;
   p.D = D;
   p.err = c->err;
+#ifdef EKV_TEST_WAIT_TIMEOUT
+  p.inject_timeout = g_inject_timeout_calls > 0;
+  if (p.inject_timeout) --g_inject_timeout_calls;
+#endif
   if (launch_transition(p, op, n, c->num_sms, st) != cudaSuccess) return EKV_ERR_CUDA;
   note_launch(st, kAfterTransition);
   return EKV_OK;
@@ -838,8 +842,9 @@ ekv_status ekv_profile_launch_floor(ekv_ctx* c, int reps, void* stream, double* 
 
 #ifdef EKV_TEST_WAIT_TIMEOUT
 // Test build only (libekv_waittest.so; not declared in ekv.h): the next `calls` decode
-// calls (tensor-core consumer) make the first ring wait of CTA 0, warp 0 run out, so a
-// test can check the timeout report and that the context is usable afterwards.
+// calls (tensor-core consumer) make the first ring wait of CTA 0, warp 0 run out, or transitions
+// a wait of CTA 0 for its third page, so a test can check the timeout report and that the context
+// is usable afterwards.
 ekv_status ekv_test_inject_wait_timeout(int calls) {
   if (calls < 0) return EKV_ERR_INVALID_ARG;
   g_inject_timeout_calls = calls;

@@ -283,6 +283,10 @@ transition_kernel(const DemoteParams p, int n, int S) {
   if (tid == 0) s_nonfinite = s_bad[0] = s_bad[1] = 0;
   load_chunk(0);
   __syncthreads();
+#ifdef EKV_TEST_WAIT_TIMEOUT
+  // test build only: 16 bytes more than any copy delivers on the third slot's (or the last one's) first phase
+  if (p.inject_timeout && blockIdx.x == 0 && tid == 0) mbar_expect_tx(&full[min(2, S - 1)], 16);
+#endif
   if (tid == 0)
     for (int k = 0; k < min(S, m); ++k) issue(k);
 
@@ -357,6 +361,7 @@ transition_kernel(const DemoteParams p, int n, int S) {
         report_error(p.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_TIMEOUT, blockIdx.x);
         for (int kk = k; kk < min(k + S, m); ++kk)     // this CTA's copies still in flight
           mbar_wait(&full[kk % S], (uint32_t)(kk / S) & 1u);
+        if (OP == kToMicro) bulk_store_wait();         // and those out of this CTA's buffers
       }
       return;
     }

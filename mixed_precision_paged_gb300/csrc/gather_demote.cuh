@@ -62,6 +62,9 @@ struct DemoteParams {
   int num_slots;          // value slots of v_pages (locations 0 .. 2*num_slots-1)
   int Hkv, D;
   int* err;
+#ifdef EKV_TEST_WAIT_TIMEOUT
+  int inject_timeout;     // test build only: 1 makes a ring wait of CTA 0 run out
+#endif
 };
 
 // K16/V8 cache writer: one new token per sequence.
