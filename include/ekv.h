@@ -392,7 +392,8 @@ ekv_status ekv_append_kv_rope(ekv_ctx* ctx, const void* q, const void* k_new, co
  * queries that see one of its keys (of one KV head for a bad per-(page, head) scale).
  * The one scale of a uniform E4M3 pool may be any positive finite one. Scales per (page, head), or beside
  * pages of other forms, may be up to 2^40; a larger one fails its check (EKV_DETAIL_SCALE), and one below
- * 2^-44 counts as 2^-44 (the page's values, below 2^-35, leave no trace in fp16). Returns
+ * 2^-44 counts as 2^-44 (the page's values, below 2^-35, leave no trace in fp16).
+ * After EKV_DETAIL_TIMEOUT no row of the call's out and lse is to be used. Returns
  * EKV_ERR_CAPACITY when batch > cfg.max_batch, EKV_ERR_UNSUPPORTED when block_table_stride > 131072,
  * when the K pool has 2^31 or more head rows, or when a V pool that may hold FP16 pages has as many units
  * of the largest power of two of bytes that divides v_page_stride_bytes and 2 * D. Other arguments as

@@ -4,7 +4,7 @@ No CMake: each translation unit is compiled in parallel, then linked with the st
 CUDA runtime. The result is written atomically next to this file.
 
 A second library, libekv_waittest.so, is built beside it for the tests only: the
-decode and transition units compiled with EKV_TEST_WAIT_TIMEOUT (a 5 ms bound on the
+decode, transition and attention units compiled with EKV_TEST_WAIT_TIMEOUT (a 5 ms bound on the
 pipeline waits and an entry point that makes one wait run out), linked with the other
 objects of the production build. Nothing but the tests loads it.
 """
@@ -26,7 +26,8 @@ TEST_LIB = os.path.join(HERE, "libekv_waittest.so")
 SOURCES = ["ekv_api.cu", "decode_simt.cu", "decode_mma.cu", "gather_demote.cu", "append_rope.cu", "extend_tc05_d64.cu", "extend_tc05_d128.cu",
            "noalloc.cu", "prefill_mma.cu", "prefill_tc05.cu"]
 # translation units that see the parameters or the wait bound of what a test runs out: rebuilt for the test library
-TEST_SOURCES = ["ekv_api.cu", "decode_simt.cu", "decode_mma.cu", "noalloc.cu", "gather_demote.cu"]
+TEST_SOURCES = ["ekv_api.cu", "decode_simt.cu", "decode_mma.cu", "noalloc.cu", "gather_demote.cu",
+                "extend_tc05_d64.cu", "extend_tc05_d128.cu"]
 TEST_DEFINE = "-DEKV_TEST_WAIT_TIMEOUT"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

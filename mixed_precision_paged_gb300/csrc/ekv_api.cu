@@ -122,6 +122,8 @@ int last_kernel(cudaStream_t st) {
 #ifdef EKV_TEST_WAIT_TIMEOUT
 // test build only: calls left (decode, transitions) that run a ring wait out
 int g_inject_timeout_calls = 0;
+// test build only: the wait that the next call of ekv_extend_attention runs out
+int g_inject_extend_wait = 0;
 #endif
 
 // Partial rows of ekv_extend_attention: two segments of a pair of query tiles per CTA.
@@ -723,6 +725,10 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
   if (fp16_pages && !encode_group_map(&m.v16, v_pages, D, Hkv, places, unit)) return EKV_ERR_INVALID_ARG;
   if ((vm == kXE4M3 || vm == kXMixed) && !encode_e4m3_slice_map(&m.v8, v_pages, D, Hkv, num_pages, v_page_stride_bytes))
     return EKV_ERR_INVALID_ARG;
+#ifdef EKV_TEST_WAIT_TIMEOUT
+  x.inject_timeout = g_inject_extend_wait;
+  g_inject_extend_wait = 0;
+#endif
   const cudaError_t e = D == 128 ? launch_extend_tc05_128(m, x, vm, c->split_ctas, st)
                                  : launch_extend_tc05_64(m, x, vm, c->split_ctas, st);
   if (e != cudaSuccess) return EKV_ERR_CUDA;
@@ -848,6 +854,14 @@ ekv_status ekv_profile_launch_floor(ekv_ctx* c, int reps, void* stream, double* 
 ekv_status ekv_test_inject_wait_timeout(int calls) {
   if (calls < 0) return EKV_ERR_INVALID_ARG;
   g_inject_timeout_calls = calls;
+  return EKV_OK;
+}
+
+// Test build only: the wait (1 .. 9, see extend_tc05_kernel) of CTA 0 that the next call of
+// ekv_extend_attention runs out; 0: none.
+ekv_status ekv_test_inject_extend_timeout(int wait) {
+  if (wait < 0 || wait > 9) return EKV_ERR_INVALID_ARG;
+  g_inject_extend_wait = wait;
   return EKV_OK;
 }
 #endif

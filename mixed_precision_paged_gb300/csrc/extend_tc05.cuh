@@ -79,6 +79,9 @@ struct ExtTcParams {
   const float* scale_ptr;                   // one E4M3 scale for every code (it scales the output), or null
   int nw;                                   // ALT: softmax warps of a stream, for rows below 32 * nw
   int v16_mul, v16_head;                    // FP16 value map: index = page * v16_mul + head * v16_head
+#ifdef EKV_TEST_WAIT_TIMEOUT
+  int inject_timeout;                       // test build only: the wait of CTA 0 that runs out, see the kernel; 0: none
+#endif
 };
 
 template <int D, int VM, bool ALT>
@@ -446,6 +449,13 @@ extend_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     mbar_init(&bars->mma_final, 1);
     bars->abort = 0;
     fence_barrier_init();
+#ifdef EKV_TEST_WAIT_TIMEOUT
+    if (p.inject_timeout && blockIdx.x == 0) {           // test build only: 16 bytes that no copy delivers
+      uint64_t* const waits[] = {&bars->q_full[0], &bars->k_full[1], &bars->v_full[0], &bars->raw_full[1][0], &bars->s_full[0],
+                                 &bars->p_full[0], &bars->pv_done[0], &bars->seg_full[0], &bars->meta_full[1]};
+      mbar_expect_tx(waits[p.inject_timeout - 1], 16);
+    }
+#endif
     tma_prefetch_desc(&tq);
     tma_prefetch_desc(&tk);
     if (VM == kXFP16 || VM == kXMixed) tma_prefetch_desc(&tv16);
