@@ -78,8 +78,9 @@ typedef enum { EKV_MODE_TARGET_FP16 = 0, EKV_MODE_COMPACT_E4M3 = 1, EKV_MODE_BAS
  *                 and 2i+1 in the high half of byte i), then its 16 rows of scale bytes
  *                 ([16][D/32], E8M0: scale = 2^(byte - 127)); value = E2M1(code) * scale, one scale per
  *                 32 values of a token's head row. Scale bytes run from 103 to 140 (2^-24 .. 2^13),
- *                 so that every value is an fp16 value; any other byte is a data error
- *                 (EKV_DETAIL_SCALE) and its 32 values read as zero. Pages of this form are written by
+ *                 so that every value is an fp16 value (but .5 and 1.5 under 103, which read as 0 and
+ *                 2^-23: the calls that write this form make no such codes); any other byte is a data
+ *                 error (EKV_DETAIL_SCALE) and its 32 values read as zero. Pages of this form are written by
  *                 ekv_demote_pages_micro and ekv_append_kv_rope, read by ekv_extend_attention and
  *                 ekv_expand_pages_micro; every other call reports EKV_DETAIL_PAGE_MODE for them. */
                EKV_MODE_MICRO_FP4 = 3 } ekv_page_mode;

@@ -49,7 +49,7 @@ struct ExtendParams {
   int max_q;
   int window;               // 0x7fffffff: none
   float qscale;             // sm_scale * log2(e)
-  int tile_tokens;          // many-row kernel: tokens of a query tile
+  int tile_tokens;          // tokens of a query tile
 };
 
 // The least b in [0, batch] with cu[b + 1] > i (batch: i lies behind the last sequence), found by

@@ -172,7 +172,7 @@ struct Seq {
   int L, n, q0;            // tokens, new tokens, first row of q
 };
 
-// Reads sequence b; false (nothing to attend) when it is empty or fails its checks.
+// Reads sequence b; false when it has no new tokens (see seq_ok for its checks).
 __device__ __forceinline__ bool load_seq(const ExtendParams& e, int b, Seq& s) {
   const CacheView& c = e.c;
   s.q0 = __ldg(c.cu_q + b);

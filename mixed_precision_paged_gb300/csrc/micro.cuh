@@ -4,11 +4,12 @@
 // A block of 32 values of a token's head row shares a scale 2^k; a value is an E2M1 code
 // (sign, 2 exponent bits, 1 fraction bit: 0, .5, 1, 1.5, 2, 3, 4, 6) times it. k is the
 // least that keeps the block's largest magnitude a <= 6 * 2^k, so nothing saturates and
-// the error of a value is at most half a step: 2^k (between 4 and 6 times 2^k), a sixth
-// of a at worst. k stays in [-24, 13]: below, fp16 has no finer values; above, 4 * 2^14 would
-// leave fp16's range (a block whose maximum is over 49152 saturates there). So every
-// code times its scale is an fp16 value, and the product with the attention weights needs
-// no further rounding.
+// the error of a value is at most half a step: 2^k (between 4 and 6 times 2^k), a fifth
+// of a at worst (a = 5 * 2^k). k stays in [-24, 13]: below, fp16 has no finer values; above,
+// 4 * 2^14 would leave fp16's range (a block whose maximum is over 49152 saturates there, 65504 by
+// a quarter). So every code times its scale is an fp16 value, and the product with the attention
+// weights needs no further rounding. (Under 2^-24 the codes .5 and 1.5 are not: fp16 values need none of
+// them, and micro_decode8 rounds foreign ones to 0 and 2^-23.)
 #pragma once
 
 #include <cuda_fp4.h>
@@ -59,7 +60,8 @@ __device__ __forceinline__ __half2 micro_scale_h2(uint32_t byte) {
   return __float2half2_rn(__uint_as_float(byte << 23));
 }
 
-// The values of 8 codes (4 bytes) under a scale, as 4 registers of two fp16 each (exact).
+// The values of 8 codes (4 bytes) under a scale, as 4 registers of two fp16 each (exact, but .5 and
+// 1.5 under 2^-24).
 __device__ __forceinline__ uint4 micro_decode8(uint32_t codes, __half2 scale) {
   uint32_t o[4];
 #pragma unroll
