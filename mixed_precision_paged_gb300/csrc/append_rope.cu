@@ -5,14 +5,15 @@
 // the caller's table, rounded once to fp16. Pure streaming: every input value is read once and
 // every output written once (per token 2 B in and out of each query, key and FP16 value), plus
 // the table row, which all heads of a token share: the floor is those bytes at HBM rate. 65,536 tokens of
-// 32 + 2 x 8 heads of 128, FP16 pages: 253 us, 6.4 TB/s. (Consecutive tokens a warp, which saves look-ups, 259 us.)
+// 32 + 2 x 8 heads of 128, FP16 pages: 252 us, 6.4 TB/s. (Consecutive tokens a warp, which saves look-ups, 259 us.)
 //
 // One warp takes a token, or a share of its heads when tokens are few. A lane owns unit u of a
 // head, 16 values: with half-split pairs the 8-value vectors u and u + rope_dim / 16, so that
 // both ends of 8 pairs meet in one lane; with interleaved pairs, and past rope_dim, the vectors
 // 2u and 2u + 1. Either way its angles are 8u .. 8u + 7, loaded once and used for every head
 // the lane sees. The rows of q, k and v are loaded before the sequence of the token is known (their
-// addresses need the token's index only), so the search and the page lookups hide behind them.
+// addresses need the token's index only, once the end of the last sequence is known), so the search and the
+// page lookups hide behind them.
 #include "extend.cuh"
 #include "micro.cuh"
 
@@ -82,8 +83,7 @@ rope_append_kernel(const RopeAppendParams p, int parts, int part_rows) {
   // below rope_dim / 8, and 2u of the first unit past them is rope_dim / 8
   const bool split = rot && p.rope_style == 0;
   const int v0 = split ? u : 2 * u, v1 = split ? u + p.rope_dim / 16 : 2 * u + 1;
-  // Rows behind the last sequence are not touched: k_new and v_new may end there. (Known before the first row is
-  // loaded, which costs a look-up once, 1 us of 253.)
+  // Rows behind the last sequence are not touched: k_new and v_new may end there.
   const int end = min(c.total_q, __ldg(c.cu_q + c.batch));
   const long long items = (long long)end * parts;
   // a sequence of fewer than no new tokens has no row that would show it

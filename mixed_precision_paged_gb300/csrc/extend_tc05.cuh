@@ -32,8 +32,12 @@
 // threefold, with the GPC's instruction cache at 86% of its request rate. So a role's loop stands once, the
 // makers are driven by block descriptions instead of walking the plan, and unrolling is chosen by measurement.
 // Every wait is bounded; a timeout is reported and every role winds down.
-// Measured, 32/8 heads, D 128: 32 x 1 token behind 8K keys of E4M3 143 us (5.7 TB/s, 6.6 between start and end), 48 x 5
-// over mixed pages 148 us, 4,096 tokens behind 16K of E4M3 840 to 900 us (1,480 to 1,380 TFLOP/s): a step of two tiles
+// Rounding: scores, maxima, sums, partial rows and outputs up to the last step are fp32. The weights go to fp16, which is
+// what the tensor core multiplies by fp16 values (bf16 has three bits less, and TF32 half the rate and twice the bytes of V):
+// up to 2^-11 of a weight, which the result's own rounding to fp16 hides but for a tenth (against 64 bits, relative:
+// 2.0e-4 to 2.2e-4 over the measured cases, 1.9e-4 to 2.1e-4 with fp32 weights). ex2.approx is off by 2^-22.
+// Measured, 32/8 heads, D 128: 32 x 1 token behind 8K keys of E4M3 144 us (5.6 TB/s, 6.6 between start and end), 48 x 5
+// over mixed pages 147 us, 4,096 tokens behind 16K of E4M3 840 to 910 us (1,480 to 1,360 TFLOP/s): a step of two tiles
 // takes 3,300 cycles for 2,176 of MMA, the hand-overs between softmax and products the rest.
 #pragma once
 
