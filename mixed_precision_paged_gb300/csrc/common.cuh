@@ -146,21 +146,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// 1-D bulk copy shared -> global of `bytes` (multiple of 16; both addresses 16-byte aligned) by one
-// thread, in a group of its own; the waits for that thread's copies: until the shared memory of all but
-// the last N has been read, and until all are complete.
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(
-                   reinterpret_cast<uint64_t>(dst)),
-               "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
-template <int N>
-__device__ __forceinline__ void bulk_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void bulk_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // 16-byte asynchronous copy global -> shared through L2 (cp.async, LSU path), and the
 // wait for all of this thread's such copies.
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
