@@ -65,8 +65,8 @@ constexpr float kHeadroom = 7.f;
 // E4M3 scales where they differ by page, or beside pages of other forms: a page beyond kScaleMost fails its check (above
 // 2^25 no code but 0 stands for a value within fp16's range), and below kScaleLeast a scale counts as that (such values,
 // under 448 * 2^-44 < 2^-35, leave no trace in an fp16 output). So 1 / scale is finite, and a weight p' = 2^(score +
-// log2 scale - m) that ex2 flushes, below 2^-126, belongs to a key whose score is 2^42 below another's:
-// up to 2^-126 * 2^(40 + 44) of the sum, however the scales differ.
+// log2 scale - m) that ex2 flushes, below 2^-126, belongs to a key that is at most 2^-126 * 2^(40 + 44) = 2^-42 of the
+// sum, however the scales differ.
 constexpr float kScaleLeast = 1.f / (1ll << 44), kScaleMost = (float)(1ll << 40);
 
 struct ExtTcSplit {                         // an item that crosses CTAs, for the joining kernel
