@@ -369,6 +369,95 @@ ekv_status ekv_append_kv_rope(ekv_ctx* ctx, const void* q, const void* k_new, co
                               const int32_t* seq_lens, const int32_t* cu_q, int batch, int total_q,
                               void* stream);
 
+/* How the angles of rotary positions are made (ekv_rope_table). A pair i of rope_dim / 2 turns by
+ * w_i = theta^(-2 i / rope_dim) / (2 pi) of a whole turn from one position to the next; a model whose context was
+ * stretched divides some or all of the w_i by `factor`:
+ *  PLAIN     none.
+ *  LINEAR    all (positions are interpolated).
+ *  BY_TURNS  by how often a pair turns over the original context, r_i = original_len * w_i: kept where r_i >= fast,
+ *            divided where r_i <= slow, between them w_i (g + (1 - g) / factor) with g = (r_i - slow) / (fast - slow).
+ *  BY_DIMS   the same ends, but between them g falls evenly with i: from 1 at i = max(0, floor(d(fast))) to 0 at
+ *            i = min(rope_dim - 1, ceil(d(slow))), d(r) = rope_dim ln(original_len / (2 pi r)) / (2 ln theta); where
+ *            the second lies not above the first, g is 1 up to the first and 0 behind it. */
+typedef enum { EKV_ROPE_PLAIN = 0, EKV_ROPE_LINEAR = 1, EKV_ROPE_BY_TURNS = 2, EKV_ROPE_BY_DIMS = 3 } ekv_rope_scaling;
+
+typedef struct {
+  double theta;           /* > 1 */
+  int scaling;            /* ekv_rope_scaling */
+  double factor;          /* >= 1; not looked at under PLAIN */
+  double original_len;    /* > 0; BY_TURNS and BY_DIMS alone, like the next two */
+  double slow, fast;      /* 0 < slow < fast */
+  double magnitude;       /* cosines and sines are multiplied by it (1: plain rotations) */
+} ekv_rope_config;
+
+/* Cosines and sines of the positions first .. first + rope_len - 1, as ekv_append_kv_rope and
+ * ekv_append_kv_norm_rope read them:
+ *   table[r][i] = magnitude * cos(2 pi w_i (first + r)),  table[r][rope_dim / 2 + i] = magnitude * sin(...).
+ * Angles are reduced in 64 bits (to 2^-27 of a turn at the last position, 2^-40 at position 2^18), values rounded to
+ * fp32 (a few units of its last place). A table for the writers begins at position 0; rows may be added in pieces.
+ *  cfg          HOST struct, read before the call returns.
+ *  table        fp32 [rope_len][rope_dim], 16-byte aligned (written).
+ *  first        >= 0, first + rope_len at most 2^31 - 1.
+ *  rope_dim     16 .. 128, a multiple of 16. */
+ekv_status ekv_rope_table(ekv_ctx* ctx, const ekv_rope_config* cfg, float* table, int first,
+                          int rope_len, int rope_dim, void* stream);
+
+/* ekv_append_kv_rope for models that normalise queries and keys per head, and for E4M3 pages that
+ * have no scale yet. Before the rotation, every head row x of q and of k_new becomes
+ *   x_d / sqrt(mean_d x_d^2 + norm_eps) * weight_d
+ * (fp32; rounded to fp16 once, after the rotation).
+ *  q_weight     fp16 [D], 16-byte aligned; NULL: queries are not normalised. k_weight likewise.
+ *  norm_eps     positive and finite (not looked at without weights).
+ *  k_out        fp16 [total_q][H_kv][D], contiguous, 16-byte aligned, or NULL: the new keys as they are
+ *               written to their pages, packed for ekv_prompt_attention; may be k_new itself when contiguous.
+ *  v_scales     as before; written where grow_scales is set.
+ *  grow_scales  0: E4M3 pages are written under the scales that they have. 1 (scale_mode
+ *               EKV_SCALE_PER_PAGE_HEAD, v_scales not NULL): the call makes them. With a the largest magnitude of
+ *               the values that it writes to page p for KV head h (infinities count as 65504, NaN for nothing):
+ *               it writes row 0:  v_scales[p * H_kv + h] = fp32_rn(max(a, 2^-24) / 448), whatever was there;
+ *               else:  the scale s becomes s 2^k, k >= 0 the least with fp32_rn(448 s) 2^k >= a, and where k > 0 the codes
+ *               of the rows before the first new one become E4M3_rn(value 2^-k): the same values but for what falls
+ *               below the form's least. New codes are E4M3_rn_satfinite(fp32_rn(v / scale)) under the new scale.
+ *               Pages of other forms are written as without it. No two sequences of a call may write the
+ *               same page.
+ * Where a sequence fails its checks nothing of it is written; where a page or scale fails, q_out and k_out are
+ * written all the same. Everything else as for ekv_append_kv_rope. */
+ekv_status ekv_append_kv_norm_rope(ekv_ctx* ctx, const void* q, const void* k_new, const void* v_new,
+                                   long long q_stride, long long k_stride, long long v_stride,
+                                   const void* q_weight, const void* k_weight, float norm_eps,
+                                   const float* rope_table, int rope_len, int rope_dim, int rope_style,
+                                   void* q_out, void* k_out, void* k_pages, void* v_pages,
+                                   long long v_page_stride_bytes, int num_pages, float* v_scales,
+                                   int scale_mode, int grow_scales, const uint8_t* page_mode,
+                                   int uniform_mode, const int32_t* block_table, int block_table_stride,
+                                   const int32_t* seq_lens, const int32_t* cu_q, int batch, int total_q,
+                                   void* stream);
+
+/* Causal attention of whole prompts over their own keys and values, straight from the rows of the projection: no
+ * pages, no gather. Prompt i has the rows cu_seqlens[i] .. cu_seqlens[i+1] - 1; its query at position s and query head
+ * h_q of KV head h = h_q / G:
+ *   out = sum_k softmax_k(sm_scale * q . K_k) V_k,  lse = log sum_k exp(sm_scale * q . K_k)
+ * over the keys max(0, s - window + 1) <= k <= s of the prompt (window 0: all k <= s). A prompt may have any
+ * number of tokens, none among them. The values of a prompt must be finite: NaN or infinity times the weight 0 of an
+ * earlier query is NaN, as in ekv_prefill_attention (other prompts do not meet them). NaNs of queries and keys reach
+ * the queries that meet them and no others; a query whose scores are all -inf gets zeros and lse -inf.
+ *  q, k, v      fp16 rows of [H_q][D], [H_kv][D], [H_kv][D], `total` of them; q_stride, k_stride, v_stride: values
+ *               between the rows of consecutive tokens (a multiple of 8, at least the row), so that all three may be
+ *               slices of one projection's output. 16-byte aligned.
+ *  cu_seqlens   DEVICE int32 [n + 1], nondecreasing from 0, at most `total`; n at most cfg.max_batch (else
+ *               EKV_ERR_CAPACITY). A prompt that breaks this is reported (EKV_DETAIL_SEQ_LEN), its rows not written.
+ *  total        HOST: rows of q, k, v and out, at most 2^24 (else EKV_ERR_UNSUPPORTED). Rows behind the last prompt are
+ *               left as they are.
+ *  window       keys a query sees, its own among them; 0: no window.
+ *  out          fp16 [total][H_q][D], contiguous, 16-byte aligned; must not overlap q, k or v.
+ *  lse          fp32 [total][H_q], natural logarithm, or NULL.
+ * After EKV_DETAIL_TIMEOUT no row of the call's out and lse is to be used. Sums are fp32; the weights enter the
+ * product with V rounded to fp16 (2^-11 of each term, or 2^-32 of the largest for terms below 2^-21 of that). */
+ekv_status ekv_prompt_attention(ekv_ctx* ctx, const void* q, const void* k, const void* v,
+                                long long q_stride, long long k_stride, long long v_stride,
+                                const int32_t* cu_seqlens, int n, int total, int window, float sm_scale,
+                                void* out, float* lse, void* stream);
+
 /* Attention of new tokens over the paged cache: for a decode step, for the verification of
  * draft tokens, for a prompt chunk behind a cached prefix, and for ragged mixes of them. With b, r, i
  * and t as for ekv_append_kv_rope (which writes the new tokens' rows beforehand), query head h_q

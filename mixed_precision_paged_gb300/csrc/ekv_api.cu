@@ -15,6 +15,8 @@
 #include "micro.cuh"
 #include "pool_maps.h"
 #include "prefill.cuh"
+#include "prompt.cuh"
+#include "rope_table.cuh"
 
 namespace ekv {
 cudaError_t launch_split_simt(const CUtensorMap& tk, const CUtensorMap& t8, const CUtensorMap& t16,
@@ -124,6 +126,8 @@ int last_kernel(cudaStream_t st) {
 int g_inject_timeout_calls = 0;
 // test build only: the wait that the next call of ekv_extend_attention runs out
 int g_inject_extend_wait = 0;
+// test build only: the wait that the next call of ekv_prompt_attention runs out
+int g_inject_prompt_wait = 0;
 #endif
 
 // Partial rows of ekv_extend_attention: two segments of a pair of query tiles per CTA.
@@ -623,15 +627,16 @@ ekv_status cache_view(ekv_ctx* c, CacheView* v, const void* k_pages, const void*
 
 }  // namespace
 
-ekv_status ekv_append_kv_rope(ekv_ctx* c, const void* q, const void* k_new, const void* v_new, long long q_stride,
-                              long long k_stride, long long v_stride, const float* rope_table, int rope_len,
-                              int rope_dim, int rope_style, void* q_out, void* k_pages, void* v_pages,
+namespace {
+
+// Checks and parameters of both rotary writers.
+ekv_status rope_append_params(ekv_ctx* c, RopeAppendParams* p, const void* q, const void* k_new, const void* v_new,
+                              long long q_stride, long long k_stride, long long v_stride, const float* rope_table,
+                              int rope_len, int rope_dim, int rope_style, void* q_out, void* k_pages, void* v_pages,
                               long long v_page_stride_bytes, int num_pages, const float* v_scales, int scale_mode,
                               const uint8_t* page_mode, int uniform_mode, const int32_t* block_table,
                               int block_table_stride, const int32_t* seq_lens, const int32_t* cu_q, int batch,
-                              int total_q, void* stream) {
-  if (!c || batch < 0 || total_q < 0) return EKV_ERR_INVALID_ARG;
-  if (batch == 0 || total_q == 0) return EKV_OK;
+                              int total_q) {
   const int Hq = c->cfg.num_q_heads, Hkv = c->cfg.num_kv_heads, D = c->cfg.head_dim;
   if (!k_new || !v_new || (q && !q_out)) return EKV_ERR_INVALID_ARG;
   if (rope_dim < 0 || rope_dim > D || rope_dim % 16 != 0 || (rope_style != 0 && rope_style != 1)) return EKV_ERR_INVALID_ARG;
@@ -641,27 +646,154 @@ ekv_status ekv_append_kv_rope(ekv_ctx* c, const void* q, const void* k_new, cons
     return EKV_ERR_INVALID_ARG;
   if (q && (!aligned16(q) || !aligned16(q_out))) return EKV_ERR_INVALID_ARG;
   if (!aligned16(k_new) || !aligned16(v_new)) return EKV_ERR_INVALID_ARG;
-  RopeAppendParams p;
-  const ekv_status s = cache_view(c, &p.c, k_pages, v_pages, v_page_stride_bytes, num_pages, v_scales, scale_mode,
+  memset(p, 0, sizeof(*p));
+  const ekv_status s = cache_view(c, &p->c, k_pages, v_pages, v_page_stride_bytes, num_pages, v_scales, scale_mode,
                                   page_mode, uniform_mode, block_table, block_table_stride, seq_lens, cu_q, batch,
                                   total_q);
   if (s != EKV_OK) return s;
-  p.q = static_cast<const __half*>(q);
-  p.k_new = static_cast<const __half*>(k_new);
-  p.v_new = static_cast<const __half*>(v_new);
-  p.q_stride = q_stride;
-  p.k_stride = k_stride;
-  p.v_stride = v_stride;
-  p.rope = rope_table;
-  p.rope_len = rope_len;
-  p.rope_dim = rope_dim;
-  p.rope_style = rope_style;
-  p.q_out = static_cast<__half*>(q_out);
+  p->q = static_cast<const __half*>(q);
+  p->k_new = static_cast<const __half*>(k_new);
+  p->v_new = static_cast<const __half*>(v_new);
+  p->q_stride = q_stride;
+  p->k_stride = k_stride;
+  p->v_stride = v_stride;
+  p->rope = rope_table;
+  p->rope_len = rope_len;
+  p->rope_dim = rope_dim;
+  p->rope_style = rope_style;
+  p->q_out = static_cast<__half*>(q_out);
+  return EKV_OK;
+}
+
+}  // namespace
+
+ekv_status ekv_append_kv_rope(ekv_ctx* c, const void* q, const void* k_new, const void* v_new, long long q_stride,
+                              long long k_stride, long long v_stride, const float* rope_table, int rope_len,
+                              int rope_dim, int rope_style, void* q_out, void* k_pages, void* v_pages,
+                              long long v_page_stride_bytes, int num_pages, const float* v_scales, int scale_mode,
+                              const uint8_t* page_mode, int uniform_mode, const int32_t* block_table,
+                              int block_table_stride, const int32_t* seq_lens, const int32_t* cu_q, int batch,
+                              int total_q, void* stream) {
+  if (!c || batch < 0 || total_q < 0) return EKV_ERR_INVALID_ARG;
+  if (batch == 0 || total_q == 0) return EKV_OK;
+  RopeAppendParams p;
+  const ekv_status s = rope_append_params(c, &p, q, k_new, v_new, q_stride, k_stride, v_stride, rope_table, rope_len,
+                                          rope_dim, rope_style, q_out, k_pages, v_pages, v_page_stride_bytes, num_pages,
+                                          v_scales, scale_mode, page_mode, uniform_mode, block_table,
+                                          block_table_stride, seq_lens, cu_q, batch, total_q);
+  if (s != EKV_OK) return s;
   DeviceGuard g(c->device);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   c->last_stream = st;
   if (launch_rope_append(p, c->num_sms, st) != cudaSuccess) return EKV_ERR_CUDA;
   note_launch(st, kAfterTransition);               // may write any page of a sequence, not its last alone
+  return EKV_OK;
+}
+
+ekv_status ekv_append_kv_norm_rope(ekv_ctx* c, const void* q, const void* k_new, const void* v_new, long long q_stride,
+                                   long long k_stride, long long v_stride, const void* q_weight, const void* k_weight,
+                                   float norm_eps, const float* rope_table, int rope_len, int rope_dim, int rope_style,
+                                   void* q_out, void* k_out, void* k_pages, void* v_pages, long long v_page_stride_bytes,
+                                   int num_pages, float* v_scales, int scale_mode, int grow_scales,
+                                   const uint8_t* page_mode, int uniform_mode, const int32_t* block_table,
+                                   int block_table_stride, const int32_t* seq_lens, const int32_t* cu_q, int batch,
+                                   int total_q, void* stream) {
+  if (!c || batch < 0 || total_q < 0) return EKV_ERR_INVALID_ARG;
+  if (batch == 0 || total_q == 0) return EKV_OK;
+  if (!aligned16(q_weight) || !aligned16(k_weight) || !aligned16(k_out)) return EKV_ERR_INVALID_ARG;
+  if ((q_weight || k_weight) && (!(norm_eps > 0.f) || !isfinite(norm_eps))) return EKV_ERR_INVALID_ARG;
+  if (grow_scales != 0 && grow_scales != 1) return EKV_ERR_INVALID_ARG;
+  if (grow_scales && (!v_scales || scale_mode != EKV_SCALE_PER_PAGE_HEAD)) return EKV_ERR_INVALID_ARG;
+  RopeAppendParams p;
+  const ekv_status s = rope_append_params(c, &p, q, k_new, v_new, q_stride, k_stride, v_stride, rope_table, rope_len,
+                                          rope_dim, rope_style, q_out, k_pages, v_pages, v_page_stride_bytes, num_pages,
+                                          v_scales, scale_mode, page_mode, uniform_mode, block_table,
+                                          block_table_stride, seq_lens, cu_q, batch, total_q);
+  if (s != EKV_OK) return s;
+  p.q_weight = static_cast<const __half*>(q_weight);
+  p.k_weight = static_cast<const __half*>(k_weight);
+  p.eps = norm_eps;
+  p.k_out = static_cast<__half*>(k_out);
+  p.grow = grow_scales;
+  DeviceGuard g(c->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  c->last_stream = st;
+  if (launch_norm_append(p, c->num_sms, st) != cudaSuccess) return EKV_ERR_CUDA;
+  note_launch(st, kAfterTransition);               // may write any page of a sequence, and scales
+  return EKV_OK;
+}
+
+ekv_status ekv_rope_table(ekv_ctx* c, const ekv_rope_config* cfg, float* table, int first, int rope_len, int rope_dim,
+                          void* stream) {
+  if (!c || !cfg || first < 0 || rope_len < 0 || first > 0x7fffffff - rope_len) return EKV_ERR_INVALID_ARG;
+  if (rope_dim < 16 || rope_dim > 2 * kMaxRopePairs || rope_dim % 16 != 0) return EKV_ERR_INVALID_ARG;
+  if (!(cfg->theta > 1.0) || !isfinite(cfg->theta) || !isfinite(cfg->magnitude)) return EKV_ERR_INVALID_ARG;
+  if (cfg->scaling < EKV_ROPE_PLAIN || cfg->scaling > EKV_ROPE_BY_DIMS) return EKV_ERR_INVALID_ARG;
+  if (cfg->scaling != EKV_ROPE_PLAIN && (!(cfg->factor >= 1.0) || !isfinite(cfg->factor))) return EKV_ERR_INVALID_ARG;
+  if (cfg->scaling >= EKV_ROPE_BY_TURNS &&
+      (!(cfg->original_len > 0.0) || !isfinite(cfg->original_len) || !(cfg->slow > 0.0) || !(cfg->fast > cfg->slow) ||
+       !isfinite(cfg->fast)))
+    return EKV_ERR_INVALID_ARG;
+  if (rope_len == 0) return EKV_OK;
+  if (!table || !aligned16(table)) return EKV_ERR_INVALID_ARG;
+  RopeTableParams p;
+  p.table = table;
+  p.first = first;
+  p.rows = rope_len;
+  p.half = rope_dim / 2;
+  p.magnitude = (float)cfg->magnitude;
+  rope_turns(p.turns, rope_dim, *cfg);
+  DeviceGuard g(c->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  c->last_stream = st;
+  if (launch_rope_table(p, c->num_sms, st) != cudaSuccess) return EKV_ERR_CUDA;
+  note_launch(st, kAfterReader);                   // (no call reads a table before its grid-dependency wait)
+  return EKV_OK;
+}
+
+ekv_status ekv_prompt_attention(ekv_ctx* c, const void* q, const void* k, const void* v, long long q_stride,
+                                long long k_stride, long long v_stride, const int32_t* cu_seqlens, int n, int total,
+                                int window, float sm_scale, void* out, float* lse, void* stream) {
+  if (!c || n < 0 || total < 0 || window < 0) return EKV_ERR_INVALID_ARG;
+  if (n > c->cfg.max_batch) return EKV_ERR_CAPACITY;
+  if (n == 0 || total == 0) return EKV_OK;
+  const int Hq = c->cfg.num_q_heads, Hkv = c->cfg.num_kv_heads, D = c->cfg.head_dim;
+  if (!q || !k || !v || !cu_seqlens || !out) return EKV_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return EKV_ERR_INVALID_ARG;
+  if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return EKV_ERR_INVALID_ARG;
+  if (q_stride < (long long)Hq * D || (q_stride & 7) || k_stride < (long long)Hkv * D || (k_stride & 7) ||
+      v_stride < (long long)Hkv * D || (v_stride & 7))
+    return EKV_ERR_INVALID_ARG;
+  if (total > kMaxPromptRows) return EKV_ERR_UNSUPPORTED;
+  if (!(sm_scale > 0.f) || !isfinite(sm_scale)) sm_scale = 1.0f / sqrtf((float)D);
+  PromptParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __half*>(q);
+  p.k = static_cast<const __half*>(k);
+  p.v = static_cast<const __half*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.cu = cu_seqlens;
+  p.out = static_cast<__half*>(out);
+  p.lse = lse;
+  p.n = n;
+  p.total = total;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.window = window > 0 ? window : 0x7fffffff;
+  p.qscale = sm_scale * 1.4426950408889634f;
+  p.err = c->err;
+#ifdef EKV_TEST_WAIT_TIMEOUT
+  p.inject_timeout = g_inject_prompt_wait;
+  g_inject_prompt_wait = 0;
+#endif
+  DeviceGuard g(c->device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  c->last_stream = st;
+  if (launch_prompt_tc05(p, D, c->num_sms, st) != cudaSuccess) return EKV_ERR_CUDA;
+  note_launch(st, kAfterReader);
   return EKV_OK;
 }
 
@@ -719,7 +851,7 @@ ekv_status ekv_extend_attention(ekv_ctx* c, const void* q, const void* k_pages, 
   if ((long long)num_pages * kPage * Hkv > 0x7fffffffLL || (fp16_pages && places > 0x7fffffffLL)) return EKV_ERR_UNSUPPORTED;
   x.v16_mul = (int)(v_page_stride_bytes / unit);
   x.v16_head = 2 * D / unit;
-  if (!encode_query_map(&m.q, q, D, Hkv, p.G, total_q, x.e.tile_tokens) ||
+  if (!encode_query_map(&m.q, q, D, Hkv, p.G, total_q, x.e.tile_tokens, (long long)Hq * D) ||
       !encode_group_map(&m.k, k_pages, D, Hkv, (unsigned long long)num_pages * kPage * Hkv, 2 * D))
     return EKV_ERR_INVALID_ARG;
   if (fp16_pages && !encode_group_map(&m.v16, v_pages, D, Hkv, places, unit)) return EKV_ERR_INVALID_ARG;
@@ -862,6 +994,14 @@ ekv_status ekv_test_inject_wait_timeout(int calls) {
 ekv_status ekv_test_inject_extend_timeout(int wait) {
   if (wait < 0 || wait > 9) return EKV_ERR_INVALID_ARG;
   g_inject_extend_wait = wait;
+  return EKV_OK;
+}
+
+// Test build only: the wait (1 .. 10, see prompt_tc05_kernel) of CTA 0 that the next call of
+// ekv_prompt_attention runs out; 0: none.
+ekv_status ekv_test_inject_prompt_timeout(int wait) {
+  if (wait < 0 || wait > 10) return EKV_ERR_INVALID_ARG;
+  g_inject_prompt_wait = wait;
   return EKV_OK;
 }
 #endif

@@ -35,6 +35,12 @@ struct RopeAppendParams {
   const float* rope;        // [rope_len][rope_dim]
   int rope_len, rope_dim, rope_style;
   __half* q_out;
+  // norm_append_kernel alone
+  const __half* q_weight;   // [D]; null: queries are not normalised
+  const __half* k_weight;   // the same of keys
+  float eps;
+  __half* k_out;            // [total_q][Hkv][D] or null
+  int grow;                 // 1: the call makes the scales of E4M3 pages
 };
 
 // Pages of a sequence at most (2^21 tokens): keeps the block counts of the plan in 32 bits.
@@ -70,5 +76,6 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t* cu, int batch, 
 }
 
 cudaError_t launch_rope_append(const RopeAppendParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_append(const RopeAppendParams& p, int num_sms, cudaStream_t st);
 
 }  // namespace ekv

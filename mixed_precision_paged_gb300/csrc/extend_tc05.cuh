@@ -1462,13 +1462,13 @@ inline bool encode_group_map(CUtensorMap* tm, const void* base, int D, int Hkv, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Query rows: 5-D view (d mod 64, g, d / 64, KV head, token) of q [T][Hq][D]; the box {64, G, 1, 1, TT}
-// lands TT * G rows of 128 B, row = token * G + g. Tokens past T read as zeros.
-inline bool encode_query_map(CUtensorMap* tm, const void* q, int D, int Hkv, int G, int T, int tile_tokens) {
+// Query rows: 5-D view (d mod 64, g, d / 64, KV head, token) of q [T][Hq][D], `stride` values between tokens; the
+// box {64, G, 1, 1, TT} lands TT * G rows of 128 B, row = token * G + g. Tokens past T read as zeros.
+inline bool encode_query_map(CUtensorMap* tm, const void* q, int D, int Hkv, int G, int T, int tile_tokens, long long stride) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[5] = {64, (cuuint64_t)G, (cuuint64_t)(D / 64), (cuuint64_t)Hkv, (cuuint64_t)T};
-  cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)G * D * 2, (cuuint64_t)Hkv * G * D * 2};
+  cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)G * D * 2, (cuuint64_t)stride * 2};
   cuuint32_t box[5] = {64, (cuuint32_t)G, 1, 1, (cuuint32_t)tile_tokens};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(q), dims, strides, box, estr,

@@ -1,0 +1,588 @@
+// prompt_tc05.cu -- causal attention of packed prompts, straight from the rows of the projection, on the
+// fifth-generation tensor cores.
+//
+// For a prompt of rows row0 .. row0 + L - 1, query position s and query head hq of KV head h:
+//   out = sum_k softmax_k(sm_scale q_s . k_k) v_k over max(0, s - window + 1) <= k <= s.
+// 4 D FLOP a visible pair and head against 2 D bytes of a row of q, k, v or out: prompts of some hundred tokens
+// are bound by HBM, longer ones by the tensor pipe, with the exponentials next.
+//   * tiles: 128 query rows (the MMA's M), `heads` query heads of a KV head times 128 / heads tokens, row = token *
+//     heads + head. heads = 1 takes 128 tokens of one head; heads = G fills a tile with short prompts.
+//   * items: two tiles that follow each other and share every key block of 128 tokens, one tile's softmax under the
+//     other's products. Persistent CTAs, one a SM.
+//   * plan: the items of all prompts, heaviest first. An item's weight goes by its query block, so the prompts are
+//     sorted by their number of query blocks (in shared memory, by every CTA for itself), and item x of the list is
+//     found by a search over the places where a prompt joins in. The list is dealt in a snake, which balances a sorted
+//     list about as well as a queue does, without one. Empty blocks of short prompts are not in it.
+//   * roles: warp 0 loads queries, keys and values (TMA); warp 1 issues the MMAs; warp 2 owns tensor memory; warp 3
+//     zeroes the value rows past a prompt's end in its last block, so that weight 0 never meets what the next prompt
+//     (or nobody) wrote there; warps 4-7 and 8-11 are the softmax of tile 0 and 1, a thread per row.
+// Tensor memory of tile t: S and P at 256 t, O at 256 t + 128. The order of the MMAs and the lazily moved maximum are those
+// of the prefill (prefill_tc05.cu); the reference of a row lies 2^kHeadroom below its maximum, so that fp16 weights keep
+// their bits down to 2^-21 of the largest (extend_tc05.cuh). Every wait is bounded; a timeout is reported and
+// every role winds down.
+#include "extend_tc05.cuh"
+#include "prompt.cuh"
+
+namespace ekv {
+
+namespace {
+
+using namespace xt;
+
+constexpr int kPThreads = 384;
+
+template <int D>
+struct PT {
+  static constexpr int NB = D / 64;                    // 64-value slabs of a row
+  static constexpr int QB = kTRows * D * 2;            // bytes of a query tile
+  static constexpr int IB = kTKeys * D * 2;            // bytes of a K or V block
+  static constexpr int NS = D == 128 ? 4 : 8;          // ring stages
+};
+
+template <int NS>
+struct PromptBars {
+  uint64_t q_full[2];            // [tile]: the tile's query rows of its next item landed
+  uint64_t q_empty[2];           // [tile]: an item's last S has read the tile's query rows
+  uint64_t kv_full[NS];          // a block landed (a prompt's last value block: and its end zeroed)
+  uint64_t kv_empty[NS];         // the MMAs reading the stage have completed
+  uint64_t v_raw[NS];            // a prompt's last value block landed
+  uint64_t s_full[2];            // [tile]: S of the next block written
+  uint64_t p_full[2];            // [tile]: P written, S read (one arrival per softmax warp)
+  uint64_t pv_done[2];           // [tile]: an item's last O += P V completed
+  uint64_t o_free[2];            // [tile]: an item's O read out (one arrival per softmax warp)
+  uint64_t mma_final;            // every MMA issued has completed
+  int red[kPThreads / 32];
+  uint32_t tmem_base;
+  int abort;
+};
+
+// The plan, in shared memory: prompts by falling number of query blocks, (blocks << 12) | (4095 - prompt), and
+// first[k - 1], the place in the list of (prompt, query block) pairs from which on k prompts take part.
+struct Plan {
+  uint32_t key[kMaxBatch];
+  int first[kMaxBatch];
+};
+
+template <int D>
+constexpr int prompt_smem_bytes() {
+  return 2 * PT<D>::QB + PT<D>::NS * PT<D>::IB + (int)sizeof(Plan) + (int)sizeof(PromptBars<PT<D>::NS>);
+}
+
+// Sorts the prompts and fills `first`; returns the number of (prompt, query block) pairs. All threads.
+__device__ __forceinline__ int make_plan(const PromptParams& p, Plan& pl, int* red) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int step = 2 * p.tile_tokens;
+  int n2 = 1;
+  while (n2 < p.n) n2 <<= 1;
+  for (int i = tid; i < n2; i += kPThreads) {
+    uint32_t key = 0;
+    if (i < p.n) {
+      const int a = __ldg(p.cu + i), b = __ldg(p.cu + i + 1);
+      const bool good = a >= 0 && b >= a && b <= p.total;
+      if (!good && blockIdx.x == 0) report_error(p.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SEQ_LEN, i);
+      const int blocks = good ? (b - a + step - 1) / step : 0;
+      key = ((uint32_t)blocks << 12) | (uint32_t)(kMaxBatch - 1 - i);
+    }
+    pl.key[i] = key;
+  }
+  __syncthreads();
+  for (int size = 2; size <= n2; size <<= 1)               // bitonic, falling
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      for (int x = tid; x < n2 / 2; x += kPThreads) {
+        const int i = ((x & ~(d - 1)) << 1) | (x & (d - 1)), j = i | d;
+        const uint32_t a = pl.key[i], b = pl.key[j];
+        if ((a < b) == ((i & size) == 0)) {
+          pl.key[i] = b;
+          pl.key[j] = a;
+        }
+      }
+      __syncthreads();
+    }
+  // first[k - 1] = (blocks of the k first prompts) - k * (blocks of the k-th)
+  const int each = (p.n + kPThreads - 1) / kPThreads, k0 = tid * each, k1 = min(k0 + each, p.n);
+  int sum = 0;
+  for (int k = k0; k < k1; ++k) sum += (int)(pl.key[k] >> 12);
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) red[warp] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int w = 0; w < kPThreads / 32; ++w) {
+    if (w < warp) before += red[w];
+    total += red[w];
+  }
+  before += incl - sum;
+  for (int k = k0; k < k1; ++k) {
+    const int blocks = (int)(pl.key[k] >> 12);
+    before += blocks;
+    pl.first[k] = before - (k + 1) * blocks;
+  }
+  __syncthreads();
+  return total;
+}
+
+// One work item: two tiles of one prompt and `heads` query heads.
+struct PromptItem {
+  int row0, L, hg;         // the prompt's first row, its tokens; the group of heads
+  int q0[2];               // [tile] first token
+  int ja[2], jb[2];        // [tile] key blocks [ja, jb); none where the tile has no token
+  int jlo, jhi;            // of either
+};
+
+// Item w of the list (the whole warp).
+__device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, const Plan& pl, int w) {
+  const int lane = threadIdx.x & 31, groups = p.Hq / p.heads;
+  const int x = w / groups;
+  PromptItem it;
+  it.hg = w % groups;
+  int lo = 0, n = p.n;                                     // the last k with first[k] <= x, of n from lo on
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const bool in = lane * step < n && pl.first[lo + lane * step] <= x;
+    const int last = __popc(__ballot_sync(0xffffffffu, in)) - 1;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  const int off = x - pl.first[lo];
+  const int qb = (int)(pl.key[lo] >> 12) - 1 - off / (lo + 1);
+  const int i = kMaxBatch - 1 - (int)(pl.key[off % (lo + 1)] & 4095u);
+  it.row0 = __ldg(p.cu + i);
+  it.L = __ldg(p.cu + i + 1) - it.row0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    it.q0[t] = (2 * qb + t) * p.tile_tokens;
+    const bool active = it.q0[t] < it.L;
+    it.ja[t] = active && it.q0[t] >= p.window ? (it.q0[t] - p.window + 1) / kTKeys : 0;
+    it.jb[t] = active ? (min(it.q0[t] + p.tile_tokens, it.L) + kTKeys - 1) / kTKeys : 0;
+  }
+  it.jlo = it.ja[0];
+  it.jhi = max(it.jb[0], it.jb[1]);
+  return it;
+}
+
+// The r-th item of this CTA: dealt in rounds of gridDim.x, alternately forwards and backwards.
+__device__ __forceinline__ int dealt(int r) {
+  const int g = (int)gridDim.x, c = (int)blockIdx.x;
+  return r * g + ((r & 1) ? g - 1 - c : c);
+}
+
+// The S row of one key block, read from tensor memory into registers once; MASK: keys outside lc + 1 .. lc + seen
+// become -inf. Returns the row's maximum (raw score).
+template <bool MASK>
+__device__ __forceinline__ float prompt_row(uint32_t t_s, int lc, uint32_t seen, uint32_t (&a)[4][32]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tc05::ld32(t_s + 32 * c, a[c]);
+  tc05::wait_ld();
+  float mg[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (MASK) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if ((uint32_t)(32 * c + e - lc - 1) >= seen) a[c][e] = __float_as_uint(-INFINITY);
+    }
+    float m8[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t* y = a[c] + 8 * g;
+      m8[g] = fmaxf(max3(max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2])), __uint_as_float(y[3]),
+                         __uint_as_float(y[4])),
+                    max3(__uint_as_float(y[5]), __uint_as_float(y[6]), __uint_as_float(y[7])));
+    }
+    mg[c] = max3(m8[0], m8[1], fmaxf(m8[2], m8[3]));
+  }
+  return max3(mg[0], mg[1], fmaxf(mg[2], mg[3]));
+}
+
+// P = 2^(S qs + nm) of the row in registers, as fp16 pairs over the first 64 columns of S (read by then);
+// returns the sum of the fp32 exponentials.
+__device__ __forceinline__ float prompt_weights(uint32_t t_s, float qs, float nm, uint32_t (&a)[4][32]) {
+  float la[4] = {0.f, 0.f, 0.f, 0.f}, lb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float a0, a1;
+      ffma2(a0, a1, __uint_as_float(a[c][2 * e]), __uint_as_float(a[c][2 * e + 1]), qs, nm);
+      const float p0 = ex2(a0), p1 = ex2(a1);
+      fadd2(la[e & 3], lb[e & 3], p0, p1);
+      a[c][e] = pack2(p0, p1);                             // (a[c][2 e] and a[c][2 e + 1] are read)
+    }
+    tst16(t_s + 16 * c, &a[c][0]);
+  }
+  fadd2(la[0], lb[0], la[2], lb[2]);
+  fadd2(la[1], lb[1], la[3], lb[3]);
+  return (la[0] + la[1]) + (lb[0] + lb[1]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPThreads, 1)
+prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv, const PromptParams p) {
+  using C = PT<D>;
+  constexpr int NS = C::NS, NB = C::NB;
+  extern __shared__ __align__(1024) uint8_t sm_1k[];
+  uint8_t* sQ = sm_1k;                                     // [2][NB][128 rows][128 B]
+  uint8_t* sKV = sQ + 2 * C::QB;                           // [NS][NB][128 rows][128 B]
+  Plan& pl = *reinterpret_cast<Plan*>(sKV + NS * C::IB);
+  PromptBars<NS>* bars = reinterpret_cast<PromptBars<NS>*>(sKV + NS * C::IB + sizeof(Plan));
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (smem_u32(sm_1k) & 1023u) {                           // the swizzled layouts would not hold
+    if (threadIdx.x == 0) report_error(p.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_TIMEOUT, -2);
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->q_full[t], 1);
+      mbar_init(&bars->q_empty[t], 1);
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t], kTRows / 32);
+      mbar_init(&bars->pv_done[t], 1);
+      mbar_init(&bars->o_free[t], kTRows / 32);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&bars->kv_full[s], 1);
+      mbar_init(&bars->kv_empty[s], 1);
+      mbar_init(&bars->v_raw[s], 1);
+    }
+    mbar_init(&bars->mma_final, 1);
+    bars->abort = 0;
+    fence_barrier_init();
+#ifdef EKV_TEST_WAIT_TIMEOUT
+    if (p.inject_timeout && blockIdx.x == 0) {             // test build only: 16 bytes that no copy delivers
+      uint64_t* const waits[] = {&bars->q_full[0], &bars->kv_full[0], &bars->kv_full[1], &bars->v_raw[1], &bars->s_full[0],
+                                 &bars->p_full[0], &bars->pv_done[0], &bars->kv_empty[0], &bars->q_empty[0],
+                                 &bars->o_free[0]};
+      mbar_expect_tx(waits[p.inject_timeout - 1], 16);
+    }
+#endif
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (warp == 2) tc05::tmem_alloc(&bars->tmem_base, 512);
+  const int W = make_plan(p, pl, bars->red) * (p.Hq / p.heads);   // items
+  tc05::fence_before_sync();
+  __syncthreads();
+  tc05::fence_after_sync();
+  const uint32_t tbase = bars->tmem_base;
+  const int TT = p.tile_tokens;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    int stage = 0, u = 0;
+    uint32_t phase = 0, edges = 0;                         // edges: bit per stage whose last copy went to v_raw
+    uint32_t raw_ph = 0;                                   // bit per stage: parity of v_raw's last phase begun
+    uint32_t ql[2] = {0u, 0u};                             // query tiles loaded, per tile
+    bool ok = true;
+    for (int r = 0; ok && dealt(r) < W; ++r) {
+      const PromptItem it = prompt_item(p, pl, dealt(r));
+      const int h = it.hg * p.heads / p.G;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || it.ja[t] >= it.jb[t]) continue;
+        if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
+        if (!ok) continue;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(TT * p.heads * D * 2));
+          for (int s = 0; s < NB; ++s)
+            tma_load_5d(sQ + t * C::QB + s * kTRows * 128, &tq, 0, 0, s, it.hg, it.row0 + it.q0[t], &bars->q_full[t]);
+        }
+        ++ql[t];
+      }
+      const bool edge = it.L < it.jhi * kTKeys;            // the last block reaches past the prompt
+      for (int j = it.jlo; ok && j < it.jhi; ++j) {
+        for (int is_v = 0; is_v < 2; ++is_v) {
+          if (u >= NS) ok = wait_warp(&bars->kv_empty[stage], phase ^ 1u, abort);
+          if (!ok) break;
+          const bool raw = is_v && edge && j == it.jhi - 1;
+          uint64_t* bar = raw ? &bars->v_raw[stage] : &bars->kv_full[stage];
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, C::IB);
+            tma_load_4d(sKV + stage * C::IB, is_v ? &tv : &tk, 0, it.row0 + j * kTKeys, 0, h, bar);
+          }
+          edges = raw ? edges | 1u << stage : edges & ~(1u << stage);
+          if (raw) raw_ph ^= 1u << stage;
+          ++u;
+          if (++stage == NS) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) give_up(p.err, abort);
+    // the copies still in flight land before the CTA can exit
+    for (int v = u > NS ? u - NS : 0; v < u; ++v) {
+      const int s = v % NS;
+      if ((edges >> s) & 1u) drain(&bars->v_raw[s], ((raw_ph >> s) & 1u) ^ 1u);
+      else drain(&bars->kv_full[s], (uint32_t)(v / NS) & 1u);
+    }
+    for (int t = 0; t < 2; ++t)
+      if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
+  } else if (warp == 3) {
+    // ------------------------------------- value rows past a prompt's end: zeros
+    int u = 0;                                             // blocks up to the item's end
+    uint32_t raw_ph = 0;
+    bool ok = true;
+    for (int r = 0; ok && dealt(r) < W; ++r) {
+      const PromptItem it = prompt_item(p, pl, dealt(r));
+      u += 2 * (it.jhi - it.jlo);
+      const int zr = it.L - (it.jhi - 1) * kTKeys;         // rows >= zr of the last block
+      if (zr >= kTKeys) continue;
+      const int s = (u - 1) % NS;
+      ok = wait_warp(&bars->v_raw[s], (raw_ph >> s) & 1u, abort);
+      raw_ph ^= 1u << s;
+      if (!ok) break;
+      uint8_t* dst = sKV + s * C::IB;
+      const int per_slab = (kTKeys - zr) * 8;              // 16-byte chunks past the prompt
+      for (int e = lane; e < per_slab * NB; e += 32) {
+        const int slab = e / per_slab, rem = e % per_slab;
+        *reinterpret_cast<uint4*>(dst + slab * kTKeys * 128 + (zr + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->kv_full[s]);
+    }
+    if (!ok && lane == 0) give_up(p.err, abort);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA issuer
+    // The whole warp runs the control flow and computes the descriptors; one elected lane issues.
+    constexpr uint32_t idS = tc05::idesc_f16_f32(kTRows, kTKeys, false);
+    constexpr uint32_t idO = tc05::idesc_f16_f32(kTRows, D, true);
+    constexpr uint32_t HI = tc05::sdesc_hi(1024);          // 8-row groups 1024 B apart
+    const uint32_t q_lo = tc05::sdesc_lo(smem_u32(sQ), 16);
+    const uint32_t k_lo = tc05::sdesc_lo(smem_u32(sKV), 16);
+    const uint32_t v_lo = tc05::sdesc_lo(smem_u32(sKV), kTKeys * 128);
+    int ks = 0, vs = 1;                                    // ring cursors of the K blocks and the V blocks
+    uint32_t kp = 0, vp = 0;
+    uint32_t qc[2] = {0u, 0u}, pc[2] = {0u, 0u}, oc[2] = {0u, 0u};   // phases taken: q_full, p_full; items with an O
+    auto adv2 = [&](int& s, uint32_t& ph) {
+      s += 2;
+      if (s >= NS) {
+        s -= NS;
+        ph ^= 1u;
+      }
+    };
+    auto commit_one = [&](uint64_t* bar) {
+      if (tc05::elect_one()) tc05::commit(bar);
+      __syncwarp();
+    };
+    bool ok = true;
+    for (int r = 0; ok && dealt(r) < W; ++r) {
+      const PromptItem it = prompt_item(p, pl, dealt(r));
+      // S_t of block j, over the P_t before it (read by an O_t += P_t V issued earlier: one thread's MMAs run in order)
+      auto issue_s = [&](int t, int j) {
+        if (j == it.ja[t]) {
+          ok = wait_warp(&bars->q_full[t], qc[t] & 1u, abort);
+          ++qc[t];
+          if (!ok) return;
+        }
+        tc05::fence_after_sync();
+        const uint32_t qa = q_lo + t * (C::QB >> 4), ka = k_lo + ks * (C::IB >> 4);
+        if (tc05::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc05::mma_ss(tbase + t * 256, tc05::sdesc_join(qa + (((k >> 2) * (kTRows * 128) + (k & 3) * 32) >> 4), HI),
+                         tc05::sdesc_join(ka + (((k >> 2) * (kTKeys * 128) + (k & 3) * 32) >> 4), HI), idS, k > 0);
+          tc05::commit(&bars->s_full[t]);
+          if (j + 1 == it.jb[t]) tc05::commit(&bars->q_empty[t]);
+        }
+        __syncwarp();
+      };
+      ok = wait_warp(&bars->kv_full[ks], kp, abort);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (ok && it.ja[t] == it.jlo && it.jlo < it.jb[t]) issue_s(t, it.jlo);
+      if (!ok) break;
+      commit_one(&bars->kv_empty[ks]);
+      adv2(ks, kp);
+      for (int j = it.jlo; ok && j < it.jhi; ++j) {
+        ok = wait_warp(&bars->kv_full[vs], vp, abort);
+        if (!ok) break;
+        const uint32_t va = v_lo + vs * (C::IB >> 4);
+        bool k_ready = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (ok && j >= it.ja[t] && j < it.jb[t]) {
+            // O_t += P_t V_j once the softmax has written P (and, for an item's first block, once the
+            // previous item's O_t has been read out)
+            ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
+            ++pc[t];
+            if (ok && j == it.ja[t] && oc[t] > 0) ok = wait_warp(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
+            if (ok) {
+              tc05::fence_after_sync();
+              const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
+              const bool acc0 = j > it.ja[t];
+              if (tc05::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kTKeys / 16; ++k)
+                  tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2048 >> 4), HI), idO, acc0 || k > 0);
+                if (j + 1 == it.jb[t]) tc05::commit(&bars->pv_done[t]);
+              }
+              __syncwarp();
+            }
+          }
+          if (ok && j + 1 >= it.ja[t] && j + 1 < it.jb[t]) {   // S_t of the next block, right behind
+            if (!k_ready) ok = wait_warp(&bars->kv_full[ks], kp, abort);
+            k_ready = true;
+            if (ok) issue_s(t, j + 1);
+          }
+        }
+        if (!ok) break;
+        commit_one(&bars->kv_empty[vs]);
+        adv2(vs, vp);
+        if (j + 1 < it.jhi) {
+          commit_one(&bars->kv_empty[ks]);
+          adv2(ks, kp);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (it.ja[t] < it.jb[t]) ++oc[t];
+    }
+    if (!ok && lane == 0) give_up(p.err, abort);
+    commit_one(&bars->mma_final);
+    if (lane == 0) drain(&bars->mma_final, 0);
+  } else if (warp >= 4) {
+    // ------------------------------------------------------- softmax, tile t
+    const int t = (warp - 4) >> 2, r = threadIdx.x - 128 - t * kTRows;
+    const uint32_t lanebase = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float qs = p.qscale;
+    const uint32_t t_s = tbase + t * 256 + lanebase, t_o = tbase + t * 256 + 128 + lanebase;
+    const int tok_t = r / p.heads;                         // this row's token within the tile
+    uint32_t sc = 0, pvc = 0;                              // phases taken: s_full, pv_done
+    bool ok = true;
+    for (int ri = 0; ok && dealt(ri) < W; ++ri) {
+      const PromptItem it = prompt_item(p, pl, dealt(ri));
+      const int ja = t ? it.ja[1] : it.ja[0], jb = t ? it.jb[1] : it.jb[0], q0 = t ? it.q0[1] : it.q0[0];
+      if (ja >= jb) continue;
+      const int pos = q0 + tok_t;
+      const int lo = max(pos - p.window, -1);              // the row sees keys lo + 1 .. pos
+      const int all_lo = min(q0 + TT, it.L) - 1 - p.window;   // every row sees keys above this and up to q0
+      const bool valid = tok_t < TT && pos < it.L;
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = ja; j < jb; ++j) {
+        // S of block j is there; O += P V of block j - 1 has completed too (its commit came first)
+        ok = wait_warp(&bars->s_full[t], sc & 1u, abort);
+        ++sc;
+        if (!ok) break;
+        tc05::fence_after_sync();
+        const int k0 = j * kTKeys;
+        uint32_t sv[4][32];
+        float mx = k0 + kTKeys - 1 > q0 || k0 <= all_lo ? prompt_row<true>(t_s, lo - k0, (uint32_t)(pos - lo), sv)
+                                                        : prompt_row<false>(t_s, 0, 0u, sv);
+        mx = fmaf(mx, qs, -kHeadroom);
+        const float m_new = fmaxf(m_ref, mx);
+        const bool need = m_new > m_ref + 8.f;
+        if (__any_sync(0xffffffffu, need)) {
+          const float alpha = need ? ex2(m_ref - m_new) : 1.f;
+          if (j > ja) {
+#pragma unroll 1
+            for (int x = 0; x < D / 16; ++x) {
+              uint32_t o[16];
+              tld16(t_o + 16 * x, o);
+              tc05::wait_ld();
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
+              tst16(t_o + 16 * x, o);
+            }
+          }
+          l *= alpha;
+          if (need) m_ref = m_new;
+        }
+        // a row that has seen no key yet keeps m = -inf: its weights are 2^-inf = 0
+        l += prompt_weights(t_s, qs, m_ref == -INFINITY ? 0.f : -m_ref, sv);
+        tc05::wait_st();
+        tc05::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[t]);
+      }
+      if (!ok) break;
+      ok = wait_warp(&bars->pv_done[t], pvc & 1u, abort);
+      ++pvc;
+      if (!ok) break;
+      tc05::fence_after_sync();
+      const bool none = l == 0.f;                          // every score -inf (a NaN goes on to the output)
+      const float inv = none ? 0.f : 1.f / l;
+      const size_t orow = (size_t)(it.row0 + pos) * p.Hq + it.hg * p.heads + r % p.heads;
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t o[32];
+        tc05::ld32(t_o + 32 * x, o);
+        tc05::wait_ld();
+        if (x == D / 32 - 1) {                             // O is read out: the next item may overwrite it
+          tc05::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->o_free[t]);
+        }
+        if (valid) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            uint4 w;
+            w.x = pack2(__uint_as_float(o[8 * y + 0]) * inv, __uint_as_float(o[8 * y + 1]) * inv);
+            w.y = pack2(__uint_as_float(o[8 * y + 2]) * inv, __uint_as_float(o[8 * y + 3]) * inv);
+            w.z = pack2(__uint_as_float(o[8 * y + 4]) * inv, __uint_as_float(o[8 * y + 5]) * inv);
+            w.w = pack2(__uint_as_float(o[8 * y + 6]) * inv, __uint_as_float(o[8 * y + 7]) * inv);
+            if (none) w = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(p.out + orow * D + 32 * x + 8 * y) = w;
+          }
+        }
+      }
+      if (valid && p.lse) p.lse[orow] = none ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+    }
+    if (!ok && lane == 0) give_up(p.err, abort);
+  }
+  tc05::fence_before_sync();
+  __syncthreads();
+  if (warp == 2) {
+    tc05::fence_after_sync();
+    tc05::tmem_free(tbase, 512);
+  }
+}
+
+// Key or value rows: 4-D view (d mod 64, row, d / 64, head), `stride` values between rows; the box {64, 128, D / 64, 1}
+// lands 128 rows of one head as [D / 64][128 rows][128 B], 128B swizzle. Rows past `rows` read as zeros.
+bool encode_kv_map(CUtensorMap* tm, const void* base, int D, int heads, int rows, long long stride) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)(D / 64), (cuuint64_t)heads};
+  cuuint64_t strides[3] = {(cuuint64_t)stride * 2, 128, (cuuint64_t)D * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)kTKeys, (cuuint32_t)(D / 64), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t st) {
+  CUtensorMap tq, tk, tv;
+  if (!encode_query_map(&tq, p.q, D, p.Hq / p.heads, p.heads, p.total, p.tile_tokens, p.q_stride) ||
+      !encode_kv_map(&tk, p.k, D, p.Hkv, p.total, p.k_stride) || !encode_kv_map(&tv, p.v, D, p.Hkv, p.total, p.v_stride))
+    return cudaErrorInvalidValue;
+  constexpr int smem = prompt_smem_bytes<D>();
+  static_assert(smem <= 232448, "shared memory of one CTA");
+  cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(prompt_tc05_kernel<D>), smem);
+  if (e != cudaSuccess) return e;
+  // at most so many items: a CTA for each, and one a processor
+  const long long items = ((long long)p.total / (2 * p.tile_tokens) + p.n) * (p.Hq / p.heads);
+  prompt_tc05_kernel<D><<<(int)(items < num_sms ? items : num_sms), kPThreads, smem, st>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_tc05(PromptParams p, int D, int num_sms, cudaStream_t st) {
+  p.heads = p.G;
+  p.tile_tokens = kTRows / p.heads;
+  return D == 128 ? launch_prompt<128>(p, num_sms, st) : launch_prompt<64>(p, num_sms, st);
+}
+
+}  // namespace ekv

@@ -36,6 +36,11 @@ EKV_MODE_MICRO_FP4 = 3
 EKV_SCALE_PER_TENSOR = 0
 EKV_SCALE_PER_PAGE_HEAD = 1
 
+EKV_ROPE_PLAIN = 0
+EKV_ROPE_LINEAR = 1
+EKV_ROPE_BY_TURNS = 2
+EKV_ROPE_BY_DIMS = 3
+
 EKV_DETAIL_NONE = 0
 EKV_DETAIL_PAGE_ID = 1
 EKV_DETAIL_SCALE = 2
@@ -49,13 +54,20 @@ EXPORTED = ["ekv_create", "ekv_destroy", "ekv_paged_decode", "ekv_gather_prefill
             "ekv_set_decode_variant", "ekv_query", "ekv_paged_decode_noalloc",
             "ekv_demote_pages_base", "ekv_promote_pages", "ekv_append_kv", "ekv_paged_decode_elastic",
             "ekv_transition_pages", "ekv_prefill_attention", "ekv_gather_prefill_elastic",
-            "ekv_append_kv_rope", "ekv_extend_attention", "ekv_demote_pages_micro", "ekv_expand_pages_micro",
+            "ekv_append_kv_rope", "ekv_rope_table", "ekv_append_kv_norm_rope", "ekv_prompt_attention", "ekv_extend_attention", "ekv_demote_pages_micro", "ekv_expand_pages_micro",
             "ekv_set_pdl", "ekv_profile_launch_floor", "ekv_status_string"]
 
 
 class ekv_config(ctypes.Structure):
     _fields_ = [("num_q_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("max_batch", ctypes.c_int)]
+
+
+class ekv_rope_config(ctypes.Structure):
+    """How rotary angles are made: theta, scaling, factor, original_len, slow, fast, magnitude (see include/ekv.h)."""
+    _fields_ = [("theta", ctypes.c_double), ("scaling", ctypes.c_int), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("slow", ctypes.c_double), ("fast", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
 
 
 _vp = ctypes.c_void_p
@@ -80,6 +92,10 @@ _lib.ekv_prefill_attention.argtypes = [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i,
 _lib.ekv_append_kv.argtypes = [_vp, _vp, _vp, _vp, _vp, _ll, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp]
 _lib.ekv_append_kv_rope.argtypes = [_vp, _vp, _vp, _vp, _ll, _ll, _ll, _vp, _i, _i, _i, _vp, _vp, _vp, _ll, _i, _vp, _i,
                                     _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp]
+_lib.ekv_rope_table.argtypes = [_vp, ctypes.POINTER(ekv_rope_config), _vp, _i, _i, _i, _vp]
+_lib.ekv_append_kv_norm_rope.argtypes = [_vp, _vp, _vp, _vp, _ll, _ll, _ll, _vp, _vp, ctypes.c_float, _vp, _i, _i, _i, _vp, _vp,
+                                         _vp, _vp, _ll, _i, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp]
+_lib.ekv_prompt_attention.argtypes = [_vp, _vp, _vp, _vp, _ll, _ll, _ll, _vp, _i, _i, _i, ctypes.c_float, _vp, _vp, _vp]
 _lib.ekv_extend_attention.argtypes = [_vp, _vp, _vp, _vp, _ll, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i,
                                       ctypes.c_float, _vp, _vp, _vp]
 _lib.ekv_demote_pages_micro.argtypes = [_vp, _vp, _ll, _i, _vp, _i, _vp, _vp]
@@ -276,6 +292,33 @@ def ekv_append_kv_rope(ctx, q, k_new, v_new, q_stride, k_stride, v_stride, rope_
                                    _ptr(v_pages), v_page_stride_bytes, num_pages, _ptr(v_scales), scale_mode,
                                    _ptr(page_mode), uniform_mode, _ptr(block_table), block_table_stride,
                                    _ptr(seq_lens), _ptr(cu_q), batch, total_q, _stream(stream)), "ekv_append_kv_rope")
+
+
+def ekv_rope_table(ctx, cfg, table, first, rope_len, rope_dim, stream=None):
+    """Cosines and sines of the positions first .. first + rope_len - 1 under an ``ekv_rope_config`` (None: refused)."""
+    _check(_lib.ekv_rope_table(ctx, ctypes.byref(cfg) if cfg else None, _ptr(table), first, rope_len, rope_dim,
+                               _stream(stream)), "ekv_rope_table")
+
+
+def ekv_append_kv_norm_rope(ctx, q, k_new, v_new, q_stride, k_stride, v_stride, q_weight, k_weight, norm_eps, rope_table,
+                            rope_len, rope_dim, rope_style, q_out, k_out, k_pages, v_pages, v_page_stride_bytes, num_pages,
+                            v_scales, scale_mode, grow_scales, page_mode, uniform_mode, block_table, block_table_stride,
+                            seq_lens, cu_q, batch, total_q, stream=None):
+    """Normalise the heads of the new tokens' queries and keys, rotate them, write keys and values into the paged cache
+    (with grow_scales under E4M3 scales that the call makes)."""
+    _check(_lib.ekv_append_kv_norm_rope(ctx, _ptr(q), _ptr(k_new), _ptr(v_new), q_stride, k_stride, v_stride, _ptr(q_weight),
+                                        _ptr(k_weight), float(norm_eps), _ptr(rope_table), rope_len, rope_dim, rope_style,
+                                        _ptr(q_out), _ptr(k_out), _ptr(k_pages), _ptr(v_pages), v_page_stride_bytes, num_pages,
+                                        _ptr(v_scales), scale_mode, int(grow_scales), _ptr(page_mode), uniform_mode,
+                                        _ptr(block_table), block_table_stride, _ptr(seq_lens), _ptr(cu_q), batch, total_q,
+                                        _stream(stream)), "ekv_append_kv_norm_rope")
+
+
+def ekv_prompt_attention(ctx, q, k, v, q_stride, k_stride, v_stride, cu_seqlens, n, total, window, sm_scale, out, lse=None,
+                         stream=None):
+    """Causal attention of packed prompts over their own rows of q, k and v, with an optional window."""
+    _check(_lib.ekv_prompt_attention(ctx, _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride, _ptr(cu_seqlens), n, total,
+                                     window, float(sm_scale), _ptr(out), _ptr(lse), _stream(stream)), "ekv_prompt_attention")
 
 
 def ekv_extend_attention(ctx, q, k_pages, v_pages, v_page_stride_bytes, num_pages, v_scales, scale_mode, page_mode,
