@@ -42,7 +42,7 @@ __device__ __forceinline__ uint32_t finite_mag16(const uint4& a, const uint4& b)
   return m;
 }
 
-// 16 values as E4M3 codes of the IEEE quotient by s; r = 1 / s where s is far from the ends of fp32's range.
+// 16 values as E4M3 codes of the IEEE quotient by s; plain: they are finite and s is far from the ends of fp32's range, r = 1 / s.
 __device__ __forceinline__ uint4 e4m3_encode16(const uint4& a, const uint4& b, float s, float r, bool plain) {
   if (!plain) {
     const uint2 lo = e4m3_encode8(a, s), hi = e4m3_encode8(b, s);
@@ -135,8 +135,15 @@ __device__ __forceinline__ void grow_values(const RopeAppendParams& p, int warp,
       float s = r0 > 0 ? *scale : 0.f;
       uint32_t m2 = 0;
 #pragma unroll
-      for (int x = 0; x < NP; ++x) m2 = __vmaxu2(m2, finite_mag16(a0[x], a1[x]));
-      const uint32_t mag = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+      for (int x = 0; x < NP; ++x) m2 = __vmaxu2(m2, max_mag16(a0[x], a1[x]));
+      uint32_t mag = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+      const bool finite = mag < 0x7c00u;
+      if (!finite) {
+        m2 = 0;
+#pragma unroll
+        for (int x = 0; x < NP; ++x) m2 = __vmaxu2(m2, finite_mag16(a0[x], a1[x]));
+        mag = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+      }
       const float a = __half2float(__ushort_as_half((unsigned short)mag));
       uint8_t* base = const_cast<uint8_t*>(c.v_pages) + (size_t)pg * c.v_page_stride + h * D + 16 * u;
       if (r0 == 0) {
@@ -164,7 +171,7 @@ __device__ __forceinline__ void grow_values(const RopeAppendParams& p, int warp,
           if (lane == 0) *scale = s;
         }
       }
-      const bool plain = s > 1e-30f && s < 1e30f;
+      const bool plain = finite && s > 1e-30f && s < 1e30f;
       const float r = __frcp_rn(s);
 #pragma unroll
       for (int x = 0; x < NP; ++x) {
