@@ -23,11 +23,11 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libekv.so")
 TEST_LIB = os.path.join(HERE, "libekv_waittest.so")
-SOURCES = ["ekv_api.cu", "decode_simt.cu", "decode_mma.cu", "gather_demote.cu", "append_rope.cu", "extend_tc05_d64.cu", "extend_tc05_d128.cu",
+SOURCES = ["ekv_api.cu", "decode_simt.cu", "decode_mma.cu", "gather_demote.cu", "append_rope.cu", "append_norm.cu", "extend_tc05_d64.cu", "extend_tc05_d128.cu",
            "noalloc.cu", "prefill_mma.cu", "prefill_tc05.cu", "prompt_tc05.cu", "rope_table.cu"]
 # translation units that see the parameters or the wait bound of what a test runs out: rebuilt for the test library
 TEST_SOURCES = ["ekv_api.cu", "decode_simt.cu", "decode_mma.cu", "noalloc.cu", "gather_demote.cu",
-                "extend_tc05_d64.cu", "extend_tc05_d128.cu", "prompt_tc05.cu"]
+                "extend_tc05_d64.cu", "extend_tc05_d128.cu", "prompt_tc05.cu", "append_rope.cu", "append_norm.cu"]
 TEST_DEFINE = "-DEKV_TEST_WAIT_TIMEOUT"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -122,7 +122,7 @@ int last_kernel(cudaStream_t st) {
 }
 
 #ifdef EKV_TEST_WAIT_TIMEOUT
-// test build only: calls left (decode, transitions) that run a ring wait out
+// test build only: calls left (decode, transitions, normalising writer) that run a ring wait out
 int g_inject_timeout_calls = 0;
 // test build only: the wait that the next call of ekv_extend_attention runs out
 int g_inject_extend_wait = 0;
@@ -715,6 +715,10 @@ ekv_status ekv_append_kv_norm_rope(ekv_ctx* c, const void* q, const void* k_new,
   p.eps = norm_eps;
   p.k_out = static_cast<__half*>(k_out);
   p.grow = grow_scales;
+#ifdef EKV_TEST_WAIT_TIMEOUT
+  p.inject_timeout = g_inject_timeout_calls > 0;
+  if (p.inject_timeout) --g_inject_timeout_calls;
+#endif
   DeviceGuard g(c->device);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   c->last_stream = st;

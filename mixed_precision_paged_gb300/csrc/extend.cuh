@@ -35,12 +35,15 @@ struct RopeAppendParams {
   const float* rope;        // [rope_len][rope_dim]
   int rope_len, rope_dim, rope_style;
   __half* q_out;
-  // norm_append_kernel alone
+  // append_norm.cu alone
   const __half* q_weight;   // [D]; null: queries are not normalised
   const __half* k_weight;   // the same of keys
   float eps;
   __half* k_out;            // [total_q][Hkv][D] or null
   int grow;                 // 1: the call makes the scales of E4M3 pages
+#ifdef EKV_TEST_WAIT_TIMEOUT
+  int inject_timeout;       // test build only: the stream's first wait of CTA 0 runs out
+#endif
 };
 
 // Pages of a sequence at most (2^21 tokens): keeps the block counts of the plan in 32 bits.
@@ -75,7 +78,35 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t* cu, int batch, 
   return lo;
 }
 
+// The same by one lane, for rows first <= i < last of which every lane has its own: the guess of a batch of equal
+// lengths first (one round trip for a decode step), then the eight sequences beside it, then the rest.
+__device__ __forceinline__ int lane_find_sequence(const int32_t* cu, int batch, int i, int first, int last) {
+  int lo = 0, hi = batch;
+  const int g = min(batch - 1, (int)((long long)(i - first) * batch / (last - first)));
+  const int c0 = __ldg(cu + g), c1 = __ldg(cu + g + 1);
+  if (c1 <= i) {
+    lo = g + 1;
+    const int m = min(g + 8, batch - 1);
+    if (__ldg(cu + m + 1) > i) hi = m;
+    else lo = max(lo, m + 1);
+  } else if (c0 <= i) {
+    return g;
+  } else {
+    hi = g;
+    const int m = max(g - 8, 0);
+    if (__ldg(cu + m) <= i) lo = m;
+    else hi = m;
+  }
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(cu + mid + 1) <= i) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
 cudaError_t launch_rope_append(const RopeAppendParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_norm_append(const RopeAppendParams& p, int num_sms, cudaStream_t st);
+cudaError_t set_smem_attr(const void* kern, int bytes);
 
 }  // namespace ekv
