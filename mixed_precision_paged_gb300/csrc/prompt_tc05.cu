@@ -20,6 +20,7 @@
 // of the prefill (prefill_tc05.cu); the reference of a row lies 2^kHeadroom below its maximum, so that fp16 weights keep
 // their bits down to 2^-21 of the largest (extend_tc05.cuh). Every wait is bounded; a timeout is reported and
 // every role winds down.
+#include <stdlib.h>
 #include "extend_tc05.cuh"
 #include "prompt.cuh"
 
@@ -274,183 +275,188 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
   const uint32_t tbase = bars->tmem_base;
   const int TT = p.tile_tokens;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ loads
-    int stage = 0, u = 0;
-    uint32_t phase = 0, edges = 0;                         // edges: bit per stage whose last copy went to v_raw
-    uint32_t raw_ph = 0;                                   // bit per stage: parity of v_raw's last phase begun
-    uint32_t ql[2] = {0u, 0u};                             // query tiles loaded, per tile
-    bool ok = true;
-    for (int r = 0; ok && dealt(r) < W; ++r) {
-      const PromptItem it = prompt_item(p, pl, dealt(r));
-      const int h = it.hg * p.heads / p.G;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (!ok || it.ja[t] >= it.jb[t]) continue;
-        if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
-        if (!ok) continue;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(TT * p.heads * D * 2));
-          for (int s = 0; s < NB; ++s)
-            tma_load_5d(sQ + t * C::QB + s * kTRows * 128, &tq, 0, 0, s, it.hg, it.row0 + it.q0[t], &bars->q_full[t]);
-        }
-        ++ql[t];
-      }
-      const bool edge = it.L < it.jhi * kTKeys;            // the last block reaches past the prompt
-      for (int j = it.jlo; ok && j < it.jhi; ++j) {
-        for (int is_v = 0; is_v < 2; ++is_v) {
-          if (u >= NS) ok = wait_warp(&bars->kv_empty[stage], phase ^ 1u, abort);
-          if (!ok) break;
-          const bool raw = is_v && edge && j == it.jhi - 1;
-          uint64_t* bar = raw ? &bars->v_raw[stage] : &bars->kv_full[stage];
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar, C::IB);
-            tma_load_4d(sKV + stage * C::IB, is_v ? &tv : &tk, 0, it.row0 + j * kTKeys, 0, h, bar);
-          }
-          edges = raw ? edges | 1u << stage : edges & ~(1u << stage);
-          if (raw) raw_ph ^= 1u << stage;
-          ++u;
-          if (++stage == NS) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
-    }
-    if (!ok && lane == 0) give_up(p.err, abort);
-    // the copies still in flight land before the CTA can exit
-    for (int v = u > NS ? u - NS : 0; v < u; ++v) {
-      const int s = v % NS;
-      if ((edges >> s) & 1u) drain(&bars->v_raw[s], ((raw_ph >> s) & 1u) ^ 1u);
-      else drain(&bars->kv_full[s], (uint32_t)(v / NS) & 1u);
-    }
-    for (int t = 0; t < 2; ++t)
-      if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
-  } else if (warp == 3) {
-    // ------------------------------------- value rows past a prompt's end: zeros
-    int u = 0;                                             // blocks up to the item's end
-    uint32_t raw_ph = 0;
-    bool ok = true;
-    for (int r = 0; ok && dealt(r) < W; ++r) {
-      const PromptItem it = prompt_item(p, pl, dealt(r));
-      u += 2 * (it.jhi - it.jlo);
-      const int zr = it.L - (it.jhi - 1) * kTKeys;         // rows >= zr of the last block
-      if (zr >= kTKeys) continue;
-      const int s = (u - 1) % NS;
-      ok = wait_warp(&bars->v_raw[s], (raw_ph >> s) & 1u, abort);
-      raw_ph ^= 1u << s;
-      if (!ok) break;
-      uint8_t* dst = sKV + s * C::IB;
-      const int per_slab = (kTKeys - zr) * 8;              // 16-byte chunks past the prompt
-      for (int e = lane; e < per_slab * NB; e += 32) {
-        const int slab = e / per_slab, rem = e % per_slab;
-        *reinterpret_cast<uint4*>(dst + slab * kTKeys * 128 + (zr + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->kv_full[s]);
-    }
-    if (!ok && lane == 0) give_up(p.err, abort);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------- MMA issuer
-    // The whole warp runs the control flow and computes the descriptors; one elected lane issues.
-    constexpr uint32_t idS = tc05::idesc_f16_f32(kTRows, kTKeys, false);
-    constexpr uint32_t idO = tc05::idesc_f16_f32(kTRows, D, true);
-    constexpr uint32_t HI = tc05::sdesc_hi(1024);          // 8-row groups 1024 B apart
-    const uint32_t q_lo = tc05::sdesc_lo(smem_u32(sQ), 16);
-    const uint32_t k_lo = tc05::sdesc_lo(smem_u32(sKV), 16);
-    const uint32_t v_lo = tc05::sdesc_lo(smem_u32(sKV), kTKeys * 128);
-    int ks = 0, vs = 1;                                    // ring cursors of the K blocks and the V blocks
-    uint32_t kp = 0, vp = 0;
-    uint32_t qc[2] = {0u, 0u}, pc[2] = {0u, 0u}, oc[2] = {0u, 0u};   // phases taken: q_full, p_full; items with an O
-    auto adv2 = [&](int& s, uint32_t& ph) {
-      s += 2;
-      if (s >= NS) {
-        s -= NS;
-        ph ^= 1u;
-      }
-    };
-    auto commit_one = [&](uint64_t* bar) {
-      if (tc05::elect_one()) tc05::commit(bar);
-      __syncwarp();
-    };
-    bool ok = true;
-    for (int r = 0; ok && dealt(r) < W; ++r) {
-      const PromptItem it = prompt_item(p, pl, dealt(r));
-      // S_t of block j, over the P_t before it (read by an O_t += P_t V issued earlier: one thread's MMAs run in order)
-      auto issue_s = [&](int t, int j) {
-        if (j == it.ja[t]) {
-          ok = wait_warp(&bars->q_full[t], qc[t] & 1u, abort);
-          ++qc[t];
-          if (!ok) return;
-        }
-        tc05::fence_after_sync();
-        const uint32_t qa = q_lo + t * (C::QB >> 4), ka = k_lo + ks * (C::IB >> 4);
-        if (tc05::elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc05::mma_ss(tbase + t * 256, tc05::sdesc_join(qa + (((k >> 2) * (kTRows * 128) + (k & 3) * 32) >> 4), HI),
-                         tc05::sdesc_join(ka + (((k >> 2) * (kTKeys * 128) + (k & 3) * 32) >> 4), HI), idS, k > 0);
-          tc05::commit(&bars->s_full[t]);
-          if (j + 1 == it.jb[t]) tc05::commit(&bars->q_empty[t]);
-        }
-        __syncwarp();
-      };
-      ok = wait_warp(&bars->kv_full[ks], kp, abort);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (ok && it.ja[t] == it.jlo && it.jlo < it.jb[t]) issue_s(t, it.jlo);
-      if (!ok) break;
-      commit_one(&bars->kv_empty[ks]);
-      adv2(ks, kp);
-      for (int j = it.jlo; ok && j < it.jhi; ++j) {
-        ok = wait_warp(&bars->kv_full[vs], vp, abort);
-        if (!ok) break;
-        const uint32_t va = v_lo + vs * (C::IB >> 4);
-        bool k_ready = false;
+  // (each register split stands at the head of its roles' code: 80 and 208 a thread, the 168 of launch together)
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 0) {
+      // ------------------------------------------------------------ loads
+      int stage = 0, u = 0;
+      uint32_t phase = 0, edges = 0;                         // edges: bit per stage whose last copy went to v_raw
+      uint32_t raw_ph = 0;                                   // bit per stage: parity of v_raw's last phase begun
+      uint32_t ql[2] = {0u, 0u};                             // query tiles loaded, per tile
+      bool ok = true;
+      for (int r = 0; ok && dealt(r) < W; ++r) {
+        const PromptItem it = prompt_item(p, pl, dealt(r));
+        const int h = it.hg * p.heads / p.G;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (ok && j >= it.ja[t] && j < it.jb[t]) {
-            // O_t += P_t V_j once the softmax has written P (and, for an item's first block, once the
-            // previous item's O_t has been read out)
-            ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
-            ++pc[t];
-            if (ok && j == it.ja[t] && oc[t] > 0) ok = wait_warp(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
-            if (ok) {
-              tc05::fence_after_sync();
-              const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
-              const bool acc0 = j > it.ja[t];
-              if (tc05::elect_one()) {
-#pragma unroll
-                for (int k = 0; k < kTKeys / 16; ++k)
-                  tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2048 >> 4), HI), idO, acc0 || k > 0);
-                if (j + 1 == it.jb[t]) tc05::commit(&bars->pv_done[t]);
-              }
-              __syncwarp();
+          if (!ok || it.ja[t] >= it.jb[t]) continue;
+          if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
+          if (!ok) continue;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(TT * p.heads * D * 2));
+            for (int s = 0; s < NB; ++s)
+              tma_load_5d(sQ + t * C::QB + s * kTRows * 128, &tq, 0, 0, s, it.hg, it.row0 + it.q0[t], &bars->q_full[t]);
+          }
+          ++ql[t];
+        }
+        const bool edge = it.L < it.jhi * kTKeys;            // the last block reaches past the prompt
+        for (int j = it.jlo; ok && j < it.jhi; ++j) {
+          for (int is_v = 0; is_v < 2; ++is_v) {
+            if (u >= NS) ok = wait_warp(&bars->kv_empty[stage], phase ^ 1u, abort);
+            if (!ok) break;
+            const bool raw = is_v && edge && j == it.jhi - 1;
+            uint64_t* bar = raw ? &bars->v_raw[stage] : &bars->kv_full[stage];
+            if (lane == 0) {
+              mbar_arrive_expect_tx(bar, C::IB);
+              tma_load_4d(sKV + stage * C::IB, is_v ? &tv : &tk, 0, it.row0 + j * kTKeys, 0, h, bar);
+            }
+            edges = raw ? edges | 1u << stage : edges & ~(1u << stage);
+            if (raw) raw_ph ^= 1u << stage;
+            ++u;
+            if (++stage == NS) {
+              stage = 0;
+              phase ^= 1u;
             }
           }
-          if (ok && j + 1 >= it.ja[t] && j + 1 < it.jb[t]) {   // S_t of the next block, right behind
-            if (!k_ready) ok = wait_warp(&bars->kv_full[ks], kp, abort);
-            k_ready = true;
-            if (ok) issue_s(t, j + 1);
-          }
-        }
-        if (!ok) break;
-        commit_one(&bars->kv_empty[vs]);
-        adv2(vs, vp);
-        if (j + 1 < it.jhi) {
-          commit_one(&bars->kv_empty[ks]);
-          adv2(ks, kp);
         }
       }
-#pragma unroll
+      if (!ok && lane == 0) give_up(p.err, abort);
+      // the copies still in flight land before the CTA can exit
+      for (int v = u > NS ? u - NS : 0; v < u; ++v) {
+        const int s = v % NS;
+        if ((edges >> s) & 1u) drain(&bars->v_raw[s], ((raw_ph >> s) & 1u) ^ 1u);
+        else drain(&bars->kv_full[s], (uint32_t)(v / NS) & 1u);
+      }
       for (int t = 0; t < 2; ++t)
-        if (it.ja[t] < it.jb[t]) ++oc[t];
+        if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
+    } else if (warp == 3) {
+      // ------------------------------------- value rows past a prompt's end: zeros
+      int u = 0;                                             // blocks up to the item's end
+      uint32_t raw_ph = 0;
+      bool ok = true;
+      for (int r = 0; ok && dealt(r) < W; ++r) {
+        const PromptItem it = prompt_item(p, pl, dealt(r));
+        u += 2 * (it.jhi - it.jlo);
+        const int zr = it.L - (it.jhi - 1) * kTKeys;         // rows >= zr of the last block
+        if (zr >= kTKeys) continue;
+        const int s = (u - 1) % NS;
+        ok = wait_warp(&bars->v_raw[s], (raw_ph >> s) & 1u, abort);
+        raw_ph ^= 1u << s;
+        if (!ok) break;
+        uint8_t* dst = sKV + s * C::IB;
+        const int per_slab = (kTKeys - zr) * 8;              // 16-byte chunks past the prompt
+        for (int e = lane; e < per_slab * NB; e += 32) {
+          const int slab = e / per_slab, rem = e % per_slab;
+          *reinterpret_cast<uint4*>(dst + slab * kTKeys * 128 + (zr + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->kv_full[s]);
+      }
+      if (!ok && lane == 0) give_up(p.err, abort);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------- MMA issuer
+      // The whole warp runs the control flow and computes the descriptors; one elected lane issues.
+      constexpr uint32_t idS = tc05::idesc_f16_f32(kTRows, kTKeys, false);
+      constexpr uint32_t idO = tc05::idesc_f16_f32(kTRows, D, true);
+      constexpr uint32_t HI = tc05::sdesc_hi(1024);          // 8-row groups 1024 B apart
+      const uint32_t q_lo = tc05::sdesc_lo(smem_u32(sQ), 16);
+      const uint32_t k_lo = tc05::sdesc_lo(smem_u32(sKV), 16);
+      const uint32_t v_lo = tc05::sdesc_lo(smem_u32(sKV), kTKeys * 128);
+      int ks = 0, vs = 1;                                    // ring cursors of the K blocks and the V blocks
+      uint32_t kp = 0, vp = 0;
+      uint32_t qc[2] = {0u, 0u}, pc[2] = {0u, 0u}, oc[2] = {0u, 0u};   // phases taken: q_full, p_full; items with an O
+      auto adv2 = [&](int& s, uint32_t& ph) {
+        s += 2;
+        if (s >= NS) {
+          s -= NS;
+          ph ^= 1u;
+        }
+      };
+      auto commit_one = [&](uint64_t* bar) {
+        if (tc05::elect_one()) tc05::commit(bar);
+        __syncwarp();
+      };
+      bool ok = true;
+      for (int r = 0; ok && dealt(r) < W; ++r) {
+        const PromptItem it = prompt_item(p, pl, dealt(r));
+        // S_t of block j, over the P_t before it (read by an O_t += P_t V issued earlier: one thread's MMAs run in order)
+        auto issue_s = [&](int t, int j) {
+          if (j == it.ja[t]) {
+            ok = wait_warp(&bars->q_full[t], qc[t] & 1u, abort);
+            ++qc[t];
+            if (!ok) return;
+          }
+          tc05::fence_after_sync();
+          const uint32_t qa = q_lo + t * (C::QB >> 4), ka = k_lo + ks * (C::IB >> 4);
+          if (tc05::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              tc05::mma_ss(tbase + t * 256, tc05::sdesc_join(qa + (((k >> 2) * (kTRows * 128) + (k & 3) * 32) >> 4), HI),
+                           tc05::sdesc_join(ka + (((k >> 2) * (kTKeys * 128) + (k & 3) * 32) >> 4), HI), idS, k > 0);
+            tc05::commit(&bars->s_full[t]);
+            if (j + 1 == it.jb[t]) tc05::commit(&bars->q_empty[t]);
+          }
+          __syncwarp();
+        };
+        ok = wait_warp(&bars->kv_full[ks], kp, abort);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && it.ja[t] == it.jlo && it.jlo < it.jb[t]) issue_s(t, it.jlo);
+        if (!ok) break;
+        commit_one(&bars->kv_empty[ks]);
+        adv2(ks, kp);
+        for (int j = it.jlo; ok && j < it.jhi; ++j) {
+          ok = wait_warp(&bars->kv_full[vs], vp, abort);
+          if (!ok) break;
+          const uint32_t va = v_lo + vs * (C::IB >> 4);
+          bool k_ready = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (ok && j >= it.ja[t] && j < it.jb[t]) {
+              // O_t += P_t V_j once the softmax has written P (and, for an item's first block, once the
+              // previous item's O_t has been read out)
+              ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
+              ++pc[t];
+              if (ok && j == it.ja[t] && oc[t] > 0) ok = wait_warp(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
+              if (ok) {
+                tc05::fence_after_sync();
+                const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
+                const bool acc0 = j > it.ja[t];
+                if (tc05::elect_one()) {
+#pragma unroll
+                  for (int k = 0; k < kTKeys / 16; ++k)
+                    tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2048 >> 4), HI), idO, acc0 || k > 0);
+                  if (j + 1 == it.jb[t]) tc05::commit(&bars->pv_done[t]);
+                }
+                __syncwarp();
+              }
+            }
+            if (ok && j + 1 >= it.ja[t] && j + 1 < it.jb[t]) {   // S_t of the next block, right behind
+              if (!k_ready) ok = wait_warp(&bars->kv_full[ks], kp, abort);
+              k_ready = true;
+              if (ok) issue_s(t, j + 1);
+            }
+          }
+          if (!ok) break;
+          commit_one(&bars->kv_empty[vs]);
+          adv2(vs, vp);
+          if (j + 1 < it.jhi) {
+            commit_one(&bars->kv_empty[ks]);
+            adv2(ks, kp);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (it.ja[t] < it.jb[t]) ++oc[t];
+      }
+      if (!ok && lane == 0) give_up(p.err, abort);
+      commit_one(&bars->mma_final);
+      if (lane == 0) drain(&bars->mma_final, 0);
     }
-    if (!ok && lane == 0) give_up(p.err, abort);
-    commit_one(&bars->mma_final);
-    if (lane == 0) drain(&bars->mma_final, 0);
-  } else if (warp >= 4) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------- softmax, tile t
     const int t = (warp - 4) >> 2, r = threadIdx.x - 128 - t * kTRows;
     const uint32_t lanebase = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -580,7 +586,7 @@ cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_prompt_tc05(PromptParams p, int D, int num_sms, cudaStream_t st) {
-  p.heads = p.G;
+  p.heads = getenv("EKV_H1") ? 1 : p.G;
   p.tile_tokens = kTRows / p.heads;
   return D == 128 ? launch_prompt<128>(p, num_sms, st) : launch_prompt<64>(p, num_sms, st);
 }
