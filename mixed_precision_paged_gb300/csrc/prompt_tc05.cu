@@ -40,6 +40,17 @@ struct PT {
   static constexpr int NS = D == 128 ? 4 : 8;          // ring stages
 };
 
+constexpr int kItems = 4;                                 // descriptions of items
+constexpr int kItemReaders = 3 + 2 * kTRows / 32;        // warps that read one: loads, zeros, MMAs and softmax
+
+// One work item: two tiles of one prompt and `heads` query heads.
+struct PromptItem {
+  int row0, L, hg;         // the prompt's first row, its tokens; the group of heads
+  int q0[2];               // [tile] first token
+  int ja[2], jb[2];        // [tile] key blocks [ja, jb); none where the tile has no token
+  int jlo, jhi;            // of either; jlo < 0: no item follows
+};
+
 template <int NS>
 struct PromptBars {
   uint64_t q_full[2];            // [tile]: the tile's query rows of its next item landed
@@ -52,6 +63,8 @@ struct PromptBars {
   uint64_t pv_done[2];           // [tile]: an item's last O += P V completed
   uint64_t o_free[2];            // [tile]: an item's O read out (one arrival per softmax warp)
   uint64_t mma_final;            // every MMA issued has completed
+  uint64_t item_full[kItems], item_empty[kItems];   // a description posted; read by its readers
+  PromptItem item[kItems];
   int red[kPThreads / 32];
   uint32_t tmem_base;
   int abort;
@@ -126,14 +139,6 @@ __device__ __forceinline__ int make_plan(const PromptParams& p, Plan& pl, int* r
   return total;
 }
 
-// One work item: two tiles of one prompt and `heads` query heads.
-struct PromptItem {
-  int row0, L, hg;         // the prompt's first row, its tokens; the group of heads
-  int q0[2];               // [tile] first token
-  int ja[2], jb[2];        // [tile] key blocks [ja, jb); none where the tile has no token
-  int jlo, jhi;            // of either
-};
-
 // Item w of the list (the whole warp).
 __device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, const Plan& pl, int w) {
   const int lane = threadIdx.x & 31, groups = p.Hq / p.heads;
@@ -163,6 +168,18 @@ __device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, const P
   it.jlo = it.ja[0];
   it.jhi = max(it.jb[0], it.jb[1]);
   return it;
+}
+
+// The next item, as posted by warp 2, for a reader's warp; false: none follows, or a wait gave up (ok).
+template <int NS>
+__device__ __forceinline__ bool next_item(PromptBars<NS>* bars, int r, PromptItem& it, bool& ok) {
+  const int s = r % kItems;
+  ok = wait_warp(&bars->item_full[s], (uint32_t)(r / kItems) & 1u, &bars->abort);
+  if (!ok) return false;
+  it = bars->item[s];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->item_empty[s]);
+  return it.jlo >= 0;
 }
 
 // The r-th item of this CTA: dealt in rounds of gridDim.x, alternately forwards and backwards.
@@ -220,6 +237,13 @@ __device__ __forceinline__ float prompt_weights(uint32_t t_s, float qs, float nm
   return (la[0] + la[1]) + (lb[0] + lb[1]);
 }
 
+// 32 bytes to a 32-byte aligned place.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPThreads, 1)
 prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -253,6 +277,10 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       mbar_init(&bars->v_raw[s], 1);
     }
     mbar_init(&bars->mma_final, 1);
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(&bars->item_full[s], 1);
+      mbar_init(&bars->item_empty[s], kItemReaders);
+    }
     bars->abort = 0;
     fence_barrier_init();
 #ifdef EKV_TEST_WAIT_TIMEOUT
@@ -285,22 +313,10 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       uint32_t raw_ph = 0;                                   // bit per stage: parity of v_raw's last phase begun
       uint32_t ql[2] = {0u, 0u};                             // query tiles loaded, per tile
       bool ok = true;
-      for (int r = 0; ok && dealt(r) < W; ++r) {
-        const PromptItem it = prompt_item(p, pl, dealt(r));
+      PromptItem it;
+      for (int r = 0; next_item(bars, r, it, ok); ++r) {
         const int h = it.hg * p.heads / p.G;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || it.ja[t] >= it.jb[t]) continue;
-          if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
-          if (!ok) continue;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(TT * p.heads * D * 2));
-            for (int s = 0; s < NB; ++s)
-              tma_load_5d(sQ + t * C::QB + s * kTRows * 128, &tq, 0, 0, s, it.hg, it.row0 + it.q0[t], &bars->q_full[t]);
-          }
-          ++ql[t];
-        }
-        const bool edge = it.L < it.jhi * kTKeys;            // the last block reaches past the prompt
+        const bool edge = it.L < it.jhi * kTKeys;          // the last block reaches past the prompt
         for (int j = it.jlo; ok && j < it.jhi; ++j) {
           for (int is_v = 0; is_v < 2; ++is_v) {
             if (u >= NS) ok = wait_warp(&bars->kv_empty[stage], phase ^ 1u, abort);
@@ -319,7 +335,22 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               phase ^= 1u;
             }
           }
+          if (j > it.jlo) continue;
+          // the query tiles, behind the first blocks: these have free stages before the tiles' last rows are read
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || it.ja[t] >= it.jb[t]) continue;
+            if (ql[t] > 0) ok = wait_warp(&bars->q_empty[t], (ql[t] - 1u) & 1u, abort);
+            if (!ok) continue;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&bars->q_full[t], (uint32_t)(TT * p.heads * D * 2));
+              for (int s = 0; s < NB; ++s)
+                tma_load_5d(sQ + t * C::QB + s * kTRows * 128, &tq, 0, 0, s, it.hg, it.row0 + it.q0[t], &bars->q_full[t]);
+            }
+            ++ql[t];
+          }
         }
+        if (!ok) break;
       }
       if (!ok && lane == 0) give_up(p.err, abort);
       // the copies still in flight land before the CTA can exit
@@ -330,13 +361,32 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       }
       for (int t = 0; t < 2; ++t)
         if (ql[t] > 0) drain(&bars->q_full[t], (ql[t] - 1u) & 1u);
+    } else if (warp == 2) {
+      // ------------------------------------------ the items' descriptions, ahead of their readers
+      bool ok = true;
+      for (int r = 0; ok; ++r) {
+        const int s = r % kItems;
+        const bool none = dealt(r) >= W;
+        PromptItem it;
+        if (none) it.jlo = -1;
+        else it = prompt_item(p, pl, dealt(r));
+        if (r >= kItems) ok = wait_warp(&bars->item_empty[s], (uint32_t)(r / kItems - 1) & 1u, abort);
+        if (!ok) break;
+        if (lane == 0) {
+          bars->item[s] = it;
+          mbar_arrive(&bars->item_full[s]);
+        }
+        __syncwarp();
+        if (none) break;
+      }
+      if (!ok && lane == 0) give_up(p.err, abort);
     } else if (warp == 3) {
       // ------------------------------------- value rows past a prompt's end: zeros
       int u = 0;                                             // blocks up to the item's end
       uint32_t raw_ph = 0;
       bool ok = true;
-      for (int r = 0; ok && dealt(r) < W; ++r) {
-        const PromptItem it = prompt_item(p, pl, dealt(r));
+      PromptItem it;
+      for (int r = 0; next_item(bars, r, it, ok); ++r) {
         u += 2 * (it.jhi - it.jlo);
         const int zr = it.L - (it.jhi - 1) * kTKeys;         // rows >= zr of the last block
         if (zr >= kTKeys) continue;
@@ -379,8 +429,8 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         __syncwarp();
       };
       bool ok = true;
-      for (int r = 0; ok && dealt(r) < W; ++r) {
-        const PromptItem it = prompt_item(p, pl, dealt(r));
+      PromptItem it;
+      for (int r = 0; next_item(bars, r, it, ok); ++r) {
         // S_t of block j, over the P_t before it (read by an O_t += P_t V issued earlier: one thread's MMAs run in order)
         auto issue_s = [&](int t, int j) {
           if (j == it.ja[t]) {
@@ -447,6 +497,7 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             adv2(ks, kp);
           }
         }
+        if (!ok) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (it.ja[t] < it.jb[t]) ++oc[t];
@@ -463,10 +514,12 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const float qs = p.qscale;
     const uint32_t t_s = tbase + t * 256 + lanebase, t_o = tbase + t * 256 + 128 + lanebase;
     const int tok_t = r / p.heads;                         // this row's token within the tile
+    // a row's results leave 32 bytes at a time, a whole sector, where out lies so
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     uint32_t sc = 0, pvc = 0;                              // phases taken: s_full, pv_done
     bool ok = true;
-    for (int ri = 0; ok && dealt(ri) < W; ++ri) {
-      const PromptItem it = prompt_item(p, pl, dealt(ri));
+    PromptItem it;
+    for (int ri = 0; next_item(bars, ri, it, ok); ++ri) {
       const int ja = t ? it.ja[1] : it.ja[0], jb = t ? it.jb[1] : it.jb[0], q0 = t ? it.q0[1] : it.q0[0];
       if (ja >= jb) continue;
       const int pos = q0 + tok_t;
@@ -529,15 +582,17 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           if (lane == 0) mbar_arrive(&bars->o_free[t]);
         }
         if (valid) {
+          uint32_t w[16];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            uint4 w;
-            w.x = pack2(__uint_as_float(o[8 * y + 0]) * inv, __uint_as_float(o[8 * y + 1]) * inv);
-            w.y = pack2(__uint_as_float(o[8 * y + 2]) * inv, __uint_as_float(o[8 * y + 3]) * inv);
-            w.z = pack2(__uint_as_float(o[8 * y + 4]) * inv, __uint_as_float(o[8 * y + 5]) * inv);
-            w.w = pack2(__uint_as_float(o[8 * y + 6]) * inv, __uint_as_float(o[8 * y + 7]) * inv);
-            if (none) w = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(p.out + orow * D + 32 * x + 8 * y) = w;
+          for (int y = 0; y < 16; ++y) w[y] = none ? 0u : pack2(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
+          __half* dst = p.out + orow * D + 32 * x;
+          if (wide) {
+            store32(dst, w);
+            store32(dst + 16, w + 8);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              *reinterpret_cast<uint4*>(dst + 8 * y) = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
           }
         }
       }
