@@ -317,26 +317,26 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       for (int r = 0; next_item(bars, r, it, ok); ++r) {
         const int h = it.hg * p.heads / p.G;
         const bool edge = it.L < it.jhi * kTKeys;          // the last block reaches past the prompt
-        for (int j = it.jlo; ok && j < it.jhi; ++j) {
-          for (int is_v = 0; is_v < 2; ++is_v) {
-            if (u >= NS) ok = wait_warp(&bars->kv_empty[stage], phase ^ 1u, abort);
-            if (!ok) break;
-            const bool raw = is_v && edge && j == it.jhi - 1;
-            uint64_t* bar = raw ? &bars->v_raw[stage] : &bars->kv_full[stage];
-            if (lane == 0) {
-              mbar_arrive_expect_tx(bar, C::IB);
-              tma_load_4d(sKV + stage * C::IB, is_v ? &tv : &tk, 0, it.row0 + j * kTKeys, 0, h, bar);
-            }
-            edges = raw ? edges | 1u << stage : edges & ~(1u << stage);
-            if (raw) raw_ph ^= 1u << stage;
-            ++u;
-            if (++stage == NS) {
-              stage = 0;
-              phase ^= 1u;
-            }
+        for (int x = 0; ok && x < 2 * (it.jhi - it.jlo); ++x) {   // K, V, K, V, ...
+          if (u >= NS) ok = wait_warp(&bars->kv_empty[stage], phase ^ 1u, abort);
+          if (!ok) break;
+          const int j = it.jlo + x / 2;
+          const bool is_v = x & 1, raw = is_v && edge && j == it.jhi - 1;
+          uint64_t* bar = raw ? &bars->v_raw[stage] : &bars->kv_full[stage];
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, C::IB);
+            tma_load_4d(sKV + stage * C::IB, is_v ? &tv : &tk, 0, it.row0 + j * kTKeys, 0, h, bar);
           }
-          if (j > it.jlo) continue;
-          // the query tiles, behind the first blocks: these have free stages before the tiles' last rows are read
+          edges = raw ? edges | 1u << stage : edges & ~(1u << stage);
+          if (raw) raw_ph ^= 1u << stage;
+          ++u;
+          if (++stage == NS) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (x > 0) continue;
+          // The query tiles come behind the first keys, which have a free stage before the tiles' last rows are read, and
+          // before the values, which are wanted later: 32 KB take 700 cycles to arrive.
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!ok || it.ja[t] >= it.jb[t]) continue;
@@ -431,71 +431,71 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       bool ok = true;
       PromptItem it;
       for (int r = 0; next_item(bars, r, it, ok); ++r) {
-        // S_t of block j, over the P_t before it (read by an O_t += P_t V issued earlier: one thread's MMAs run in order)
+        // S_t of block j from stage ks, by one lane: over the P_t before it (read by an O_t += P_t V issued earlier: one
+        // thread's MMAs run in order)
         auto issue_s = [&](int t, int j) {
-          if (j == it.ja[t]) {
-            ok = wait_warp(&bars->q_full[t], qc[t] & 1u, abort);
-            ++qc[t];
-            if (!ok) return;
-          }
-          tc05::fence_after_sync();
           const uint32_t qa = q_lo + t * (C::QB >> 4), ka = k_lo + ks * (C::IB >> 4);
-          if (tc05::elect_one()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              tc05::mma_ss(tbase + t * 256, tc05::sdesc_join(qa + (((k >> 2) * (kTRows * 128) + (k & 3) * 32) >> 4), HI),
-                           tc05::sdesc_join(ka + (((k >> 2) * (kTKeys * 128) + (k & 3) * 32) >> 4), HI), idS, k > 0);
-            tc05::commit(&bars->s_full[t]);
-            if (j + 1 == it.jb[t]) tc05::commit(&bars->q_empty[t]);
-          }
-          __syncwarp();
+          for (int k = 0; k < D / 16; ++k)
+            tc05::mma_ss(tbase + t * 256, tc05::sdesc_join(qa + (((k >> 2) * (kTRows * 128) + (k & 3) * 32) >> 4), HI),
+                         tc05::sdesc_join(ka + (((k >> 2) * (kTKeys * 128) + (k & 3) * 32) >> 4), HI), idS, k > 0);
+          tc05::commit(&bars->s_full[t]);
+          if (j + 1 == it.jb[t]) tc05::commit(&bars->q_empty[t]);
         };
         ok = wait_warp(&bars->kv_full[ks], kp, abort);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (ok && it.ja[t] == it.jlo && it.jlo < it.jb[t]) issue_s(t, it.jlo);
+        for (int t = 0; t < 2; ++t) {
+          if (ok && it.ja[t] == it.jlo && it.jlo < it.jb[t]) {
+            ok = wait_warp(&bars->q_full[t], qc[t] & 1u, abort);
+            ++qc[t];
+            tc05::fence_after_sync();
+            if (ok && tc05::elect_one()) issue_s(t, it.jlo);
+            __syncwarp();
+          }
+        }
         if (!ok) break;
         commit_one(&bars->kv_empty[ks]);
         adv2(ks, kp);
         for (int j = it.jlo; ok && j < it.jhi; ++j) {
+          const bool more = j + 1 < it.jhi;
           ok = wait_warp(&bars->kv_full[vs], vp, abort);
+          if (ok && more) ok = wait_warp(&bars->kv_full[ks], kp, abort);
           if (!ok) break;
           const uint32_t va = v_lo + vs * (C::IB >> 4);
-          bool k_ready = false;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (ok && j >= it.ja[t] && j < it.jb[t]) {
-              // O_t += P_t V_j once the softmax has written P (and, for an item's first block, once the
-              // previous item's O_t has been read out)
+            // O_t += P_t V_j once the softmax has written P (and, for an item's first block, once the previous item's O_t
+            // has been read out), and right behind it S_t of the next block
+            const bool pv = j >= it.ja[t] && j < it.jb[t], sn = j + 1 >= it.ja[t] && j + 1 < it.jb[t];
+            if (ok && pv) {
               ok = wait_warp(&bars->p_full[t], pc[t] & 1u, abort);
               ++pc[t];
               if (ok && j == it.ja[t] && oc[t] > 0) ok = wait_warp(&bars->o_free[t], (oc[t] - 1u) & 1u, abort);
-              if (ok) {
-                tc05::fence_after_sync();
+            }
+            if (ok && sn && j + 1 == it.ja[t]) {
+              ok = wait_warp(&bars->q_full[t], qc[t] & 1u, abort);
+              ++qc[t];
+            }
+            if (!ok) break;
+            tc05::fence_after_sync();
+            if (tc05::elect_one()) {
+              if (pv) {
                 const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
                 const bool acc0 = j > it.ja[t];
-                if (tc05::elect_one()) {
 #pragma unroll
-                  for (int k = 0; k < kTKeys / 16; ++k)
-                    tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2048 >> 4), HI), idO, acc0 || k > 0);
-                  if (j + 1 == it.jb[t]) tc05::commit(&bars->pv_done[t]);
-                }
-                __syncwarp();
+                for (int k = 0; k < kTKeys / 16; ++k)
+                  tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2048 >> 4), HI), idO, acc0 || k > 0);
+                if (j + 1 == it.jb[t]) tc05::commit(&bars->pv_done[t]);
               }
+              if (t == 1) tc05::commit(&bars->kv_empty[vs]);
+              if (sn) issue_s(t, j + 1);
+              if (t == 1 && more) tc05::commit(&bars->kv_empty[ks]);
             }
-            if (ok && j + 1 >= it.ja[t] && j + 1 < it.jb[t]) {   // S_t of the next block, right behind
-              if (!k_ready) ok = wait_warp(&bars->kv_full[ks], kp, abort);
-              k_ready = true;
-              if (ok) issue_s(t, j + 1);
-            }
+            __syncwarp();
           }
           if (!ok) break;
-          commit_one(&bars->kv_empty[vs]);
           adv2(vs, vp);
-          if (j + 1 < it.jhi) {
-            commit_one(&bars->kv_empty[ks]);
-            adv2(ks, kp);
-          }
+          if (more) adv2(ks, kp);
         }
         if (!ok) break;
 #pragma unroll
