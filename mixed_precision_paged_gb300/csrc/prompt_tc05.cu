@@ -433,14 +433,14 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       for (int r = 0; next_item(bars, r, it, ok); ++r) {
         // S_t of block j from stage ks, by one lane: over the P_t before it (read by an O_t += P_t V issued earlier: one
         // thread's MMAs run in order)
-        auto issue_s = [&](int t, int j) {
-          const uint32_t qa = q_lo + t * (C::QB >> 4), ka = k_lo + ks * (C::IB >> 4);
+        auto issue_s = [&](int t, uint32_t ka, bool last) {
+          const uint32_t qa = q_lo + t * (C::QB >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             tc05::mma_ss(tbase + t * 256, tc05::sdesc_join(qa + (((k >> 2) * (kTRows * 128) + (k & 3) * 32) >> 4), HI),
                          tc05::sdesc_join(ka + (((k >> 2) * (kTKeys * 128) + (k & 3) * 32) >> 4), HI), idS, k > 0);
           tc05::commit(&bars->s_full[t]);
-          if (j + 1 == it.jb[t]) tc05::commit(&bars->q_empty[t]);
+          if (last) tc05::commit(&bars->q_empty[t]);
         };
         ok = wait_warp(&bars->kv_full[ks], kp, abort);
 #pragma unroll
@@ -449,7 +449,9 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
             ok = wait_warp(&bars->q_full[t], qc[t] & 1u, abort);
             ++qc[t];
             tc05::fence_after_sync();
-            if (ok && tc05::elect_one()) issue_s(t, it.jlo);
+            const uint32_t ka = k_lo + ks * (C::IB >> 4);
+            const bool last = it.jlo + 1 == it.jb[t];
+            if (ok && tc05::elect_one()) issue_s(t, ka, last);
             __syncwarp();
           }
         }
@@ -461,7 +463,8 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
           ok = wait_warp(&bars->kv_full[vs], vp, abort);
           if (ok && more) ok = wait_warp(&bars->kv_full[ks], kp, abort);
           if (!ok) break;
-          const uint32_t va = v_lo + vs * (C::IB >> 4);
+          const uint32_t va = v_lo + vs * (C::IB >> 4), ka = k_lo + ks * (C::IB >> 4);
+          uint64_t *const v_free = &bars->kv_empty[vs], *const k_free = &bars->kv_empty[ks];
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             // O_t += P_t V_j once the softmax has written P (and, for an item's first block, once the previous item's O_t
@@ -477,19 +480,19 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
               ++qc[t];
             }
             if (!ok) break;
+            const bool acc0 = j > it.ja[t], last_pv = j + 1 == it.jb[t], last_s = j + 2 == it.jb[t];
+            const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
             tc05::fence_after_sync();
             if (tc05::elect_one()) {
               if (pv) {
-                const uint32_t pa = tbase + t * 256, od = tbase + t * 256 + 128;
-                const bool acc0 = j > it.ja[t];
 #pragma unroll
                 for (int k = 0; k < kTKeys / 16; ++k)
                   tc05::mma_ts(od, pa + 8 * k, tc05::sdesc_join(va + k * (2048 >> 4), HI), idO, acc0 || k > 0);
-                if (j + 1 == it.jb[t]) tc05::commit(&bars->pv_done[t]);
+                if (last_pv) tc05::commit(&bars->pv_done[t]);
               }
-              if (t == 1) tc05::commit(&bars->kv_empty[vs]);
-              if (sn) issue_s(t, j + 1);
-              if (t == 1 && more) tc05::commit(&bars->kv_empty[ks]);
+              if (t == 1) tc05::commit(v_free);
+              if (sn) issue_s(t, ka, last_s);
+              if (t == 1 && more) tc05::commit(k_free);
             }
             __syncwarp();
           }
