@@ -188,30 +188,38 @@ __device__ __forceinline__ int dealt(int r) {
   return r * g + ((r & 1) ? g - 1 - c : c);
 }
 
-// The S row of one key block, read from tensor memory into registers once; MASK: keys outside lc + 1 .. lc + seen
-// become -inf. Returns the row's maximum (raw score).
+// The maximum of 32 scores.
+__device__ __forceinline__ float max32(const uint32_t (&a)[32]) {
+  float m8[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t* y = a + 8 * g;
+    m8[g] = fmaxf(max3(max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2])), __uint_as_float(y[3]),
+                       __uint_as_float(y[4])),
+                  max3(__uint_as_float(y[5]), __uint_as_float(y[6]), __uint_as_float(y[7])));
+  }
+  return max3(m8[0], m8[1], fmaxf(m8[2], m8[3]));
+}
+
+// The S row of one key block, read from tensor memory into registers once; MASK: columns outside lc + 1 .. hc become
+// -inf. Returns the row's maximum (raw score).
 template <bool MASK>
-__device__ __forceinline__ float prompt_row(uint32_t t_s, int lc, uint32_t seen, uint32_t (&a)[4][32]) {
+__device__ __forceinline__ float prompt_row(uint32_t t_s, int lc, int hc, uint32_t (&a)[4][32]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) tc05::ld32(t_s + 32 * c, a[c]);
   tc05::wait_ld();
   float mg[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    if (MASK) {
+    if (MASK) {                                            // a bit per column: 32 tests of one register
+      const int h = hc - 32 * c, l = lc - 32 * c;
+      const uint32_t upto = h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1u, below = l >= 31 ? ~0u : l < 0 ? 0u : (2u << l) - 1u;
+      const uint32_t seen = upto & ~below;
 #pragma unroll
       for (int e = 0; e < 32; ++e)
-        if ((uint32_t)(32 * c + e - lc - 1) >= seen) a[c][e] = __float_as_uint(-INFINITY);
+        if (!((seen >> e) & 1u)) a[c][e] = __float_as_uint(-INFINITY);
     }
-    float m8[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const uint32_t* y = a[c] + 8 * g;
-      m8[g] = fmaxf(max3(max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2])), __uint_as_float(y[3]),
-                         __uint_as_float(y[4])),
-                    max3(__uint_as_float(y[5]), __uint_as_float(y[6]), __uint_as_float(y[7])));
-    }
-    mg[c] = max3(m8[0], m8[1], fmaxf(m8[2], m8[3]));
+    mg[c] = max32(a[c]);
   }
   return max3(mg[0], mg[1], fmaxf(mg[2], mg[3]));
 }
@@ -538,8 +546,7 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         tc05::fence_after_sync();
         const int k0 = j * kTKeys;
         uint32_t sv[4][32];
-        float mx = k0 + kTKeys - 1 > q0 || k0 <= all_lo ? prompt_row<true>(t_s, lo - k0, (uint32_t)(pos - lo), sv)
-                                                        : prompt_row<false>(t_s, 0, 0u, sv);
+        float mx = k0 + kTKeys - 1 > q0 || k0 <= all_lo ? prompt_row<true>(t_s, lo - k0, pos - k0, sv) : prompt_row<false>(t_s, 0, 0, sv);
         mx = fmaf(mx, qs, -kHeadroom);
         const float m_new = fmaxf(m_ref, mx);
         const bool need = m_new > m_ref + 8.f;
@@ -574,7 +581,7 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
       const bool none = l == 0.f;                          // every score -inf (a NaN goes on to the output)
       const float inv = none ? 0.f : 1.f / l;
       const size_t orow = (size_t)(it.row0 + pos) * p.Hq + it.hg * p.heads + r % p.heads;
-#pragma unroll
+#pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         uint32_t o[32];
         tc05::ld32(t_o + 32 * x, o);
