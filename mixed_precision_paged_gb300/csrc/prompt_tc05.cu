@@ -437,8 +437,10 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         __syncwarp();
       };
       bool ok = true;
-      PromptItem it;
-      for (int r = 0; next_item(bars, r, it, ok); ++r) {
+      PromptItem it, after;
+      bool go = next_item(bars, 0, after, ok);
+      for (int r = 1; go; ++r) {
+        it = after;
         // S_t of block j from stage ks, by one lane: over the P_t before it (read by an O_t += P_t V issued earlier: one
         // thread's MMAs run in order)
         auto issue_s = [&](int t, uint32_t ka, bool last) {
@@ -466,6 +468,8 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         if (!ok) break;
         commit_one(&bars->kv_empty[ks]);
         adv2(ks, kp);
+        go = next_item(bars, r, after, ok);                // (there long before it is wanted)
+        if (!ok) break;
         for (int j = it.jlo; ok && j < it.jhi; ++j) {
           const bool more = j + 1 < it.jhi;
           ok = wait_warp(&bars->kv_full[vs], vp, abort);
@@ -529,10 +533,15 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
     const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     uint32_t sc = 0, pvc = 0;                              // phases taken: s_full, pv_done
     bool ok = true;
-    PromptItem it;
-    for (int ri = 0; next_item(bars, ri, it, ok); ++ri) {
+    PromptItem it, after;                                  // the next item is looked at while this one's last product runs
+    bool more = next_item(bars, 0, after, ok);
+    for (int ri = 1; more; ++ri) {
+      it = after;
       const int ja = t ? it.ja[1] : it.ja[0], jb = t ? it.jb[1] : it.jb[0], q0 = t ? it.q0[1] : it.q0[0];
-      if (ja >= jb) continue;
+      if (ja >= jb) {
+        more = next_item(bars, ri, after, ok);
+        continue;
+      }
       const int pos = q0 + tok_t;
       const int lo = max(pos - p.window, -1);              // the row sees keys lo + 1 .. pos
       const int all_lo = min(q0 + TT, it.L) - 1 - p.window;   // every row sees keys above this and up to q0
@@ -573,6 +582,8 @@ prompt_tc05_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
+      if (!ok) break;
+      more = next_item(bars, ri, after, ok);
       if (!ok) break;
       ok = wait_warp(&bars->pv_done[t], pvc & 1u, abort);
       ++pvc;
