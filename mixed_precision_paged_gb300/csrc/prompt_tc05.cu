@@ -13,14 +13,21 @@
 //     sorted by their number of query blocks (in shared memory, by every CTA for itself), and item x of the list is
 //     found by a search over the places where a prompt joins in. The list is dealt in a snake, which balances a sorted
 //     list about as well as a queue does, without one. Empty blocks of short prompts are not in it.
-//   * roles: warp 0 loads queries, keys and values (TMA); warp 1 issues the MMAs; warp 2 owns tensor memory; warp 3
+//   * roles: warp 0 loads queries, keys and values (TMA); warp 1 issues the MMAs; warp 2 owns tensor memory and posts the
+//     items' descriptions up to four ahead (looked up by every role for itself, an item cost each 1,000 cycles); warp 3
 //     zeroes the value rows past a prompt's end in its last block, so that weight 0 never meets what the next prompt
 //     (or nobody) wrote there; warps 4-7 and 8-11 are the softmax of tile 0 and 1, a thread per row.
 // Tensor memory of tile t: S and P at 256 t, O at 256 t + 128. The order of the MMAs and the lazily moved maximum are those
 // of the prefill (prefill_tc05.cu); the reference of a row lies 2^kHeadroom below its maximum, so that fp16 weights keep
 // their bits down to 2^-21 of the largest (extend_tc05.cuh). Every wait is bounded; a timeout is reported and
 // every role winds down.
-#include <stdlib.h>
+// What the steps towards this form gave (200 prompts of 1-300 tokens, 32/4 heads / 16 of 100-4,096, 32/8 heads, us): first
+// form 207 / 461; registers split between the roles, no spills 193 / 449; descriptions, queries behind the first keys and results
+// in whole 32-byte sectors 158 / 426; one elected region a step, descriptors outside it 158 / 418; masks tested bit by
+// bit of one register instead of by compares, a quarter of the epilogue's code 154 / 408; the next item looked at early
+// 147 / 408. Dropped: queries prefetched to L2 (166 / 432: TMA's rate, not DRAM, sets their 4,600 cycles), chunks of 32 keys
+// that no row sees left out (152 / 414: the branches cost the full blocks more), the same with fewer MMA steps (156 / 434),
+// items drawn from a counter (154 / 416).
 #include "extend_tc05.cuh"
 #include "prompt.cuh"
 
@@ -136,7 +143,10 @@ __device__ __forceinline__ int make_plan(const PromptParams& p, Plan& pl, int* r
     pl.first[k] = before - (k + 1) * blocks;
   }
   __syncthreads();
-  return total;
+  // prompts one behind the other have at most so many; lengths that go up and down may claim rows many times over
+  if (total <= p.total / step + p.n) return total;
+  if (blockIdx.x == 0 && tid == 0) report_error(p.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SEQ_LEN, -1);
+  return 0;
 }
 
 // Item w of the list (the whole warp).
@@ -662,7 +672,11 @@ cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_prompt_tc05(PromptParams p, int D, int num_sms, cudaStream_t st) {
-  p.heads = getenv("EKV_H1") ? 1 : p.G;
+  // Packed heads fill the tiles of short prompts and keep the masked edges of a window short; a long prompt's tiles are full
+  // either way, and with one head each the CTAs of a KV head read the same keys at about the same time. D 128, one head / packed:
+  // 8 x 8,192 tokens 2,947 / 3,180 us, 4 x 8,192 1,503 / 1,512, under a window of 2,048 770 / 756, 16 prompts of 100 to
+  // 4,096 426 / 408, 200 of 1 to 300 (G 8) 244 / 148. D 64: packed everywhere (4 x 8,192 541 / 535).
+  p.heads = D == 128 && p.window == 0x7fffffff && p.total >= 4096ll * p.n ? 1 : p.G;
   p.tile_tokens = kTRows / p.heads;
   return D == 128 ? launch_prompt<128>(p, num_sms, st) : launch_prompt<64>(p, num_sms, st);
 }
