@@ -130,8 +130,10 @@ def _ptr(x):
     """Device/host address of a tensor or array, an int address, or None -> NULL."""
     if x is None:
         return None
-    if hasattr(x, "data_ptr"):
+    try:                                                # (asking first costs as much again)
         return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
     if isinstance(x, np.ndarray):

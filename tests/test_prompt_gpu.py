@@ -235,6 +235,76 @@ def test_results_do_not_depend_on_the_batch(ekv_lib, torch_cuda):
     assert torch.equal(o[:700], out[:700]) and torch.equal(l[:700], lse[:700])
 
 
+def test_alignment_of_results_and_wide_strides(ekv_lib, torch_cuda):
+    """out on a 16-byte border that is none of 32; rows further apart than their heads, by different amounts."""
+    torch = torch_cuda
+    rng = np.random.default_rng(235)
+    lens = [130, 40]
+    cu, T = cu_of(lens), 170
+    x = rows_of(rng, T, 8, 2, 64)
+    wide = [torch.zeros((T, h * 64 + pad), device="cuda", dtype=torch.float16) for h, pad in ((8, 8), (2, 24), (2, 200))]
+    for y, z in zip(wide, np.split(x, [8, 10], 1)):
+        y[:, : z.shape[1] * 64] = torch.from_numpy(z.reshape(T, -1).copy()).cuda()
+    ctx = ekv_lib.Context(8, 2, 64, 2)
+    room = torch.full((T * 512 + 16,), float("nan"), device="cuda", dtype=torch.float16)
+    lse = torch.empty((T, 8), device="cuda")
+    for shift in (0, 8):
+        out = room[shift:shift + T * 512]
+        ekv_lib.ekv_prompt_attention(ctx.handle, *wide, *(y.stride(0) for y in wide), torch.from_numpy(cu).cuda(), 2, T, 0, 0.0, out, lse)
+        assert ctx.error() == (0, 0)
+        check(x[:, :8], x[:, 8:10], x[:, 10:], cu, out.view(T, 8, 64), lse)
+    ekv_lib.ekv_prompt_attention(ctx.handle, *wide, *(y.stride(0) for y in wide), torch.from_numpy(cu).cuda(), 2, T, 0, 0.0, out, None)
+    assert ctx.error() == (0, 0)
+
+
+@pytest.mark.parametrize("lens", [[5000, 4100], [8192]])
+def test_long_prompts(ekv_lib, torch_cuda, lens):
+    """Lengths from which on a tile takes one head: sampled rows against 64 bits."""
+    torch = torch_cuda
+    cu, T = cu_of(lens), sum(lens)
+    q, k, v = torch.randn((T, 12, 128), device="cuda", dtype=torch.float16).split((8, 2, 2), 1)
+    ctx = ekv_lib.Context(8, 2, 128, 2)
+    out, lse = attend(ekv_lib, ctx, q, k, v, torch.from_numpy(cu).cuda(), len(lens), T)
+    assert ctx.error() == (0, 0)
+    rng = np.random.default_rng(236)
+    for a, b in zip(cu, cu[1:]):
+        for r in sorted({0, 1, 127, 128, 255, 256, 4095, int(b - a) - 1} | {int(x) for x in rng.integers(0, b - a, 40)}):
+            for h in range(8):
+                s = (k[a:a + r + 1, h // 4].double() @ q[a + r, h].double()) / 128 ** 0.5
+                p = torch.softmax(s, 0)
+                ref, big = p @ v[a:a + r + 1, h // 4].double(), p @ v[a:a + r + 1, h // 4].double().abs()
+                # the result's rounding and the weights', and the scores' (see _extend.bounds)
+                assert ((out[a + r, h].double() - ref).abs() <= 2.0 ** -11 * ref.abs() + 2.0 ** -10.5 * big + 2.0 ** -24).all()
+                assert abs(lse[a + r, h].double() - torch.logsumexp(s, 0)) <= 1e-4
+
+
+def test_lengths_that_claim_rows_many_times_over_are_refused(ekv_lib, torch_cuda):
+    torch = torch_cuda
+    q, k, v = torch.randn((500, 8, 64), device="cuda", dtype=torch.float16).split((4, 2, 2), 1)
+    ctx = ekv_lib.Context(4, 2, 64, 400)
+    out, _ = attend(ekv_lib, ctx, q, k, v, torch.tensor([0, 500] * 200 + [0], dtype=torch.int32, device="cuda"), 400, 500)
+    assert ctx.error() == (ekv_lib.EKV_ERR_DEVICE_CHECK, ekv_lib.EKV_DETAIL_SEQ_LEN) and torch.isnan(out).all()
+
+
+def test_calls_on_two_streams_at_once(ekv_lib, torch_cuda):
+    """The call keeps nothing in its context but the error word."""
+    torch = torch_cuda
+    q, k, v = torch.randn((4000, 12, 128), device="cuda", dtype=torch.float16).split((8, 2, 2), 1)
+    ctx = ekv_lib.Context(8, 2, 128, 40)
+    cus = [torch.arange(0, 4001, 4000 // n, dtype=torch.int32, device="cuda") for n in (40, 5)]
+    alone = [attend(ekv_lib, ctx, q, k, v, c, len(c) - 1, 4000) for c in cus]
+    streams = [torch.cuda.Stream() for _ in cus]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, c in zip(streams, cus):
+            with torch.cuda.stream(s):
+                got.append(attend(ekv_lib, ctx, q, k, v, c, len(c) - 1, 4000))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[0], g[0]) and torch.equal(a[1], g[1]) for a, g in zip(alone, got))
+    assert ctx.error() == (0, 0)
+
+
 def test_bad_lengths_are_reported(ekv_lib, torch_cuda):
     torch = torch_cuda
     q, k, v = torch.randn((200, 8, 64), device="cuda", dtype=torch.float16).split((4, 2, 2), 1)
