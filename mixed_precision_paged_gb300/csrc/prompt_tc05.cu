@@ -9,10 +9,10 @@
 //     heads + head. heads = 1 takes 128 tokens of one head; heads = G fills a tile with short prompts.
 //   * items: two tiles that follow each other and share every key block of 128 tokens, one tile's softmax under the
 //     other's products. Persistent CTAs, one a SM.
-//   * plan: the items of all prompts, heaviest first. An item's weight goes by its query block, so the prompts are
-//     sorted by their number of query blocks (in shared memory, by every CTA for itself), and item x of the list is
-//     found by a search over the places where a prompt joins in. The list is dealt in a snake, which balances a sorted
-//     list about as well as a queue does, without one. Empty blocks of short prompts are not in it.
+//   * plan: the items of all prompts, heaviest first (short prompts in their order). An item's weight goes by its query block,
+//     so the prompts are sorted by their number of query blocks (in shared memory, by every CTA for itself), and item x of the
+//     list is found by a search over the places where a prompt joins in. The list is dealt in a snake, which balances a
+//     sorted list about as well as a queue does, without one. Empty blocks of short prompts are not in it.
 //   * roles: warp 0 loads queries, keys and values (TMA); warp 1 issues the MMAs; warp 2 owns tensor memory and posts the
 //     items' descriptions up to four ahead (looked up by every role for itself, an item cost each 1,000 cycles); warp 3
 //     zeroes the value rows past a prompt's end in its last block, so that weight 0 never meets what the next prompt
@@ -38,6 +38,7 @@ namespace {
 using namespace xt;
 
 constexpr int kPThreads = 384;
+constexpr int kInOrderTokens = 256;                    // longest prompt of a batch that keeps its order (see make_plan)
 
 template <int D>
 struct PT {
@@ -77,11 +78,13 @@ struct PromptBars {
   int abort;
 };
 
-// The plan, in shared memory: prompts by falling number of query blocks, (blocks << 12) | (4095 - prompt), and
-// first[k - 1], the place in the list of (prompt, query block) pairs from which on k prompts take part.
-struct Plan {
+// The plan, in shared memory: prompts as (query blocks << 12) | (4095 - prompt), and the places in the list of (prompt, query
+// block) pairs. Sorted by falling number of blocks: from first[k - 1] on k prompts take part, a block each in turn.
+// In the order of memory: prompt k's pairs begin at first[k].
+struct alignas(16) Plan {
   uint32_t key[kMaxBatch];
   int first[kMaxBatch];
+  int sorted;
 };
 
 template <int D>
@@ -89,11 +92,11 @@ constexpr int prompt_smem_bytes() {
   return 2 * PT<D>::QB + PT<D>::NS * PT<D>::IB + (int)sizeof(Plan) + (int)sizeof(PromptBars<PT<D>::NS>);
 }
 
-// Sorts the prompts and fills `first`; returns the number of (prompt, query block) pairs. All threads.
+// Fills the plan; returns the number of (prompt, query block) pairs. All threads.
 __device__ __forceinline__ int make_plan(const PromptParams& p, Plan& pl, int* red) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int step = 2 * p.tile_tokens;
-  int n2 = 1;
+  int n2 = 1, longest = 0;
   while (n2 < p.n) n2 <<= 1;
   for (int i = tid; i < n2; i += kPThreads) {
     uint32_t key = 0;
@@ -103,11 +106,15 @@ __device__ __forceinline__ int make_plan(const PromptParams& p, Plan& pl, int* r
       if (!good && blockIdx.x == 0) report_error(p.err, EKV_ERR_DEVICE_CHECK, EKV_DETAIL_SEQ_LEN, i);
       const int blocks = good ? (b - a + step - 1) / step : 0;
       key = ((uint32_t)blocks << 12) | (uint32_t)(kMaxBatch - 1 - i);
+      longest = max(longest, blocks);
     }
     pl.key[i] = key;
   }
-  __syncthreads();
-  for (int size = 2; size <= n2; size <<= 1)               // bitonic, falling
+  // Short prompts, all of about one weight, keep their order: the rows past a prompt's end that a tile loads are then the
+  // next one's, wanted at about the same time, and not read from memory twice. 32/4 heads, sorted / in order: 200 prompts of 200 to
+  // 256 tokens 209 / 188 us, 256 of 1 to 64 65.5 / 61.5; up to 512 tokens weights differ too much (16 of 1 to 512 37 / 41).
+  const bool sorted = __syncthreads_or(longest * step > kInOrderTokens);
+  for (int size = 2; sorted && size <= n2; size <<= 1)     // bitonic, falling
     for (int d = size >> 1; d > 0; d >>= 1) {
       for (int x = tid; x < n2 / 2; x += kPThreads) {
         const int i = ((x & ~(d - 1)) << 1) | (x & (d - 1)), j = i | d;
@@ -119,7 +126,7 @@ __device__ __forceinline__ int make_plan(const PromptParams& p, Plan& pl, int* r
       }
       __syncthreads();
     }
-  // first[k - 1] = (blocks of the k first prompts) - k * (blocks of the k-th)
+  // sorted: first[k - 1] = (blocks of the k first prompts) - k * (blocks of the k-th)
   const int each = (p.n + kPThreads - 1) / kPThreads, k0 = tid * each, k1 = min(k0 + each, p.n);
   int sum = 0;
   for (int k = k0; k < k1; ++k) sum += (int)(pl.key[k] >> 12);
@@ -139,9 +146,10 @@ __device__ __forceinline__ int make_plan(const PromptParams& p, Plan& pl, int* r
   before += incl - sum;
   for (int k = k0; k < k1; ++k) {
     const int blocks = (int)(pl.key[k] >> 12);
+    pl.first[k] = sorted ? before - k * blocks : before;
     before += blocks;
-    pl.first[k] = before - (k + 1) * blocks;
   }
+  if (tid == 0) pl.sorted = sorted;
   __syncthreads();
   // prompts one behind the other have at most so many; lengths that go up and down may claim rows many times over
   if (total <= p.total / step + p.n) return total;
@@ -163,9 +171,9 @@ __device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, const P
     lo += last * step;
     n = min(step, n - last * step);
   }
-  const int off = x - pl.first[lo];
-  const int qb = (int)(pl.key[lo] >> 12) - 1 - off / (lo + 1);
-  const int i = kMaxBatch - 1 - (int)(pl.key[off % (lo + 1)] & 4095u);
+  const int off = x - pl.first[lo], turn = pl.sorted ? lo + 1 : 1;   // prompts that take part here
+  const int qb = (int)(pl.key[lo] >> 12) - 1 - off / turn;
+  const int i = kMaxBatch - 1 - (int)(pl.key[pl.sorted ? off % turn : lo] & 4095u);
   it.row0 = __ldg(p.cu + i);
   it.L = __ldg(p.cu + i + 1) - it.row0;
 #pragma unroll
@@ -661,6 +669,7 @@ cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t st) {
     return cudaErrorInvalidValue;
   constexpr int smem = prompt_smem_bytes<D>();
   static_assert(smem <= 232448, "shared memory of one CTA");
+  static_assert(sizeof(Plan) % 16 == 0, "the barriers lie behind it");
   cudaError_t e = set_smem_attr(reinterpret_cast<const void*>(prompt_tc05_kernel<D>), smem);
   if (e != cudaSuccess) return e;
   // at most so many items: a CTA for each, and one a processor

@@ -74,7 +74,8 @@ def grow(v_new, v_pages, v_scales, page_mode, uniform_mode, block_table, seq_len
             if r0 == 0:
                 sc[page, h] = np.float32(max(a, 2.0 ** -24) / 448)
                 continue
-            top = float(np.float32(448.0 * float(sc[page, h])))
+            with np.errstate(over="ignore"):
+                top = float(np.float32(448.0 * float(sc[page, h])))
             k = 0
             while top * 2.0 ** k < a:
                 k += 1
