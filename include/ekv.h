@@ -393,7 +393,7 @@ typedef struct {
 /* Cosines and sines of the positions first .. first + rope_len - 1, as ekv_append_kv_rope and
  * ekv_append_kv_norm_rope read them:
  *   table[r][i] = magnitude * cos(2 pi w_i (first + r)),  table[r][rope_dim / 2 + i] = magnitude * sin(...).
- * Angles are reduced in 64 bits (to 2^-27 of a turn at the last position, 2^-40 at position 2^18), values rounded to
+ * Angles are reduced in 64 bits (frequencies are doubles: to about 2^-23 of a turn at the last position, 2^-36 at position 2^18), values rounded to
  * fp32 (a few units of its last place). A table for the writers begins at position 0; rows may be added in pieces.
  *  cfg          HOST struct, read before the call returns.
  *  table        fp32 [rope_len][rope_dim], 16-byte aligned (written).

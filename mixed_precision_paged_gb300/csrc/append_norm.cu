@@ -271,12 +271,9 @@ constexpr int kNormWarps = 8, kNormThreads = 32 * kNormWarps;
 constexpr int kNormStages = 4;                     // of a warp, at most
 constexpr int kNormSmem = 108 * 1024;              // two blocks a processor
 
-#ifndef GA_
-#define GA_ 1
-#endif
-#ifndef GB_
-#define GB_ 4
-#endif
+// Blocks of the growing scales: a quarter of the rows' blocks, for a quarter or less of the bytes (60,062 tokens, a half / a
+// third / a quarter / an eighth of them: 250 us each).
+constexpr int kGrowShare = 4;
 struct NormShape {
   int nst, stage;                                  // stages of a warp, bytes of one
   int parts, part_rows;                            // of a token, a warp each: so many head rows
@@ -492,7 +489,7 @@ cudaError_t launch_norm_append(const RopeAppendParams& p, int num_sms, cudaStrea
   sh.parts = (rows + sh.part_rows - 1) / sh.part_rows;
   if (sh.nst > kNormStages) sh.nst = kNormStages;
   // Two blocks a processor, and up to eight rounds of them where each warp still has eight tokens' parts: processors differ in
-  // speed (65,536 tokens, 1 / 2 / 4 / 6 / 8 rounds: 303 / 299 / 279 / 266 / 266 us; 16,000 tokens, 1 / 2 / 4: 70 / 76 / 82).
+  // speed (65,536 tokens, 1 / 2 / 4 / 6 / 8 rounds: 303 / 299 / 279 / 266 / 266 us; 18,285 tokens, 1 / 2 / 4: 70 / 76 / 82).
   const long long items = (long long)p.c.total_q * sh.parts, round = (long long)num_sms * 2;
   auto blocks_for = [&](long long n, long long each) {     // of n items, `each` at least a warp
     const long long most = round * 8, least = (n + kNormWarps - 1) / kNormWarps;
@@ -509,10 +506,11 @@ cudaError_t launch_norm_append(const RopeAppendParams& p, int num_sms, cudaStrea
     sh.chunk = (long long)p.c.total_q * p.c.Hkv <= 2 * warps ? 1 : kPage;
     const long long chunks = (p.c.total_q + sh.chunk - 1) / sh.chunk;
     sh.heads = 1;
-    while (sh.heads < p.c.Hkv && chunks * p.c.Hkv / (2 * sh.heads) >= GA_ * warps) sh.heads *= 2;
+    while (sh.heads < p.c.Hkv && chunks * p.c.Hkv / (2 * sh.heads) >= warps) sh.heads *= 2;
     const long long n = chunks * (p.c.Hkv / sh.heads);
     const long long least = (n + kNormWarps - 1) / kNormWarps;
-    sh.grow_blocks = (int)(least < sh.row_blocks / GB_ || least < round ? least : sh.row_blocks / GB_ > round ? sh.row_blocks / GB_ : round);
+    const long long share = sh.row_blocks / kGrowShare > round ? sh.row_blocks / kGrowShare : round;
+    sh.grow_blocks = (int)(least < share ? least : share);
   }
   if (p.c.D == 128) return p.grow ? launch<128, true>(p, sh, st) : launch<128, false>(p, sh, st);
   return p.grow ? launch<64, true>(p, sh, st) : launch<64, false>(p, sh, st);

@@ -3,7 +3,7 @@
 // Angle of pair i at position t: 2 pi t w_i, w_i the turns a position (include/ekv.h: the frequencies of
 // theta, divided where a context is stretched). Only the fraction of t w_i counts, and fp32 loses it: at
 // t = 10^6 an angle of 10^6 radians has a step of 1/16. Here w_i is a 64-bit fixed-point fraction of a turn, so that t w_i
-// wraps by itself: exact up to t 2^-65 turns, and the next row of a thread is one addition away. What
+// wraps by itself: off by at most t times w_i's error (a double's, and 2^-64), and the next row of a thread is one addition away. What
 // lies beyond the nearest quarter turn goes to fp32 with all its bits, and the quarter is put back by swaps and signs.
 // Writes 4 rope_dim bytes a position and reads nothing, so the floor is those bytes at HBM rate: 131,072 positions of 128
 // values 9.9 us. With sincospif and 64-bit conversions 31 us, with both replaced (below) 14.7: 35 instructions an angle, the
