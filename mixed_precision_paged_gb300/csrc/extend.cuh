@@ -78,10 +78,13 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t* cu, int batch, 
   return lo;
 }
 
-// The same by one lane, for rows first <= i < last of which every lane has its own: the guess of a batch of equal
-// lengths first (one round trip for a decode step), then the eight sequences beside it, then the rest.
+// The same by one lane, for rows first <= i < last, 0 <= i, of which every lane has its own: the guess of a batch of equal
+// lengths first (one round trip for a decode step), then the eight sequences beside it, then the rest. A first row below
+// zero counts as zero, so that the differences keep to 32 bits and the guess to the batch, whatever the array holds; its
+// sequence fails the caller's checks.
 __device__ __forceinline__ int lane_find_sequence(const int32_t* cu, int batch, int i, int first, int last) {
   int lo = 0, hi = batch;
+  first = max(first, 0);
   const int g = min(batch - 1, (int)((long long)(i - first) * batch / (last - first)));
   const int c0 = __ldg(cu + g), c1 = __ldg(cu + g + 1);
   if (c1 <= i) {
