@@ -130,7 +130,13 @@ def _ptr(x):
     """Device/host address of a tensor or array, an int address, or None -> NULL."""
     if x is None:
         return None
-    try:                                                # (asking first costs as much again)
+    # (by type first, 0.06 us for an address and 0.13 for a tensor; an exception would cost an address 0.45)
+    t = type(x)
+    if t is int:
+        return x
+    if t is np.ndarray:
+        return x.ctypes.data
+    try:
         return x.data_ptr()
     except AttributeError:
         pass
