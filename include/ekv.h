@@ -387,7 +387,7 @@ typedef struct {
   double factor;          /* >= 1; not looked at under PLAIN */
   double original_len;    /* > 0; BY_TURNS and BY_DIMS alone, like the next two */
   double slow, fast;      /* 0 < slow < fast */
-  double magnitude;       /* cosines and sines are multiplied by it (1: plain rotations) */
+  double magnitude;       /* cosines and sines are multiplied by it (1: plain rotations), rounded to fp32; finite there */
 } ekv_rope_config;
 
 /* Cosines and sines of the positions first .. first + rope_len - 1, as ekv_append_kv_rope and

@@ -731,7 +731,8 @@ ekv_status ekv_rope_table(ekv_ctx* c, const ekv_rope_config* cfg, float* table, 
                           void* stream) {
   if (!c || !cfg || first < 0 || rope_len < 0 || first > 0x7fffffff - rope_len) return EKV_ERR_INVALID_ARG;
   if (rope_dim < 16 || rope_dim > 2 * kMaxRopePairs || rope_dim % 16 != 0) return EKV_ERR_INVALID_ARG;
-  if (!(cfg->theta > 1.0) || !isfinite(cfg->theta) || !isfinite(cfg->magnitude)) return EKV_ERR_INVALID_ARG;
+  if (!(cfg->theta > 1.0) || !isfinite(cfg->theta)) return EKV_ERR_INVALID_ARG;
+  if (!isfinite((float)cfg->magnitude)) return EKV_ERR_INVALID_ARG;   // (the table is fp32)
   if (cfg->scaling < EKV_ROPE_PLAIN || cfg->scaling > EKV_ROPE_BY_DIMS) return EKV_ERR_INVALID_ARG;
   if (cfg->scaling != EKV_ROPE_PLAIN && (!(cfg->factor >= 1.0) || !isfinite(cfg->factor))) return EKV_ERR_INVALID_ARG;
   if (cfg->scaling >= EKV_ROPE_BY_TURNS &&
