@@ -420,8 +420,9 @@ ekv_status ekv_rope_table(ekv_ctx* ctx, const ekv_rope_config* cfg, float* table
  *               below the form's least. New codes are E4M3_rn_satfinite(fp32_rn(v / scale)) under the new scale.
  *               Pages of other forms are written as without it. No two sequences of a call may write the
  *               same page.
- * Where a sequence fails its checks nothing of it is written; where a page or scale fails, q_out and k_out are
- * written all the same. Everything else as for ekv_append_kv_rope. */
+ * Where a sequence fails its checks nothing of it is written. A position >= rope_len is its token's failure alone: nothing of
+ * that token is written, its values count for no scale, and the sequence's earlier tokens are written. Where a page or
+ * scale fails, q_out and k_out are written all the same. Everything else as for ekv_append_kv_rope. */
 ekv_status ekv_append_kv_norm_rope(ekv_ctx* ctx, const void* q, const void* k_new, const void* v_new,
                                    long long q_stride, long long k_stride, long long v_stride,
                                    const void* q_weight, const void* k_weight, float norm_eps,

@@ -22,7 +22,7 @@ def bits(x):
     return x.cpu().numpy().view(np.uint16)
 
 
-def run(ekv, torch, case, rope, hq, hkv, d, lens, cu, total, rows, grow):
+def run(ekv, torch, case, rope, hq, hkv, d, lens, cu, total, rows, grow, **kw):
     dev, x = to_device(case), torch.from_numpy(rows).cuda()
     qo, ko = (torch.full((total, h, d), 7.0, dtype=torch.float16, device="cuda") for h in (hq, hkv))
     w = torch.ones(d, dtype=torch.float16, device="cuda")
@@ -30,7 +30,7 @@ def run(ekv, torch, case, rope, hq, hkv, d, lens, cu, total, rows, grow):
     ctx = ekv.Context(hq, hkv, d, len(lens))
     write(ekv, ctx, dev, q, k, v, torch.from_numpy(rope).cuda(), rope.shape[1], 0, qo,
           torch.tensor(lens, dtype=torch.int32, device="cuda"), torch.tensor(cu, dtype=torch.int32, device="cuda"), len(lens), total,
-          q_weight=w, k_weight=w, k_out=ko, grow_scales=grow)
+          q_weight=w, k_weight=w, k_out=ko, grow_scales=grow, **kw)
     torch.cuda.synchronize()
     return ctx.error(), dev, qo, ko, w.cpu().numpy()
 
@@ -82,3 +82,27 @@ def test_arrays_of_anything_are_reported(ekv_lib, torch_cuda, grow):
             assert err == (ekv_lib.EKV_ERR_DEVICE_CHECK, ekv_lib.EKV_DETAIL_SEQ_LEN), (cu, lens)
         changed = np.any(bits(dev.k_pages) != case.k_pages.view(np.uint16), (1, 2, 3)).nonzero()[0]
         assert {int(p) for p in changed} <= used
+
+
+@pytest.mark.parametrize("grow", [0, 1])
+@pytest.mark.parametrize("rope_len", [1, 16, 33, 39, 40, 47])
+@pytest.mark.parametrize("hkv,d", [(2, 64), (8, 128)])
+def test_positions_behind_the_table(ekv_lib, torch_cuda, grow, rope_len, hkv, d):
+    """Tokens at such positions are reported and leave everything as it was; what stands before them is written as a call writes it
+    that does not have them. Their values are large: counted in, they would grow every scale."""
+    torch = torch_cuda
+    hq, lens, new = 2 * hkv, [40, 48, 3, 40, 64], [2, 48, 3, 25, 30]
+    cu = np.cumsum([0] + new)
+    case = make_case(np.array(lens), hq, hkv, d, "all", 1, 314, pool_pages=30)
+    at = np.concatenate([np.arange(n - m, n) for n, m in zip(lens, new)])
+    rows = np.random.default_rng(315).standard_normal((sum(new), hq + 2 * hkv, d)).astype(np.float16)
+    rows[at >= rope_len] *= 200
+    rope = rope_table(64, d)
+    err, dev, qo, ko, w = run(ekv_lib, torch, case, rope, hq, hkv, d, lens, cu.tolist(), len(rows), rows, grow, rope_len=rope_len)
+    assert err == (ekv_lib.EKV_ERR_DEVICE_CHECK, ekv_lib.EKV_DETAIL_SEQ_LEN)
+    good = torch.from_numpy(at < rope_len).cuda()
+    assert torch.all(qo[~good] == 7) and torch.all(ko[~good] == 7)
+    kept = [int(np.sum(at[a:b] < rope_len)) for a, b in zip(cu, cu[1:])]
+    r = rows[at < rope_len]
+    check_write(case, rope, 0, r[:, :hq], r[:, hq:hq + hkv], r[:, hq + hkv:], w, w, 1e-6,
+                np.array([n - m + k for n, m, k in zip(lens, new, kept)]), np.cumsum([0] + kept), grow, qo[good].cpu().numpy(), ko[good].cpu().numpy(), dev)
