@@ -450,6 +450,8 @@ ekv_status ekv_append_kv_norm_rope(ekv_ctx* ctx, const void* q, const void* k_ne
  *  total        HOST: rows of q, k, v and out, at most 2^24 (else EKV_ERR_UNSUPPORTED). Rows behind the last prompt are
  *               left as they are.
  *  window       keys a query sees, its own among them; 0: no window.
+ *  sm_scale     as for ekv_paged_decode. Finite scores sm_scale * q . K_k have to lie below 2^23 in magnitude: they and their
+ *               running maximum are fp32 in units of log 2, whose step is more than one from 2^24 on.
  *  out          fp16 [total][H_q][D], contiguous, 16-byte aligned; must not overlap q, k or v.
  *  lse          fp32 [total][H_q], natural logarithm, or NULL.
  * After EKV_DETAIL_TIMEOUT no row of the call's out and lse is to be used. Sums are fp32; the weights enter the
