@@ -7,6 +7,9 @@
 // stop while a warp computes (65,536 tokens of 32 + 2 x 8 heads of 128: 305 us, however rows and blocks are chosen). So they come
 // by bulk copies into a ring of a warp's own in shared memory, a token's part (its rows of q, k and v and its angles) a stage,
 // issued as many tokens ahead as there are stages. The sums and products are packed fp32 (two values an instruction).
+// A decode step is a chain of loads that wait for one another (sequence, lengths, page and mode, then the copies): 32 tokens 10.1 us on the device,
+// caches cold, on 8 blocks, where append_rope.cu, which loads its rows first and splits tokens finer, takes 8.6; 256 with
+// growing scales 13.6. With D 128 and growing scales 128 registers do not hold everything (100 bytes of spills stored, 60 loaded).
 #include "rope.cuh"
 
 namespace ekv {
@@ -271,8 +274,11 @@ constexpr int kNormWarps = 8, kNormThreads = 32 * kNormWarps;
 constexpr int kNormStages = 4;                     // of a warp, at most
 constexpr int kNormSmem = 108 * 1024;              // two blocks a processor
 
-// Blocks of the growing scales: a quarter of the rows' blocks, for a quarter or less of the bytes (60,062 tokens, a half / a
-// third / a quarter / an eighth of them: 250 us each).
+// Blocks of the growing scales, as far as there are items for them: a quarter of the rows' blocks, and one round (two a
+// processor) at least. Values are 12% of the call's bytes with 32/8 heads and packed keys, 27% with as many query heads as KV
+// heads, 43% without queries; the share hardly matters to any of them (all / a half / a quarter / an eighth of the rows'
+// blocks: 24 prompts of 700 to 4,000 tokens 242 / 242 / 244 / 242 us, with 8/8 heads 142 / 140 / 140 / 140, without queries
+// 103 / 102 / 103 / 102).
 constexpr int kGrowShare = 4;
 struct NormShape {
   int nst, stage;                                  // stages of a warp, bytes of one
